@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a4.so")
 
 SOURCES = ["api.cpp", "rotq.hip", "rotq_mfma.hip", "qgemm.hip", "qgemm_f6.hip", "lowrank.hip", "offq.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "block_api.cpp", "adapters.hip", "norm_residual.hip", "gated.hip"]
 
 # No fast-math and no denormal flushing: the quantizer's float32 division and
 # rounding must follow IEEE.  Packed-FP32 instructions are disabled.

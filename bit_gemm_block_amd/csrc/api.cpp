@@ -393,6 +393,8 @@ namespace w4a4 {
 
 int hip_status(hipError_t e) { return hip_fail(e); }
 
+int device_status() { return device_check(nullptr); }
+
 int qlinear_impl(const void* x, int x_dtype, const uint8_t* wq, int w_layout,
                          const void* w_scale, int w_scale_dtype, int64_t M, int64_t N, int64_t K,
                          int64_t had_block, int64_t w_group, const void* At, const void* Bt,

@@ -1,0 +1,73 @@
+// Internal launch interface of the operators beside the layer: block_api.cpp
+// validates, adapters.hip, norm_residual.hip and gated.hip run.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace w4a4 {
+
+// ---- low-rank adapters of many requests (adapters.hip) ----------------------
+struct AdapterArgs {
+  const void* x;  // [M, K], row distance ldx
+  int64_t ldx;
+  const void* At;  // [L, R, K]
+  const void* Bt;  // [L, N, R]
+  int L, R;
+  const int32_t* index;  // [M]
+  const int32_t* ranks;  // [L] or null
+  const float* scales;   // [L] or null
+  int64_t M, N;
+  int K;
+  const float* y;  // [M, N] or null
+  int64_t ldy;
+  float* out;
+  int64_t ldo;
+  float* t;     // [S, M, adapter_tstride(R)] float32 partial sums of x . A
+  int S;        // parts K is split into
+};
+
+// Parts that K is split into for M rows, and the row distance of t.
+int adapter_splits(int64_t M, int64_t K);
+__host__ __device__ inline int64_t adapter_tstride(int64_t R) { return (R + 31) / 32 * 32; }
+hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st);
+
+// ---- norms joined with gate and residual (norm_residual.hip) -----------------
+struct NormArgs {
+  const void* h;
+  int64_t ldh;
+  const void* y;
+  int64_t ldy;
+  const void* post_w;
+  const void* post_b;
+  const void* gate;
+  int64_t ldg, gate_rows;
+  const void* pre_w;
+  const void* pre_b;
+  void* h_out;
+  int64_t ldho;
+  void* x_out;
+  int64_t ldx;
+  int64_t M;
+  int C;
+  int post, pre;  // w4a4_norm
+  int gate_f16, x_f16;
+  float rs, offset, eps;
+};
+hipError_t launch_norm_residual(const NormArgs& a, bool h_f16, bool y_f16, bool p_f16,
+                                hipStream_t st);
+
+// ---- gated activation (gated.hip) ---------------------------------------------
+struct GatedArgs {
+  const void* gate;
+  int64_t ldg;
+  const void* up;  // or null
+  int64_t ldu;
+  void* out;
+  int64_t ldo;
+  int64_t M, F;
+};
+hipError_t launch_gated_activation(const GatedArgs& a, bool in_f16, bool out_f16, int act,
+                                   hipStream_t st);
+
+}  // namespace w4a4

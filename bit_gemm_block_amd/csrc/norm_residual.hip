@@ -1,0 +1,195 @@
+// norm_residual.hip — the seam between two blocks in one pass over a row:
+//   v = norm_post(y) * gate;  h' = h + rs v;  x = norm_pre(h').
+//
+// A row stays in the registers of one workgroup (T threads, 8 NC channels
+// each), so y and h are read once and h' and x written once; the statistics
+// are float32 sums over the row, the variance of a layer norm over the
+// centred values (a second sum over registers, not a second read).
+#include "block_internal.h"
+#include "vec_io.h"
+
+#include "w4a4_block.h"
+
+namespace w4a4 {
+namespace {
+
+// Sum over the WAVES * 64 threads of a workgroup.  Two slots in turn: a wave
+// reaches the write of slot s again only after the barrier of the other
+// slot's sum, which every wave passes after it has read slot s.
+template <int WAVES>
+struct RowSum {
+  float* lds;  // [2][WAVES]
+  int slot = 0;
+  __device__ __forceinline__ float operator()(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (WAVES > 1) {
+      float* s = lds + slot * WAVES;
+      slot ^= 1;
+      if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+      __syncthreads();
+      v = s[0];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v += s[w];
+    }
+    return v;
+  }
+};
+
+// One row per workgroup (WAVES > 1) or per wave (WAVES == 1, four rows per
+// workgroup).  VEC: every row starts on 16 bytes and C is a multiple of 8;
+// thread t's chunk i is channels 8 (i T + t) ...; otherwise element e of
+// chunk i is channel (8 i + e) T + t.
+template <int WAVES, int NC, bool VEC, typename H, typename Y, typename P>
+__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_kernel(NormArgs a) {
+  constexpr int T = WAVES * 64;
+  constexpr int E = 8 * NC;
+  __shared__ float lds[2 * WAVES];
+  RowSum<WAVES> row_sum{lds};
+  const int C = a.C;
+  const int t = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
+  const float inv_c = 1.f / static_cast<float>(C);
+  const int64_t row0 = WAVES == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (WAVES == 1 ? 4 : 1);
+
+  auto col = [&](int i, int e) { return VEC ? (i * T + t) * 8 + e : (i * 8 + e) * T + t; };
+  // out[] = elements of a row (zero past C).
+  auto load_row = [&](auto* p, float* out) {
+    using Q = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
+    if constexpr (VEC) {
+      Raw8<Q> r[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) r[i].load(p + (col(i, 0) < C ? col(i, 0) : 0));
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[8 * i + e] = col(i, 0) < C ? r[i].get(e) : 0.f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(j / 8, j % 8);
+        out[j] = c < C ? static_cast<float>(p[c]) : 0.f;
+      }
+    }
+  };
+  auto store_row = [&](auto* p, const float* v) {
+    using Q = std::remove_reference_t<decltype(*p)>;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (col(i, 0) < C) store8(p + col(i, 0), v + 8 * i);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(j / 8, j % 8);
+        if (c < C) p[c] = static_cast<Q>(v[j]);
+      }
+    }
+  };
+  auto norm = [&](float* v, int kind, const void* w, const void* b) {
+    if (kind == W4A4_NORM_LAYER) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) s += v[j];
+      const float mean = row_sum(s) * inv_c;
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] = col(j / 8, j % 8) < C ? v[j] - mean : 0.f;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) q = fmaf(v[j], v[j], q);
+    const float r = 1.f / sqrtf(row_sum(q) * inv_c + a.eps);
+    if (w) {
+      float p[E];
+      load_row(static_cast<const P*>(w), p);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= r * (a.offset + p[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= r;
+    }
+    if (b) {
+      float p[E];
+      load_row(static_cast<const P*>(b), p);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] += p[j];
+    }
+  };
+
+  for (int64_t m = row0; m < a.M; m += step) {
+    float v[E], h[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = h[j] = 0.f;
+    if (a.y) load_row(static_cast<const Y*>(a.y) + m * a.ldy, v);
+    if (a.h) load_row(static_cast<const H*>(a.h) + m * a.ldh, h);
+    if (a.post != W4A4_NORM_NONE) norm(v, a.post, a.post_w, a.post_b);
+    if (a.gate) {
+      float g[E];
+      const int64_t gr = m / a.gate_rows * a.ldg;
+      if (a.gate_f16)
+        load_row(static_cast<const _Float16*>(a.gate) + gr, g);
+      else
+        load_row(static_cast<const float*>(a.gate) + gr, g);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= g[j];
+    }
+    if (a.y) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) h[j] = fmaf(a.rs, v[j], h[j]);
+    }
+    if (a.h_out) store_row(static_cast<H*>(a.h_out) + m * a.ldho, h);
+    if (a.x_out) {
+      if (a.pre != W4A4_NORM_NONE) norm(h, a.pre, a.pre_w, a.pre_b);
+      if (a.x_f16)
+        store_row(static_cast<_Float16*>(a.x_out) + m * a.ldx, h);
+      else
+        store_row(static_cast<float*>(a.x_out) + m * a.ldx, h);
+    }
+  }
+}
+
+template <int WAVES, int NC, typename H, typename Y, typename P>
+void launch_shape(const NormArgs& a, bool vec, hipStream_t st) {
+  const int64_t groups = WAVES == 1 ? (a.M + 3) / 4 : a.M;
+  const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : (1 << 20)));
+  const dim3 block(WAVES == 1 ? 256 : WAVES * 64);
+  if (vec)
+    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, true, H, Y, P>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, false, H, Y, P>), grid, block, 0, st, a);
+}
+
+template <typename H, typename Y, typename P>
+void launch_types(const NormArgs& a, hipStream_t st) {
+  const bool vec = a.C % 8 == 0 && (!a.h || rows_aligned16(a.h, a.ldh, sizeof(H))) &&
+                   (!a.y || rows_aligned16(a.y, a.ldy, sizeof(Y))) &&
+                   (!a.gate || rows_aligned16(a.gate, a.ldg, a.gate_f16 ? 2 : 4)) &&
+                   (!a.h_out || rows_aligned16(a.h_out, a.ldho, sizeof(H))) &&
+                   (!a.x_out || rows_aligned16(a.x_out, a.ldx, a.x_f16 ? 2 : 4));
+  if (a.C <= 512) return launch_shape<1, 1, H, Y, P>(a, vec, st);
+  if (a.C <= 2048) return launch_shape<4, 1, H, Y, P>(a, vec, st);
+  if (a.C <= 4096) return launch_shape<4, 2, H, Y, P>(a, vec, st);
+  if (a.C <= 8192) return launch_shape<8, 2, H, Y, P>(a, vec, st);
+  return launch_shape<16, 2, H, Y, P>(a, vec, st);
+}
+
+}  // namespace
+
+hipError_t launch_norm_residual(const NormArgs& a, bool h_f16, bool y_f16, bool p_f16,
+                                hipStream_t st) {
+  typedef _Float16 F;
+  if (h_f16) {
+    if (y_f16)
+      p_f16 ? launch_types<F, F, F>(a, st) : launch_types<F, F, float>(a, st);
+    else
+      p_f16 ? launch_types<F, float, F>(a, st) : launch_types<F, float, float>(a, st);
+  } else {
+    if (y_f16)
+      p_f16 ? launch_types<float, F, F>(a, st) : launch_types<float, F, float>(a, st);
+    else
+      p_f16 ? launch_types<float, float, F>(a, st) : launch_types<float, float, float>(a, st);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace w4a4
