@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import List, Optional, Tuple
 
 import torch
@@ -28,6 +29,11 @@ _NORMS = {"none": 0, "rms": 1, "layer": 2}
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _DT = {torch.float32: _w.F32, torch.float16: _w.F16}
 
+# The raw handle of a device's current stream (torch's own accessor where there
+# is one: the Stream object costs another microsecond).
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                  lambda d: torch.cuda.current_stream(d).cuda_stream)
+
 _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _SIGS = {
     "w4a4_adapter_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
@@ -39,6 +45,11 @@ _SIGS = {
     "w4a4_gated_activation": (_INT, [_P, _I64, _P, _I64, _INT, _INT, _I64, _I64, _P, _I64, _INT,
                                      _P]),
 }
+# The same calls with their arguments packed in one buffer, which costs a
+# quarter of the host time of converting them one by one.
+_ADAPTER = struct.Struct("=20q")
+_NORM = struct.Struct("=13qd4q2d8q")
+_GATED = struct.Struct("=12q")
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -51,6 +62,9 @@ def lib() -> ctypes.CDLL:
             f = getattr(l, name)
             f.restype = res
             f.argtypes = args
+            if res is _INT:
+                f = getattr(l, name + "_packed")
+                f.restype, f.argtypes = _INT, [ctypes.c_char_p]
         _lib = l
     return _lib
 
@@ -68,42 +82,57 @@ def _dt(t: torch.Tensor) -> int:
     return d
 
 
-def _rows(t: torch.Tensor, name: str, device, M: int, C: int) -> int:
+def _device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("the tensors must be device tensors")
+    return t.get_device()
+
+
+def _rows(t: torch.Tensor, name: str, dev: int, M: int, C: int) -> int:
     """The row distance of a device matrix [M, C] with contiguous rows."""
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor, on the device of the others")
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != C:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the others")
+    if t.shape != (M, C):
         raise ValueError(f"{name} must be [{M}, {C}], not {list(t.shape)}")
     s0, s1 = t.stride()
-    if C > 1 and s1 != 1:
+    if s1 != 1 and C > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if M <= 1 or C == 0:
-        return max(s0, C)
-    if s0 < C:
+    if s0 >= C:
+        return s0
+    if M > 1 and C > 0:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return s0
+    return C
 
 
-def _whole(t: torch.Tensor, name: str, device, dtype, shape) -> int:
+def _whole(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
     """The address of a contiguous device tensor of this dtype and shape."""
-    if t.device != device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the others")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _call(fn: str, device, *args) -> None:
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, device, *args)
-    status = getattr(_lib or lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream)
+def _call(fn: str, packed: bytes) -> None:
+    status = getattr(_lib, fn)(packed)
     if status != _w.OK:
-        raise _w.W4A4Error(fn[5:], status)
+        raise _w.W4A4Error(fn[5:-7], status)
+
+
+def _launch(fn: str, dev: int, form: struct.Struct, *args) -> None:
+    """The packed call on dev's current stream."""
+    if _lib is None:
+        lib()
+    packed = form.pack(*args, _stream(dev))
+    if dev == torch.cuda.current_device():
+        _call(fn, packed)
+    else:
+        with torch.cuda.device(dev):
+            _call(fn, packed)
 
 
 # ---- low-rank adapters of many requests ---------------------------------------
@@ -128,30 +157,36 @@ def adapter_add(y: Optional[torch.Tensor], x: torch.Tensor, At: torch.Tensor, Bt
     Bt [adapters, N, rank] in fp16 or fp32; y (or None: zero) and out [M, N]
     float32, out may be y; index [M], ranks [adapters] (the columns in use)
     int32, scales [adapters] float32."""
-    dev = x.device
+    dev = _device(x)
     L, R, K = At.shape
     M = x.shape[0]
     N = Bt.shape[1]
+    dt = x.dtype
     ldx = _rows(x, "x", dev, M, K)
-    at = _whole(At, "At", dev, x.dtype, (L, R, K))
-    bt = _whole(Bt, "Bt", dev, x.dtype, (L, N, R))
+    at = _whole(At, "At", dev, dt, (L, R, K))
+    bt = _whole(Bt, "Bt", dev, dt, (L, N, R))
     ix = _whole(index, "index", dev, torch.int32, (M,))
-    rk = None if ranks is None else _whole(ranks, "ranks", dev, torch.int32, (L,))
-    sc = None if scales is None else _whole(scales, "scales", dev, torch.float32, (L,))
+    rk = 0 if ranks is None else _whole(ranks, "ranks", dev, torch.int32, (L,))
+    sc = 0 if scales is None else _whole(scales, "scales", dev, torch.float32, (L,))
+    yp, ldy = 0, N
+    if y is not None:
+        if y.dtype is not torch.float32:
+            raise TypeError(f"y must be float32, not {y.dtype}")
+        yp, ldy = y.data_ptr(), _rows(y, "y", dev, M, N)
+    ldo = N
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=dev)
-    for t, name in ((y, "y"), (out, "out")):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32, not {t.dtype}")
-    ldo = _rows(out, "out", dev, M, N)
-    ldy = N if y is None else _rows(y, "y", dev, M, N)
+        out = x.new_empty((M, N), dtype=torch.float32)
+    else:
+        if out.dtype is not torch.float32:
+            raise TypeError(f"out must be float32, not {out.dtype}")
+        ldo = _rows(out, "out", dev, M, N)
     if workspace is None:
-        workspace = adapter_workspace(M, K, R, dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = index.new_empty((adapter_workspace_size(M, K, R) + 3) // 4)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the device of the others")
-    _call("w4a4_adapter_add", dev, x.data_ptr(), _dt(x), ldx, at, bt, L, R, ix, rk, sc, M, N, K,
-          None if y is None else y.data_ptr(), ldy, out.data_ptr(), ldo, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _launch("w4a4_adapter_add_packed", dev, _ADAPTER, x.data_ptr(), _dt(x), ldx, at, bt, L, R, ix,
+            rk, sc, M, N, K, yp, ldy, out.data_ptr(), ldo, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out
 
 
@@ -176,44 +211,45 @@ def norm_residual(h: Optional[torch.Tensor], y: Optional[torch.Tensor] = None, *
     ref = h if h is not None else y
     if ref is None:
         raise ValueError("h or y must be given")
-    dev = ref.device
+    dev = _device(ref)
     M, C = ref.shape
-    if post_norm not in _NORMS or pre_norm not in _NORMS:
+    post, pre = _NORMS.get(post_norm), _NORMS.get(pre_norm)
+    if post is None or pre is None:
         raise ValueError('norms are "none", "rms" or "layer"')
-    ldh = C if h is None else _rows(h, "h", dev, M, C)
-    ldy = C if y is None else _rows(y, "y", dev, M, C)
-    pd = None
-    params = []
-    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
-                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        if t is None:
-            params.append(None)
-            continue
-        pd = t.dtype if pd is None else pd
-        params.append(_whole(t, name, dev, pd, (C,)))
-    gd, ldg, gp = _w.F32, C, None
+    hp, hd, ldh = 0, _dt(ref), C
+    if h is not None:
+        hp, ldh = h.data_ptr(), _rows(h, "h", dev, M, C)
+    yp, yd, ldy = 0, _w.F32, C
+    if y is not None:
+        yp, yd, ldy = y.data_ptr(), _dt(y), _rows(y, "y", dev, M, C)
+    one = next((t for t in (post_weight, post_bias, pre_weight, pre_bias) if t is not None), None)
+    pd, pdt = (_w.F32, None) if one is None else (_DT.get(one.dtype, -1), one.dtype)
+    pw = 0 if post_weight is None else _whole(post_weight, "post_weight", dev, pdt, (C,))
+    pb = 0 if post_bias is None else _whole(post_bias, "post_bias", dev, pdt, (C,))
+    qw = 0 if pre_weight is None else _whole(pre_weight, "pre_weight", dev, pdt, (C,))
+    qb = 0 if pre_bias is None else _whole(pre_bias, "pre_bias", dev, pdt, (C,))
+    gp, gd, ldg = 0, _w.F32, C
     if gate is not None:
         if gate_rows < 1:
             raise ValueError("gate_rows must be positive")
-        ldg = _rows(gate, "gate", dev, -(-M // gate_rows), C)
-        gd, gp = _dt(gate), gate.data_ptr()
-    if h_out is None and (want_h if want_h is not None else y is not None):
-        h_out = torch.empty((M, C), dtype=ref.dtype, device=dev)
-    if h_out is not None and h_out.dtype != ref.dtype:
-        raise TypeError("h_out must have h's dtype (y's without h)")
-    if x_out is None and x_dtype is not None:
-        x_out = torch.empty((M, C), dtype=x_dtype, device=dev)
-    _call("w4a4_norm_residual", dev,
-          None if h is None else h.data_ptr(), _dt(ref), ldh,
-          None if y is None else y.data_ptr(), _w.F32 if y is None else _dt(y), ldy,
-          _NORMS[post_norm], params[0], params[1], gp, gd, ldg, gate_rows, residual_scale,
-          _NORMS[pre_norm], params[2], params[3], _w.F32 if pd is None else _DT.get(pd, -1),
-          weight_offset, eps, M, C,
-          None if h_out is None else h_out.data_ptr(),
-          C if h_out is None else _rows(h_out, "h_out", dev, M, C),
-          None if x_out is None else x_out.data_ptr(),
-          _w.F32 if x_out is None else _dt(x_out),
-          C if x_out is None else _rows(x_out, "x_out", dev, M, C))
+        gp, gd, ldg = gate.data_ptr(), _dt(gate), _rows(gate, "gate", dev, -(-M // gate_rows), C)
+    op, ldho = 0, C
+    if h_out is not None:
+        if h_out.dtype is not ref.dtype:
+            raise TypeError("h_out must have h's dtype (y's without h)")
+        op, ldho = h_out.data_ptr(), _rows(h_out, "h_out", dev, M, C)
+    elif want_h or (want_h is None and y is not None):
+        h_out = ref.new_empty((M, C))
+        op = h_out.data_ptr()
+    xp, xd, ldx = 0, _w.F32, C
+    if x_out is not None:
+        xp, xd, ldx = x_out.data_ptr(), _dt(x_out), _rows(x_out, "x_out", dev, M, C)
+    elif x_dtype is not None:
+        x_out = ref.new_empty((M, C), dtype=x_dtype)
+        xp, xd = x_out.data_ptr(), _dt(x_out)
+    _launch("w4a4_norm_residual_packed", dev, _NORM, hp, hd, ldh, yp, yd, ldy, post, pw, pb, gp, gd,
+            ldg, gate_rows, residual_scale, pre, qw, qb, pd, weight_offset, eps, M, C, op, ldho, xp,
+            xd, ldx)
     return h_out, x_out
 
 
@@ -227,17 +263,19 @@ def gated_activation(gate: torch.Tensor, up: Optional[torch.Tensor], act: str = 
     a = _ACTS.get(act)
     if a is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    dev = gate.device
+    dev = _device(gate)
     M, F = gate.shape
     ldg = _rows(gate, "gate", dev, M, F)
-    ldu = F
+    up_ptr, ldu = 0, F
     if up is not None:
-        ldu = _rows(up, "up", dev, M, F)
-        if up.dtype != gate.dtype:
+        up_ptr, ldu = up.data_ptr(), _rows(up, "up", dev, M, F)
+        if up.dtype is not gate.dtype:
             raise TypeError("gate and up must have one dtype")
+    ldo = F
     if out is None:
-        out = torch.empty((M, F), dtype=out_dtype, device=dev)
-    _call("w4a4_gated_activation", dev, gate.data_ptr(), ldg,
-          None if up is None else up.data_ptr(), ldu, _dt(gate), a, M, F, out.data_ptr(),
-          _rows(out, "out", dev, M, F), _dt(out))
+        out = gate.new_empty((M, F), dtype=out_dtype)
+    else:
+        ldo = _rows(out, "out", dev, M, F)
+    _launch("w4a4_gated_activation_packed", dev, _GATED, gate.data_ptr(), ldg, up_ptr, ldu,
+            _dt(gate), a, M, F, out.data_ptr(), ldo, _dt(out))
     return out

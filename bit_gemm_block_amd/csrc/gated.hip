@@ -61,38 +61,23 @@ __device__ __forceinline__ float gated(float g, float u) {
 }
 
 // One row (or the whole matrix as one row) per grid.y step, 8 * 256
-// consecutive elements per workgroup.  VEC: rows start on 16 bytes.
-template <typename I, typename O, int ACT, bool UP, bool VEC>
+// consecutive elements per workgroup.
+template <typename I, typename O, int ACT, bool UP>
 __global__ void __launch_bounds__(256) gated_kernel(GatedArgs a) {
   for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
     const I* gr = static_cast<const I*>(a.gate) + m * a.ldg;
     const I* ur = UP ? static_cast<const I*>(a.up) + m * a.ldu : nullptr;
     O* orow = static_cast<O*>(a.out) + m * a.ldo;
     for (int64_t c = blockIdx.x; c * 2048 < a.F; c += gridDim.x) {
-      if (VEC) {
-        const int64_t f = c * 2048 + 8 * threadIdx.x;
-        if (f + 8 <= a.F) {
-          Raw8<I> g, u;
-          g.load(gr + f);
-          if (UP) u.load(ur + f);
-          float v[8];
+      const int64_t f = c * 2048 + 8 * threadIdx.x;
+      if (f >= a.F) continue;
+      const Raw8<I> g = load8_once(gr, f, a.F);
+      Raw8<I> u{};
+      if (UP) u = load8_once(ur, f, a.F);
+      float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = gated<ACT, UP>(g.get(e), UP ? u.get(e) : 1.f);
-          store8(orow + f, v);
-        } else {
-          for (int64_t i = f; i < a.F; ++i)
-            orow[i] = static_cast<O>(
-                gated<ACT, UP>(static_cast<float>(gr[i]), UP ? static_cast<float>(ur[i]) : 1.f));
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t f = c * 2048 + 256 * e + threadIdx.x;
-          if (f < a.F)
-            orow[f] = static_cast<O>(
-                gated<ACT, UP>(static_cast<float>(gr[f]), UP ? static_cast<float>(ur[f]) : 1.f));
-        }
-      }
+      for (int e = 0; e < 8; ++e) v[e] = gated<ACT, UP>(g.get(e), UP ? u.get(e) : 1.f);
+      store8(orow, f, a.F, v);
     }
   }
 }
@@ -102,20 +87,10 @@ void launch_act(const GatedArgs& a, hipStream_t st) {
   const int64_t chunks = (a.F + 2047) / 2048;
   const dim3 grid(static_cast<unsigned>(chunks < (1 << 20) ? chunks : (1 << 20)),
                   static_cast<unsigned>(a.M < 32768 ? a.M : 32768));
-  const bool vec = rows_aligned16(a.gate, a.ldg, sizeof(I)) &&
-                   (!a.up || rows_aligned16(a.up, a.ldu, sizeof(I))) &&
-                   rows_aligned16(a.out, a.ldo, sizeof(O));
-  if (a.up) {
-    if (vec)
-      hipLaunchKernelGGL((gated_kernel<I, O, ACT, true, true>), grid, dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((gated_kernel<I, O, ACT, true, false>), grid, dim3(256), 0, st, a);
-  } else {
-    if (vec)
-      hipLaunchKernelGGL((gated_kernel<I, O, ACT, false, true>), grid, dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((gated_kernel<I, O, ACT, false, false>), grid, dim3(256), 0, st, a);
-  }
+  if (a.up)
+    hipLaunchKernelGGL((gated_kernel<I, O, ACT, true>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((gated_kernel<I, O, ACT, false>), grid, dim3(256), 0, st, a);
 }
 
 template <typename I, typename O>

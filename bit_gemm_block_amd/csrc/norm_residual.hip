@@ -36,11 +36,18 @@ struct RowSum {
   }
 };
 
+// How a thread's chunk of eight channels from c = 8 (i T + t) meets the row's
+// end.  EVEN (C % 8 == 0): a chunk is in the row or past it.  SHIFTED (C >= 8):
+// the chunk that crosses the end moves back to the row's last eight channels
+// and does not own those that its neighbour has as well, so that every load is
+// one whole, unconditional one (a branch around the last elements' own loads
+// cost more than the kernel's whole work: 777 x 5003, 29.7 -> 19 us).  SHORT
+// (C < 8): elements one by one.
+enum Ends { EVEN = 0, SHIFTED = 1, SHORT = 2 };
+
 // One row per workgroup (WAVES > 1) or per wave (WAVES == 1, four rows per
-// workgroup).  VEC: every row starts on 16 bytes and C is a multiple of 8;
-// thread t's chunk i is channels 8 (i T + t) ...; otherwise element e of
-// chunk i is channel (8 i + e) T + t.
-template <int WAVES, int NC, bool VEC, typename H, typename Y, typename P>
+// workgroup), NC chunks per thread.
+template <int WAVES, int NC, int ENDS, typename H, typename Y, typename P>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_kernel(NormArgs a) {
   constexpr int T = WAVES * 64;
   constexpr int E = 8 * NC;
@@ -52,37 +59,54 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_k
   const int64_t row0 = WAVES == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (WAVES == 1 ? 4 : 1);
 
-  auto col = [&](int i, int e) { return VEC ? (i * T + t) * 8 + e : (i * 8 + e) * T + t; };
-  // out[] = elements of a row (zero past C).
+  // Chunk i starts at col[i] and owns its elements from skip[i] on.
+  int col[NC], skip[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * T + t) * 8;
+    if constexpr (ENDS == EVEN) {
+      col[i] = c < C ? c : 0;
+      skip[i] = c < C ? 0 : 8;
+    } else if constexpr (ENDS == SHIFTED) {
+      col[i] = c + 8 <= C ? c : C - 8;
+      skip[i] = c - col[i];
+    } else {
+      col[i] = c;
+      skip[i] = 0;
+    }
+  }
+  auto owned = [&](int j) {
+    const int i = j / 8, e = j % 8;
+    return ENDS == EVEN ? skip[i] == 0 : ENDS == SHIFTED ? e >= skip[i] : col[i] + e < C;
+  };
+  // Elements of a row; those that the thread does not own may be anything.
   auto load_row = [&](auto* p, float* out) {
     using Q = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
-    if constexpr (VEC) {
-      Raw8<Q> r[NC];
+    Raw8<Q> r[NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) r[i].load(p + (col(i, 0) < C ? col(i, 0) : 0));
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) out[8 * i + e] = col(i, 0) < C ? r[i].get(e) : 0.f;
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = col(j / 8, j % 8);
-        out[j] = c < C ? static_cast<float>(p[c]) : 0.f;
-      }
+    for (int i = 0; i < NC; ++i) {
+      if constexpr (ENDS == SHORT)
+        r[i] = load8_once(p, col[i], C);
+      else
+        r[i].load(p + col[i]);
     }
+#pragma unroll
+    for (int j = 0; j < E; ++j) out[j] = r[j / 8].get(j % 8);
   };
   auto store_row = [&](auto* p, const float* v) {
     using Q = std::remove_reference_t<decltype(*p)>;
-    if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (col(i, 0) < C) store8(p + col(i, 0), v + 8 * i);
-    } else {
+    for (int i = 0; i < NC; ++i) {
+      if constexpr (ENDS == SHORT) {
+        store8(p, col[i], C, v + 8 * i);
+      } else {
+        if (skip[i] == 0) {
+          store_whole8(p + col[i], v + 8 * i);
+        } else if (ENDS == SHIFTED && skip[i] < 8) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = col(j / 8, j % 8);
-        if (c < C) p[c] = static_cast<Q>(v[j]);
+          for (int e = 1; e < 8; ++e)
+            if (e >= skip[i]) p[col[i] + e] = static_cast<Q>(v[8 * i + e]);
+        }
       }
     }
   };
@@ -93,7 +117,7 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_k
       for (int j = 0; j < E; ++j) s += v[j];
       const float mean = row_sum(s) * inv_c;
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[j] = col(j / 8, j % 8) < C ? v[j] - mean : 0.f;
+      for (int j = 0; j < E; ++j) v[j] = owned(j) ? v[j] - mean : 0.f;
     }
     float q = 0.f;
 #pragma unroll
@@ -122,6 +146,8 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_k
     for (int j = 0; j < E; ++j) v[j] = h[j] = 0.f;
     if (a.y) load_row(static_cast<const Y*>(a.y) + m * a.ldy, v);
     if (a.h) load_row(static_cast<const H*>(a.h) + m * a.ldh, h);
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = owned(j) ? v[j] : 0.f;
     if (a.post != W4A4_NORM_NONE) norm(v, a.post, a.post_w, a.post_b);
     if (a.gate) {
       float g[E];
@@ -137,6 +163,8 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_k
 #pragma unroll
       for (int j = 0; j < E; ++j) h[j] = fmaf(a.rs, v[j], h[j]);
     }
+#pragma unroll
+    for (int j = 0; j < E; ++j) h[j] = owned(j) ? h[j] : 0.f;
     if (a.h_out) store_row(static_cast<H*>(a.h_out) + m * a.ldho, h);
     if (a.x_out) {
       if (a.pre != W4A4_NORM_NONE) norm(h, a.pre, a.pre_w, a.pre_b);
@@ -149,28 +177,29 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) norm_residual_k
 }
 
 template <int WAVES, int NC, typename H, typename Y, typename P>
-void launch_shape(const NormArgs& a, bool vec, hipStream_t st) {
+void launch_shape(const NormArgs& a, hipStream_t st) {
   const int64_t groups = WAVES == 1 ? (a.M + 3) / 4 : a.M;
   const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : (1 << 20)));
   const dim3 block(WAVES == 1 ? 256 : WAVES * 64);
-  if (vec)
-    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, true, H, Y, P>), grid, block, 0, st, a);
+  if constexpr (WAVES == 1) {
+    if (a.C < 8) {
+      hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, SHORT, H, Y, P>), grid, block, 0, st, a);
+      return;
+    }
+  }
+  if (a.C % 8)
+    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, SHIFTED, H, Y, P>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, false, H, Y, P>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, EVEN, H, Y, P>), grid, block, 0, st, a);
 }
 
 template <typename H, typename Y, typename P>
 void launch_types(const NormArgs& a, hipStream_t st) {
-  const bool vec = a.C % 8 == 0 && (!a.h || rows_aligned16(a.h, a.ldh, sizeof(H))) &&
-                   (!a.y || rows_aligned16(a.y, a.ldy, sizeof(Y))) &&
-                   (!a.gate || rows_aligned16(a.gate, a.ldg, a.gate_f16 ? 2 : 4)) &&
-                   (!a.h_out || rows_aligned16(a.h_out, a.ldho, sizeof(H))) &&
-                   (!a.x_out || rows_aligned16(a.x_out, a.ldx, a.x_f16 ? 2 : 4));
-  if (a.C <= 512) return launch_shape<1, 1, H, Y, P>(a, vec, st);
-  if (a.C <= 2048) return launch_shape<4, 1, H, Y, P>(a, vec, st);
-  if (a.C <= 4096) return launch_shape<4, 2, H, Y, P>(a, vec, st);
-  if (a.C <= 8192) return launch_shape<8, 2, H, Y, P>(a, vec, st);
-  return launch_shape<16, 2, H, Y, P>(a, vec, st);
+  if (a.C <= 512) return launch_shape<1, 1, H, Y, P>(a, st);
+  if (a.C <= 2048) return launch_shape<4, 1, H, Y, P>(a, st);
+  if (a.C <= 4096) return launch_shape<4, 2, H, Y, P>(a, st);
+  if (a.C <= 8192) return launch_shape<8, 2, H, Y, P>(a, st);
+  return launch_shape<16, 2, H, Y, P>(a, st);
 }
 
 }  // namespace
