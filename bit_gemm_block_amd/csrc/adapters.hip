@@ -17,6 +17,8 @@
 namespace w4a4 {
 namespace {
 
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+
 // A lane's 16-byte piece of a matrix operand: lane 16 g + r holds row r,
 // channels [FL g, FL g + FL) of a chunk of KC = 4 FL channels.
 template <typename T>
@@ -42,74 +44,108 @@ struct Frag<float> {
   }
 };
 
-// Row tiles from which the staged kernel takes over.
-constexpr int64_t kStageTiles = 64;
+constexpr int64_t kManyRows = 128;
+// Whether a call is taken as one of prompts: x . A staged, all adapters of a
+// tile in one workgroup.
+__host__ __device__ inline bool adapter_many(int64_t M, int64_t R) { return M >= kManyRows && R <= 128; }
+// Parts that K is split into, where it is.
+constexpr int kParts = 4;
+// Workgroups up to which a tile's adapters are shared out among several of them
+// (tiles of one adapter leave the others with nothing to do).
+constexpr unsigned kShareStages = 1024;
+constexpr int64_t kShareWorkgroups = 2048;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The first row of a workgroup's tile.  Consecutive workgroups go to the eight
+// XCDs in turn.  With many tiles (grid.x then a multiple of eight) each XCD
+// takes a contiguous eighth of them, so that its L2 holds the factors of the few
+// requests there; the grid's padding falls past the last row.
+__device__ __forceinline__ int64_t tile_row(const AdapterArgs& a) {
+  int64_t tile = blockIdx.x;
+  if (adapter_many(a.M, a.R)) tile = (tile & 7) * (gridDim.x >> 3) + (tile >> 3);
+  return tile * 16;
+}
 
 // The adapter of row m0 + (lane & 15), -1 where there is none.
 __device__ __forceinline__ int row_adapter(const AdapterArgs& a, int64_t m0, int lane) {
   const int64_t m = m0 + (lane & 15);
-  if (m >= a.M) return -1;
-  const int v = a.index[m];
-  return v >= 0 && v < a.L ? v : -1;
+  const int v = a.index[m < a.M ? m : a.M - 1];
+  return m < a.M && v >= 0 && v < a.L ? v : -1;
 }
-__device__ __forceinline__ int rank_of(const AdapterArgs& a, int ad) {
-  if (!a.ranks) return a.R;
-  const int r = uniform(a.ranks[ad]);
-  return r < 0 ? 0 : r > a.R ? a.R : r;
-}
+
+// The adapters' ranks.  Up to 64 adapters: lane l holds l's, loaded beside the
+// rows' adapters rather than after them.
+struct Ranks {
+  int of_lane;
+  __device__ __forceinline__ Ranks(const AdapterArgs& a, int lane) {
+    of_lane = a.ranks && a.L <= 64 && a.L > 0 ? a.ranks[lane < a.L ? lane : a.L - 1] : a.R;
+  }
+  // Of a wave-uniform adapter.
+  __device__ __forceinline__ int operator()(const AdapterArgs& a, int ad) const {
+    const int r = a.ranks && a.L > 64 ? uniform(a.ranks[ad]) : __builtin_amdgcn_readlane(of_lane, ad);
+    return r < 0 ? 0 : r > a.R ? a.R : r;
+  }
+};
 
 // ---- t = x . At^T: one 16 x 16 block per workgroup -----------------------------
 // Workgroup (tile, part of K and block of 16 ranks, slot): slot s (or every
 // slot in turn, where grid.z is 1) runs the adapter led by row s of the tile.
 // The waves share the part of K; their sums are joined in LDS in order.  All
-// loads are whole and unconditional, PF chunks of them in flight: ranks past
-// the adapter's read its last one, rows of other adapters the leading row
-// (both fall on lines that are read anyway; neither's result is stored).
-constexpr int kBlockWaves = 8;
+// loads are whole and unconditional, up to eight chunks of them in flight: ranks
+// past the adapter's read its last one, rows of other adapters the leading row
+// (both fall on lines that are read anyway; neither enters a stored result).
+constexpr int kBlockWaves = 16;
 
 template <typename T>
 __global__ void __launch_bounds__(64 * kBlockWaves) shrink_block_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
-  constexpr int PF = 4;
   __shared__ f32x4 red[kBlockWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t m0 = tile_row(a);
+  if (m0 >= a.M) return;
   const int split = blockIdx.y % a.S, rb = blockIdx.y / a.S;
   const int k0 = a.K / 64 * split / a.S * 64, k1 = a.K / 64 * (split + 1) / a.S * 64;
   const int chunks = (k1 - k0) / F::KC;
   const int c0 = chunks * wave / kBlockWaves, c1 = chunks * (wave + 1) / kBlockWaves;
   const int my = row_adapter(a, m0, lane);
+  const Ranks ranks(a, lane);
   for (int s = blockIdx.z; s < 16; s += gridDim.z) {
     const int ad = __builtin_amdgcn_readlane(my, s);
     if (ad < 0) continue;
     const bool mine = my == ad;
     if (static_cast<int>(__builtin_ctzll(__ballot(mine))) != s) continue;  // led by another row
-    const int rank = rank_of(a, ad);
+    const int rank = ranks(a, ad);
     if (16 * rb >= rank) continue;
     const int j = 16 * rb + r < rank ? 16 * rb + r : rank - 1;
     const int64_t m = m0 + (mine ? r : s);
     const T* xr = static_cast<const T*>(a.x) + m * a.ldx + k0 + g * F::FL;
     const T* ar = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K + k0 + g * F::FL;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int ch = c0;
-    for (; ch + PF <= c1; ch += PF) {
-      V xv[PF], av[PF];
+    auto batch = [&](int ch, auto n) {
+      V xv[n.value], av[n.value];
 #pragma unroll
-      for (int u = 0; u < PF; ++u) {
+      for (int u = 0; u < n.value; ++u) {
         av[u] = *reinterpret_cast<const V*>(ar + (ch + u) * F::KC);
         xv[u] = *reinterpret_cast<const V*>(xr + (ch + u) * F::KC);
       }
 #pragma unroll
-      for (int u = 0; u < PF; ++u) acc = F::mma(av[u], xv[u], acc);
+      for (int u = 0; u < n.value; ++u) acc = F::mma(av[u], xv[u], acc);
+    };
+    int ch = c0;
+    for (; ch + 8 <= c1; ch += 8) batch(ch, std::integral_constant<int, 8>());
+    if (ch + 4 <= c1) {
+      batch(ch, std::integral_constant<int, 4>());
+      ch += 4;
     }
-    for (; ch < c1; ++ch)
-      acc = F::mma(*reinterpret_cast<const V*>(ar + ch * F::KC),
-                   *reinterpret_cast<const V*>(xr + ch * F::KC), acc);
+    if (ch + 2 <= c1) {
+      batch(ch, std::integral_constant<int, 2>());
+      ch += 2;
+    }
+    if (ch < c1) batch(ch, std::integral_constant<int, 1>());
     red[wave][lane] = acc;
     __syncthreads();
     if (wave == 0) {
@@ -127,7 +163,7 @@ __global__ void __launch_bounds__(64 * kBlockWaves) shrink_block_kernel(AdapterA
 
 // ---- t = x . At^T: many rows, one adapter for most tiles ------------------------
 // A workgroup owns 16 rows and all (up to 16 NT) ranks of an adapter in them,
-// and streams a part of K through LDS: stage s holds RUN bytes of each of the
+// and streams K through LDS: stage s holds RUN bytes of each of the
 // 16 rows of x and the 16 NT rows of At, every row one contiguous run that
 // direct-to-LDS copies bring in (register loads of the matrix operands read 16
 // rows x 64 bytes per instruction, which the caches serve at a fraction of the
@@ -153,12 +189,12 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int split = blockIdx.y;
-  const int k0 = a.K / 64 * split / a.S * 64, k1 = a.K / 64 * (split + 1) / a.S * 64;
-  const int bytes = (k1 - k0) * static_cast<int>(sizeof(T));
+  const int64_t m0 = tile_row(a);
+  if (m0 >= a.M) return;
+  const int bytes = a.K * static_cast<int>(sizeof(T));
   const int nst = (bytes + RUN - 1) / RUN;
   const int my = row_adapter(a, m0, lane);
+  const Ranks ranks(a, lane);
   unsigned rest = static_cast<unsigned>(__ballot(my >= 0)) & 0xffffu;
   // Pass p of the tile's adapters runs in workgroup p mod grid.z.
   for (unsigned pass = 0; rest != 0; ++pass) {
@@ -166,7 +202,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
     const bool mine = my == ad;
     rest &= ~static_cast<unsigned>(__ballot(mine));
     if (pass % gridDim.z != blockIdx.z) continue;
-    const int rank = rank_of(a, ad);
+    const int rank = ranks(a, ad);
     if (rank == 0) continue;
 
     // Copy q of this wave: rows RPC (wave + NW q) to + RPC - 1 of the stage.
@@ -184,11 +220,11 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
         const int j = row - 16 < rank ? row - 16 : rank - 1;
         p = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K;
       }
-      src[q] = reinterpret_cast<const uint8_t*>(p + k0);
+      src[q] = reinterpret_cast<const uint8_t*>(p);
     }
     auto issue = [&](int s, uint8_t* buf) {
       const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(buf));
-      const int left = bytes - s * RUN;  // past the part's end: the stage's first unit again
+      const int left = bytes - s * RUN;  // past the row's end: the stage's first unit again
 #pragma unroll
       for (int q = 0; q < CPW; ++q)
         dma16(src[q] + s * RUN + (off[q] < left ? off[q] : 0), b + 1024 * (wave + NW * q));
@@ -238,47 +274,70 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
 #pragma unroll
     for (int c = 0; c < NT; ++c) red[wave][c][lane] = acc[c];
     __syncthreads();
-    float* tp = a.t + (static_cast<int64_t>(split) * a.M + m0 + r) * adapter_tstride(a.R);
-    for (int c = wave; c < NT && 16 * c < rank; c += NW) {
+    // Lane 16 g + r: ranks 16 c + 4 g + i of row r, scaled, zero past the rank.
+    const float scale = a.scales ? a.scales[ad] : 1.f;
+    f32x4 (*joined)[64] = reinterpret_cast<f32x4 (*)[64]>(st1);
+    for (int c = wave; c < NT; c += NW) {
       f32x4 sum = red[0][c][lane];
 #pragma unroll
       for (int w = 1; w < NW; ++w) sum += red[w][c][lane];
-      // Result lane 16 g + r: ranks 16 c + 4 g + i of row r.
-      if (mine) *reinterpret_cast<f32x4*>(tp + 16 * c + 4 * g) = sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = 16 * c + 4 * g + i < rank ? sum[i] * scale : 0.f;
+      joined[c][lane] = sum;
+    }
+    __syncthreads();
+    const int64_t ts = adapter_tstride(a.R);
+    if constexpr (sizeof(T) == 2) {
+      // t as fp16 pair, hi + lo: the row's largest finite |t| is moved to
+      // [2^13, 2^14), so that the pair holds about 22 bits whatever its size.
+      float big = 0.f;
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = fabsf(joined[c][lane][i]);
+          big = fmaxf(big, v < INFINITY ? v : 0.f);
+        }
+      big = fmaxf(big, __shfl_xor(big, 16));
+      big = fmaxf(big, __shfl_xor(big, 32));
+      int e = 0;
+      if (big > 0.f) {
+        (void)frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
+        e = 14 - e;
+        e = e > 120 ? 120 : e;
+      }
+      _Float16* hi = reinterpret_cast<_Float16*>(a.t) + (m0 + r) * ts + 4 * g;
+      for (int c = wave; 16 * c < ts; c += NW) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (c < NT) v = joined[c][lane];
+        half4 h, l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = ldexpf(v[i], e);
+          h[i] = static_cast<_Float16>(u);
+          const float d = u - static_cast<float>(h[i]);
+          l[i] = static_cast<_Float16>(fabsf(u) < INFINITY ? d : 0.f);
+        }
+        if (mine) {
+          *reinterpret_cast<half4*>(hi + 16 * c) = h;
+          *reinterpret_cast<half4*>(hi + a.M * ts + 16 * c) = l;
+        }
+      }
+      if (mine && wave == 0 && g == 0) a.t[a.M * ts + m0 + r] = ldexpf(1.f, -e);
+    } else {
+      float* tp = a.t + (m0 + r) * ts + 4 * g;
+      for (int c = wave; 16 * c < ts; c += NW) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (c < NT) v = joined[c][lane];
+        if (mine) *reinterpret_cast<f32x4*>(tp + 16 * c) = v;
+      }
     }
     __syncthreads();  // the sums are read before the next adapter's stages
   }
 }
 
-// ---- out = y + s t . Bt^T ------------------------------------------------------
-// A workgroup of four waves takes a tile of 16 rows (slot s: those of the
-// adapter that row s leads) and `steps` x 256 columns, a wave 64 of each 256.
-// Column q of the four column blocks of a wave is matrix column 4 c + q, so
-// that a lane holds four consecutive columns of a row and the loads of y and
-// the stores of out are runs of 256 bytes.
-
-// Ranks [j0, j0 + FL) of row m's t, scaled, zero past the rank.
-template <typename T>
-__device__ __forceinline__ void load_t(const AdapterArgs& a, int64_t m, int j0, int rank, float s,
-                                       float* v) {
-  constexpr int FL = Frag<T>::FL;
-  const int64_t ts = adapter_tstride(a.R);
-#pragma unroll
-  for (int e = 0; e < FL; ++e) v[e] = 0.f;
-  if (j0 >= rank) return;
-  const float* p = a.t + m * ts + j0;
-  for (int q = 0; q < a.S; ++q, p += a.M * ts) {
-#pragma unroll
-    for (int e = 0; e < FL; e += 4) {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(p + e);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[e + i] += w[i];
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < FL; ++e) v[e] = j0 + e < rank ? v[e] * s : 0.f;
-}
-
+// Four consecutive columns of a row, those past its end left alone.  y and out
+// pass once.
 __device__ __forceinline__ f32x4 load_y(const float* row, int64_t n, int64_t N) {
   if (n + 4 <= N) return __builtin_nontemporal_load(reinterpret_cast<const vf4u*>(row + n));
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -287,199 +346,396 @@ __device__ __forceinline__ f32x4 load_y(const float* row, int64_t n, int64_t N) 
     if (n + i < N) v[i] = row[n + i];
   return v;
 }
+__device__ __forceinline__ void store_out(float* row, int64_t n, int64_t N, f32x4 v) {
+  if (n + 4 <= N) {
+    __builtin_nontemporal_store(static_cast<vf4u>(v), reinterpret_cast<vf4u*>(row + n));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) row[n + i] = v[i];
+  }
+}
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(256) expand_kernel(AdapterArgs a, int steps) {
-  using F = Frag<T>;
-  typedef typename F::V V;
-  constexpr bool F16 = F::FL == 8;
+// ---- out = y + s t . Bt^T: a row at a time -------------------------------------
+// For rows that share their adapter with few others the matrix instruction
+// would multiply mostly zeros.  Here LPC lanes take a column: each holds PL
+// (16 bytes) of its ranks, so that a wave's load is one run of 1 KB of Bt, eight
+// of them in flight.  The dot products' parts are joined by halving: in
+// every step the lanes of a pair exchange the half of their columns that the
+// other one keeps, and a lane ends up with one column (or more, where LPC < 8).
+
+// The rows `rows` of the tile at m0 (all of adapter ad, or without one: ad < 0),
+// columns [n0, n0 + 512 / LPC), by one wave.
+template <typename T, int LPC, int S>
+__device__ __forceinline__ void rows_pass(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
+                                          int rank, int64_t n0) {
+  constexpr int PL = 16 / sizeof(T), CPI = 64 / LPC, NI = 8;
+  constexpr int KEEP = LPC < NI ? NI / LPC : 1;  // columns of a lane at the end
+  typedef T V __attribute__((ext_vector_type(PL)));
   const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int my = row_adapter(a, m0, lane);
-  const bool in_place = a.y == a.out;
-  // Bit r of `rows`: row r is written here; of `todo`: and has an adapter.
-  unsigned rows = a.M - m0 >= 16 ? 0xffffu : (1u << (a.M - m0)) - 1;
-  unsigned todo = static_cast<unsigned>(__ballot(my >= 0)) & 0xffffu;
-  if (gridDim.z > 1) {
-    const int s = blockIdx.z;
-    rows &= static_cast<unsigned>(__ballot(my == __builtin_amdgcn_readlane(my, s)));
-    if (rows == 0 || static_cast<int>(__builtin_ctz(rows)) != s) return;  // led by another row
-    todo &= rows;
-  }
-  if (in_place) rows = todo;
-  if (rows == 0) return;
-
-  // t as matrix operand: lane 16 g + r holds row r.
-  V hi[NC], lo[NC];
-  float un[4] = {1.f, 1.f, 1.f, 1.f};  // of rows 4 g + i
-  if (todo != 0) {
-    int rank = 0;
-    float s = 1.f, unscale = 1.f;
-    if (todo >> r & 1) {
-      rank = a.ranks ? a.ranks[my] : a.R;
-      rank = rank < 0 ? 0 : rank > a.R ? a.R : rank;
-      if (a.scales) s = a.scales[my];
-    }
-    float v[NC][F::FL];
+  const int sub = lane % LPC, grp = lane / LPC;
+  const int j0 = sub * PL;
+  V b[NI];
+  float scale = 1.f;
+  if (ad >= 0) {
+    const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load_t<T>(a, m0 + r, c * F::KC + F::FL * g, rank, s, v[c]);
-    if constexpr (F16) {
-      // The row's largest finite |t| is moved to [2^13, 2^14): t fits an fp16
-      // pair whatever its magnitude.
-      float big = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (fabsf(v[c][e]) < INFINITY) big = fmaxf(big, fabsf(v[c][e]));
-      big = fmaxf(big, __shfl_xor(big, 16));
-      big = fmaxf(big, __shfl_xor(big, 32));
-      float scale = 1.f;
-      if (big > 0.f) {
-        int e;
-        (void)frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
-        e = 14 - e;
-        e = e > 120 ? 120 : e;
-        scale = ldexpf(1.f, e);
-        unscale = ldexpf(1.f, -e);
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = v[c][e] * scale;
-          const _Float16 h = static_cast<_Float16>(u);
-          const float d = u - static_cast<float>(h);
-          hi[c][e] = h;
-          lo[c][e] = fabsf(u) < INFINITY ? static_cast<_Float16>(d) : static_cast<_Float16>(0.f);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) un[i] = __shfl(unscale, 4 * g + i);
-    } else {
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int e = 0; e < F::FL; ++e) hi[c][e] = v[c][e];
-    }
-  }
-
-  for (int step = 0; step < steps; ++step) {
-    const int64_t n0 = (static_cast<int64_t>(blockIdx.y) * steps + step) * 256 + 64 * wave;
-    if (n0 >= a.N) return;
-    const int64_t n = n0 + 4 * r;
-    f32x4 yv[4], acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      yv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (a.y && (rows >> (4 * g + i) & 1)) yv[i] = load_y(a.y + (m0 + 4 * g + i) * a.ldy, n, a.N);
-    }
-    unsigned rest = todo;
-    while (rest != 0) {
-      const int ad = __builtin_amdgcn_readlane(my, __builtin_ctz(rest));
-      const unsigned same = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
-      const int rank = rank_of(a, ad);
-      const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
-      f32x4 d[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (c * F::KC >= rank) break;
-        const int j = c * F::KC + g * F::FL;
-        V b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t col = n + q < a.N ? n + q : a.N - 1;
-          const T* p = bb + col * a.R + j;
-          b[q] = V{};
-          if (a.R % F::FL == 0) {
-            if (j < a.R) b[q] = *reinterpret_cast<const V*>(p);
-          } else {
-#pragma unroll
-            for (int e = 0; e < F::FL; ++e)
-              if (j + e < a.R) b[q][e] = p[e];
-          }
-        }
-        if (c * F::KC + F::KC > rank) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int e = 0; e < F::FL; ++e) b[q][e] = j + e < rank ? b[q][e] : static_cast<T>(0.f);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d[q] = F::mma(hi[c], b[q], d[q]);
-          if constexpr (F16) d[q] = F::mma(lo[c], b[q], d[q]);
-        }
-      }
-      // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool of = same >> (4 * g + i) & 1;  // other rows' values may be anything
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][q] = of ? d[q][i] : acc[i][q];
-      }
-      rest &= ~same;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!(rows >> (4 * g + i) & 1)) continue;
-      const f32x4 v = yv[i] + acc[i] * un[i];
-      float* p = a.out + (m0 + 4 * g + i) * a.ldo + n;
-      if (n + 4 <= a.N) {
-        __builtin_nontemporal_store(static_cast<vf4u>(v), reinterpret_cast<vf4u*>(p));
+    for (int i = 0; i < NI; ++i) {
+      const int64_t n = n0 + i * CPI + grp;
+      const T* p = bb + (n < a.N ? n : a.N - 1) * a.R;
+      if (a.R % PL == 0) {
+        b[i] = *reinterpret_cast<const V*>(p + (j0 < a.R ? j0 : 0));
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < a.N) p[q] = v[q];
+        for (int e = 0; e < PL; ++e) b[i][e] = p[j0 + e < a.R ? j0 + e : 0];
       }
+    }
+    if (a.scales) scale = a.scales[ad];
+  }
+  // The lane's columns at the end: n0 + CPI (first + i) + grp, i < KEEP.
+  int first = 0;
+  bool last = true;  // of the lanes that hold the same column, the one that stores it
+#pragma unroll
+  for (int h = LPC / 2, cnt = NI; h >= 1; h /= 2) {
+    if (cnt > 1) {
+      cnt /= 2;
+      if (sub & h) first += cnt;
+    } else if (sub & h) {
+      last = false;
+    }
+  }
+  const int64_t ts = adapter_tstride(a.R);
+  for (; rows != 0; rows &= rows - 1) {
+    const int64_t m = m0 + __builtin_ctz(rows);
+    float y[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+      const int64_t n = n0 + CPI * (first + i) + grp;
+      y[i] = a.y && n < a.N ? a.y[m * a.ldy + n] : 0.f;
+    }
+    float v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) v[i] = 0.f;
+    if (ad >= 0 && rank > 0) {
+      f32x4 tp[S][PL / 4];
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+#pragma unroll
+        for (int e = 0; e < PL / 4; ++e)
+          tp[q][e] = reinterpret_cast<const f32x4*>(a.t + (q * a.M + m) * ts + (j0 < a.R ? j0 : 0))[e];
+#pragma unroll
+      for (int e = 0; e < PL; ++e) {
+        float t = tp[0][e / 4][e % 4];
+#pragma unroll
+        for (int q = 1; q < S; ++q) t += tp[q][e / 4][e % 4];
+        t = j0 + e < rank ? t * scale : 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          v[i] = fmaf(t, j0 + e < rank ? static_cast<float>(b[i][e]) : 0.f, v[i]);
+      }
+#pragma unroll
+      for (int h = LPC / 2, cnt = NI; h >= 1; h /= 2) {
+        if (cnt > 1) {
+          cnt /= 2;
+#pragma unroll
+          for (int i = 0; i < cnt; ++i) {
+            const float keep = sub & h ? v[i + cnt] : v[i];
+            const float send = sub & h ? v[i] : v[i + cnt];
+            v[i] = keep + __shfl_xor(send, h);
+          }
+        } else {
+          v[0] += __shfl_xor(v[0], h);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+      const int64_t n = n0 + CPI * (first + i) + grp;
+      if (last && n < a.N) a.out[m * a.ldo + n] = y[i] + v[i];
     }
   }
 }
 
+// The same rows, 64 columns from n0, by one wave with the float32 matrix
+// instruction, t as it is (for groups of rows; about eight times the price of
+// the fp16 pair per product, which few rows do not notice).
+template <typename T, int RC, int S>
+__device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
+                                           int rank, int64_t n0) {
+  constexpr int PL = sizeof(T) == 2 && RC > 16 ? 8 : 4;  // ranks of a lane in a chunk
+  constexpr int KC = 4 * PL, NC = RC / KC;
+  typedef T V __attribute__((ext_vector_type(PL)));
+  const int lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n = n0 + 4 * r, ts = adapter_tstride(a.R);
+  f32x4 yv[4], d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    yv[i] = d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.y && (rows >> (4 * g + i) & 1)) yv[i] = load_y(a.y + (m0 + 4 * g + i) * a.ldy, n, a.N);
+  }
+  if (ad >= 0) {
+    const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
+    const float* tp = a.t + (m0 + (rows >> r & 1 ? r : __builtin_ctz(rows))) * ts;
+    const float scale = a.scales ? a.scales[ad] : 1.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (c * KC >= rank) break;
+      const int k = c * KC + PL * g, at = k < a.R ? k : 0;
+      V b[4];
+      f32x4 w[S][PL / 4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const T* p = bb + (n + q < a.N ? n + q : a.N - 1) * a.R;
+        if (a.R % PL == 0) {
+          b[q] = *reinterpret_cast<const V*>(p + at);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PL; ++e) b[q][e] = p[k + e < a.R ? k + e : 0];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+#pragma unroll
+        for (int e = 0; e < PL / 4; ++e)
+          w[q][e] = *reinterpret_cast<const f32x4*>(tp + q * a.M * ts + at + 4 * e);
+#pragma unroll
+      for (int e = 0; e < PL; ++e) {
+        float t = w[0][e / 4][e % 4];
+#pragma unroll
+        for (int q = 1; q < S; ++q) t += w[q][e / 4][e % 4];
+        t = k + e < rank ? t * scale : 0.f;  // past the rank: anything
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          d[q] = __builtin_amdgcn_mfma_f32_16x16x4f32(t, k + e < rank ? static_cast<float>(b[q][e]) : 0.f,
+                                                      d[q], 0, 0, 0);
+      }
+    }
+  }
+  // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (rows >> (4 * g + i) & 1)
+      store_out(a.out + (m0 + 4 * g + i) * a.ldo, n, a.N, yv[i] + f32x4{d[0][i], d[1][i], d[2][i], d[3][i]});
+}
+
+// Workgroup (4 x 512 / LPC columns, tile, slot): slot s takes the rows of the
+// adapter that row s of the tile leads, a few of them one by one.
+constexpr int kRowByRow = 3;
+
+template <typename T, int RC, int S>
+__global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
+  constexpr int LPC = RC * static_cast<int>(sizeof(T)) / 16, COLS = 4 * 512 / LPC;
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * COLS;
+  const int my = row_adapter(a, m0, lane);
+  const Ranks ranks(a, lane);
+  const int s = blockIdx.z;
+  if (m0 + s >= a.M) return;
+  const int ad = __builtin_amdgcn_readlane(my, s);
+  unsigned rows = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
+  if (a.M - m0 < 16) rows &= (1u << (a.M - m0)) - 1;
+  if (static_cast<int>(__builtin_ctz(rows)) != s) return;  // led by another row
+  if (ad < 0 && a.y == a.out) return;                      // in place, nothing to add
+  const int rank = ad < 0 ? 0 : ranks(a, ad);
+  if (__builtin_popcount(rows) <= kRowByRow) {
+    const int64_t n = n0 + wave * (COLS / 4);
+    if (n < a.N) rows_pass<T, LPC, S>(a, m0, rows, ad, rank, n);
+  } else {
+    for (int64_t n = n0 + 64 * wave; n < n0 + COLS && n < a.N; n += 256)
+      group_pass<T, RC, S>(a, m0, rows, ad, rank, n);
+  }
+}
+
+// ---- out = y + s t . Bt^T: many rows -------------------------------------------
+// A workgroup of four waves takes 16 rows and 256 columns, a wave 64 of them;
+// t comes ready as matrix operand (fp16: the pair, two products; one where
+// both parts fit an operand of 32 ranks).  Column q of a wave's four column
+// blocks is matrix column 4 c + q, so that a lane holds four consecutive columns
+// of a row and the loads of y and the stores of out are runs of 256 bytes.  The
+// loads of y and t go out beside those of the rows' adapters.
+// RC: the ranks, rounded up (16, 32, 64, 128).  SHARED: pass p of the tile's
+// adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
+template <typename T, int RC, bool SHARED>
+__global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
+  using F = Frag<T>;
+  typedef typename F::V V;
+  constexpr bool F16 = sizeof(T) == 2;
+  constexpr bool BOTH = F16 && RC == 16;  // hi in ranks 0 .. 15 of an operand, lo in 16 .. 31
+  constexpr int NC = BOTH ? 1 : RC / F::KC;
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t m0 = tile_row(a);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 256 + 64 * wave;
+  if (m0 >= a.M || n0 >= a.N) return;
+  const int64_t n = n0 + 4 * r;
+  const int64_t ts = adapter_tstride(a.R);
+  // Bit r of `rows`: row r is written here; of `todo`: and has an adapter.
+  unsigned rows = a.M - m0 >= 16 ? 0xffffu : (1u << (a.M - m0)) - 1;
+
+  f32x4 yv[4];
+  auto load_rows = [&](unsigned of) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      yv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (a.y && (of >> (4 * g + i) & 1)) yv[i] = load_y(a.y + (m0 + 4 * g + i) * a.ldy, n, a.N);
+    }
+  };
+  if constexpr (!SHARED) load_rows(rows);
+  // Row r's t (of a row without an adapter: anything, and not used).
+  V hi[NC], lo[NC];
+  f32x4 un = {1.f, 1.f, 1.f, 1.f};
+  const int64_t mt = m0 + r < a.M ? m0 + r : a.M - 1;
+  const int j = BOTH ? 8 * (g & 1) : F::FL * g;  // the lane's first rank in a chunk
+  const T* tp = reinterpret_cast<const T*>(a.t) + mt * ts + j;
+  if constexpr (BOTH) {
+    hi[0] = *reinterpret_cast<const V*>(tp + (g >> 1) * a.M * ts);
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = c * F::KC < a.R ? c * F::KC : 0;
+      hi[c] = *reinterpret_cast<const V*>(tp + at);
+      if constexpr (F16) lo[c] = *reinterpret_cast<const V*>(tp + a.M * ts + at);
+    }
+  }
+  if constexpr (F16) un = *reinterpret_cast<const f32x4*>(a.t + a.M * ts + m0 + 4 * g);
+  const int my = row_adapter(a, m0, lane);
+  const Ranks ranks(a, lane);
+  const unsigned todo = static_cast<unsigned>(__ballot(my >= 0)) & 0xffffu;
+  unsigned mine = todo;  // the rows that are multiplied here
+  if constexpr (SHARED) {
+    mine = 0;
+    unsigned pass = 0;
+    for (unsigned rest = todo; rest != 0; ++pass) {
+      const unsigned same =
+          static_cast<unsigned>(__ballot(my == __builtin_amdgcn_readlane(my, __builtin_ctz(rest)))) & 0xffffu;
+      if (pass % gridDim.z == blockIdx.z) mine |= same;
+      rest &= ~same;
+    }
+    rows = mine | (blockIdx.z == 0 ? rows & ~todo : 0);
+  }
+  if (a.y == a.out) rows = mine;
+  if (rows == 0) return;
+  if constexpr (SHARED) load_rows(rows);
+
+  f32x4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (unsigned rest = mine; rest != 0;) {
+    const int ad = __builtin_amdgcn_readlane(my, __builtin_ctz(rest));
+    const unsigned same = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
+    const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
+    const int rank = ranks(a, ad);
+    rest &= ~same;
+    if (rank == 0) continue;  // t was not written
+    f32x4 d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int k = c * F::KC + j;
+      if (c * F::KC >= rank) break;
+      V b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const T* p = bb + (n + q < a.N ? n + q : a.N - 1) * a.R;
+        if (F16 || a.R % F::FL == 0) {
+          b[q] = *reinterpret_cast<const V*>(p + (k < a.R ? k : 0));
+        } else {
+#pragma unroll
+          for (int e = 0; e < F::FL; ++e) b[q][e] = p[k + e < a.R ? k + e : 0];
+        }
+      }
+      if (c * F::KC + (BOTH ? 16 : F::KC) > rank) {  // past the rank: anything
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < F::FL; ++e) b[q][e] = k + e < rank ? b[q][e] : static_cast<T>(0.f);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        d[q] = F::mma(hi[c], b[q], d[q]);
+        if constexpr (F16 && !BOTH) d[q] = F::mma(lo[c], b[q], d[q]);
+      }
+    }
+    // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool of = same >> (4 * g + i) & 1;  // other rows' values may be anything
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][q] = of ? d[q][i] * un[i] : acc[i][q];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!(rows >> (4 * g + i) & 1)) continue;
+    store_out(a.out + (m0 + 4 * g + i) * a.ldo, n, a.N, yv[i] + acc[i]);
+  }
+}
+
+unsigned slots(int64_t M) { return M < 16 ? static_cast<unsigned>(M) : 16; }
+
+template <typename T, int RC>
+void launch_expand(const AdapterArgs& a, bool many, unsigned gx, hipStream_t st) {
+  if constexpr (RC <= 128) {
+    if (many) {
+      const unsigned gy = static_cast<unsigned>((a.N + 255) / 256);
+      const int64_t share = kShareWorkgroups / (static_cast<int64_t>(gx) * gy);
+      if (share <= 1)
+        hipLaunchKernelGGL((expand_many_kernel<T, RC, false>), dim3(gx, gy), dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((expand_many_kernel<T, RC, true>),
+                           dim3(gx, gy, static_cast<unsigned>(share < 16 ? share : 16)), dim3(256), 0, st, a);
+      return;
+    }
+  }
+  constexpr int COLS = 4 * 512 * 16 / (RC * static_cast<int>(sizeof(T)));
+  const dim3 grid(static_cast<unsigned>((a.N + COLS - 1) / COLS), static_cast<unsigned>((a.M + 15) / 16),
+                  slots(a.M));
+  if (a.S == 1)
+    hipLaunchKernelGGL((expand_rows_kernel<T, RC, 1>), grid, dim3(256), 0, st, a);
+  else if constexpr (RC <= 128)
+    hipLaunchKernelGGL((expand_rows_kernel<T, RC, kParts>), grid, dim3(256), 0, st, a);
+}
+
 template <typename T, int NT, int RUN, int NW>
-void launch_stage(const AdapterArgs& a, unsigned tiles, hipStream_t st) {
-  hipLaunchKernelGGL((shrink_stage_kernel<T, NT, RUN, NW>), dim3(tiles, a.S, 2), dim3(64 * NW), 0, st, a);
+void launch_stage(const AdapterArgs& a, unsigned gx, hipStream_t st) {
+  const unsigned share = kShareStages / gx;
+  hipLaunchKernelGGL((shrink_stage_kernel<T, NT, RUN, NW>), dim3(gx, 1, share < 2 ? 2 : share > 16 ? 16 : share),
+                     dim3(64 * NW), 0, st, a);
 }
 
 template <typename T>
 hipError_t launch_typed(const AdapterArgs& a, hipStream_t st) {
   const unsigned tiles = static_cast<unsigned>((a.M + 15) / 16);
-  const unsigned slots = static_cast<unsigned>(a.M < 16 ? a.M : 16);
-  if (tiles >= kStageTiles && a.R <= 128) {
-    if (a.R <= 16) launch_stage<T, 1, 512, 8>(a, tiles, st);
-    else if (a.R <= 32) launch_stage<T, 2, 512, 8>(a, tiles, st);
-    else if (a.R <= 64) launch_stage<T, 4, 256, 4>(a, tiles, st);
-    else launch_stage<T, 8, 256, 4>(a, tiles, st);
+  const bool many = adapter_many(a.M, a.R);
+  const unsigned gx = many ? (tiles + 7) / 8 * 8 : tiles;
+  if (many) {
+    if (a.R <= 16) launch_stage<T, 1, 512, 8>(a, gx, st);
+    else if (a.R <= 32) launch_stage<T, 2, 512, 8>(a, gx, st);
+    else if (a.R <= 64) launch_stage<T, 4, 256, 4>(a, gx, st);
+    else launch_stage<T, 8, 256, 4>(a, gx, st);
   } else {
-    hipLaunchKernelGGL((shrink_block_kernel<T>), dim3(tiles, a.S * ((a.R + 15) / 16), slots),
+    hipLaunchKernelGGL((shrink_block_kernel<T>), dim3(gx, a.S * ((a.R + 15) / 16), slots(a.M)),
                        dim3(64 * kBlockWaves), 0, st, a);
   }
-  const int steps = tiles >= 64 ? 4 : 1;
-  const dim3 grid(tiles, static_cast<unsigned>((a.N + 256 * steps - 1) / (256 * steps)), tiles >= 64 ? 1 : slots);
-  const int chunks = static_cast<int>((a.R + Frag<T>::KC - 1) / Frag<T>::KC);
-  if (chunks <= 1) hipLaunchKernelGGL((expand_kernel<T, 1>), grid, dim3(256), 0, st, a, steps);
-  else if (chunks <= 2) hipLaunchKernelGGL((expand_kernel<T, 2>), grid, dim3(256), 0, st, a, steps);
-  else if (chunks <= 4) hipLaunchKernelGGL((expand_kernel<T, 4>), grid, dim3(256), 0, st, a, steps);
-  else if (chunks <= 8) hipLaunchKernelGGL((expand_kernel<T, 8>), grid, dim3(256), 0, st, a, steps);
-  else hipLaunchKernelGGL((expand_kernel<T, 16>), grid, dim3(256), 0, st, a, steps);
+  if (a.R <= 16) launch_expand<T, 16>(a, many, gx, st);
+  else if (a.R <= 32) launch_expand<T, 32>(a, many, gx, st);
+  else if (a.R <= 64) launch_expand<T, 64>(a, many, gx, st);
+  else if (a.R <= 128) launch_expand<T, 128>(a, many, gx, st);
+  else launch_expand<T, 256>(a, many, gx, st);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Parts that K is split into: the staged kernel's tiles fill the chip by
-// themselves; a few rows need parts, at least 256 channels each.
-int adapter_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + 15) / 16;
-  if (tiles >= kStageTiles) return tiles >= 256 || K < 1024 ? 1 : 2;
-  const int64_t want = (128 + M - 1) / M;
-  const int64_t most = (K + 255) / 256;
-  const int64_t s = want < most ? want : most;
-  return static_cast<int>(s < 1 ? 1 : s > 8 ? 8 : s);
+// Parts that K is split into: where rows times blocks of ranks are too few
+// workgroups to draw on the chip's bandwidth (at most 16 of them), four.
+int adapter_splits(int64_t M, int64_t K, int64_t rank) {
+  return !adapter_many(M, rank) && M * ((rank + 15) / 16) <= 16 && K >= 512 * kParts && rank <= 128 ? kParts : 1;
 }
 
 hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st) {

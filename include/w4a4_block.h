@@ -52,11 +52,9 @@ size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank);
  *   scales  [adapters] float32, or NULL (all 1).
  *   y       [M, N] float32, or NULL (zero).  out [M, N] float32; out may
  *           equal y when ldo equals ldy.
- *   t is accumulated in float32.  With fp16 factors it enters the second
- *   product as an fp16 pair (hi + lo, scaled by a power of two per row, about
- *   22 significant bits); sums are float32.  A row's result depends on its
- *   own inputs only (not on the other rows' values) and is the same from
- *   call to call.
+ *   t and both sums are float32 (t is not rounded to the factors' type).  A
+ *   row's result depends on its own inputs only (not on the other rows'
+ *   values) and is the same from call to call.
  *   workspace: at least w4a4_adapter_workspace_size(M, K, rank) bytes.
  */
 int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, const void* Bt,
