@@ -14,6 +14,7 @@ Outputs that the caller does not pass are allocated with torch.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import struct
@@ -136,6 +137,7 @@ def _launch(fn: str, dev: int, form: struct.Struct, *args) -> None:
 
 
 # ---- low-rank adapters of many requests ---------------------------------------
+@functools.lru_cache(maxsize=1024)
 def adapter_workspace_size(M: int, K: int, rank: int) -> int:
     return int(lib().w4a4_adapter_workspace_size(M, K, rank))
 

@@ -44,12 +44,9 @@ struct Frag<float> {
   }
 };
 
+// Rows from which a call is taken as one of prompts: x . A staged, the rows'
+// products on the matrix instruction.
 constexpr int64_t kManyRows = 128;
-// Whether a call is taken as one of prompts: x . A staged, all adapters of a
-// tile in one workgroup.
-__host__ __device__ inline bool adapter_many(int64_t M, int64_t R) { return M >= kManyRows && R <= 128; }
-// Parts that K is split into, where it is.
-constexpr int kParts = 4;
 // Workgroups up to which a tile's adapters are shared out among several of them
 // (tiles of one adapter leave the others with nothing to do).
 constexpr unsigned kShareStages = 1024;
@@ -58,13 +55,11 @@ constexpr int64_t kShareWorkgroups = 2048;
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The first row of a workgroup's tile.  Consecutive workgroups go to the eight
-// XCDs in turn.  With many tiles (grid.x then a multiple of eight) each XCD
-// takes a contiguous eighth of them, so that its L2 holds the factors of the few
-// requests there; the grid's padding falls past the last row.
-__device__ __forceinline__ int64_t tile_row(const AdapterArgs& a) {
-  int64_t tile = blockIdx.x;
-  if (adapter_many(a.M, a.R)) tile = (tile & 7) * (gridDim.x >> 3) + (tile >> 3);
-  return tile * 16;
+// XCDs in turn (grid.x is a multiple of eight); each XCD takes a contiguous
+// eighth of the tiles, so that its L2 holds the factors of the few requests there.
+// The grid's padding falls past the last row.
+__device__ __forceinline__ int64_t tile_row() {
+  return (static_cast<int64_t>(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) * 16;
 }
 
 // The adapter of row m0 + (lane & 15), -1 where there is none.
@@ -88,76 +83,157 @@ struct Ranks {
   }
 };
 
-// ---- t = x . At^T: one 16 x 16 block per workgroup -----------------------------
-// Workgroup (tile, part of K and block of 16 ranks, slot): slot s (or every
-// slot in turn, where grid.z is 1) runs the adapter led by row s of the tile.
-// The waves share the part of K; their sums are joined in LDS in order.  All
-// loads are whole and unconditional, up to eight chunks of them in flight: ranks
-// past the adapter's read its last one, rows of other adapters the leading row
-// (both fall on lines that are read anyway; neither enters a stored result).
-constexpr int kBlockWaves = 16;
+// ---- t = x . At^T: a few rows --------------------------------------------------
+// A wave's load is one run of 1 KB of a rank's row of At or of a row of x; eight
+// ranks are multiplied by up to MR rows in registers, and the lanes' parts of
+// the eight sums are joined by halving: in each of the first three steps the
+// lanes of a pair exchange the half of the sums that the other one keeps, after
+// which a lane has one sum left and joins it with seven neighbours.  Larger
+// groups of rows go to the matrix instruction.
 
-template <typename T>
-__global__ void __launch_bounds__(64 * kBlockWaves) shrink_block_kernel(AdapterArgs a) {
-  using F = Frag<T>;
-  typedef typename F::V V;
-  __shared__ f32x4 red[kBlockWaves][64];
+// Ranks j0 to j0 + 7 (those past `rank`: its last one) of adapter ad with the
+// first MR rows of `rows` (its last one again, if there are fewer), over chunks
+// first, first + step, ... of K: out[8 i + j] for row i.
+template <typename T, int MR>
+__device__ __forceinline__ void rows_dot(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
+                                         int rank, int j0, int first, int step, float* out) {
+  constexpr int PL = 16 / sizeof(T), CH = 64 * PL, NJ = 8;
+  typedef T V __attribute__((ext_vector_type(PL)));
   const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = tile_row(a);
-  if (m0 >= a.M) return;
-  const int split = blockIdx.y % a.S, rb = blockIdx.y / a.S;
-  const int k0 = a.K / 64 * split / a.S * 64, k1 = a.K / 64 * (split + 1) / a.S * 64;
-  const int chunks = (k1 - k0) / F::KC;
-  const int c0 = chunks * wave / kBlockWaves, c1 = chunks * (wave + 1) / kBlockWaves;
-  const int my = row_adapter(a, m0, lane);
-  const Ranks ranks(a, lane);
-  for (int s = blockIdx.z; s < 16; s += gridDim.z) {
-    const int ad = __builtin_amdgcn_readlane(my, s);
-    if (ad < 0) continue;
-    const bool mine = my == ad;
-    if (static_cast<int>(__builtin_ctzll(__ballot(mine))) != s) continue;  // led by another row
-    const int rank = ranks(a, ad);
-    if (16 * rb >= rank) continue;
-    const int j = 16 * rb + r < rank ? 16 * rb + r : rank - 1;
-    const int64_t m = m0 + (mine ? r : s);
-    const T* xr = static_cast<const T*>(a.x) + m * a.ldx + k0 + g * F::FL;
-    const T* ar = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K + k0 + g * F::FL;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    auto batch = [&](int ch, auto n) {
-      V xv[n.value], av[n.value];
+  const T* xr[MR];
 #pragma unroll
-      for (int u = 0; u < n.value; ++u) {
-        av[u] = *reinterpret_cast<const V*>(ar + (ch + u) * F::KC);
-        xv[u] = *reinterpret_cast<const V*>(xr + (ch + u) * F::KC);
+  for (int i = 0; i < MR; ++i) {
+    xr[i] = static_cast<const T*>(a.x) + (m0 + __builtin_ctz(rows)) * a.ldx;
+    if (rows & (rows - 1)) rows &= rows - 1;
+  }
+  const T* ar = static_cast<const T*>(a.At) + static_cast<int64_t>(ad) * a.R * a.K;
+  float v[MR][NJ];
+#pragma unroll
+  for (int i = 0; i < MR; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) v[i][j] = 0.f;
+  for (int c = first; c * CH < a.K; c += step) {
+    const int k = c * CH + lane * PL;
+    if (k < a.K) {
+      V av[NJ], xv[MR];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int row = j0 + j < rank ? j0 + j : rank - 1;
+        av[j] = *reinterpret_cast<const V*>(ar + static_cast<int64_t>(row) * a.K + k);
       }
 #pragma unroll
-      for (int u = 0; u < n.value; ++u) acc = F::mma(av[u], xv[u], acc);
-    };
-    int ch = c0;
-    for (; ch + 8 <= c1; ch += 8) batch(ch, std::integral_constant<int, 8>());
-    if (ch + 4 <= c1) {
-      batch(ch, std::integral_constant<int, 4>());
-      ch += 4;
+      for (int i = 0; i < MR; ++i) xv[i] = *reinterpret_cast<const V*>(xr[i] + k);
+#pragma unroll
+      for (int i = 0; i < MR; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < PL; ++e)
+            v[i][j] = fmaf(static_cast<float>(xv[i][e]), static_cast<float>(av[j][e]), v[i][j]);
     }
-    if (ch + 2 <= c1) {
-      batch(ch, std::integral_constant<int, 2>());
-      ch += 2;
+  }
+  constexpr int LPS = 64 / NJ;  // lanes with the same sum after the halving
+#pragma unroll
+  for (int i = 0; i < MR; ++i) {
+#pragma unroll
+    for (int h = 32, cnt = NJ / 2; h >= LPS; h /= 2, cnt /= 2)
+#pragma unroll
+      for (int j = 0; j < cnt; ++j) {
+        const float keep = lane & h ? v[i][j + cnt] : v[i][j];
+        const float send = lane & h ? v[i][j] : v[i][j + cnt];
+        v[i][j] = keep + __shfl_xor(send, h);
+      }
+#pragma unroll
+    for (int h = LPS / 2; h >= 1; h /= 2) v[i][0] += __shfl_xor(v[i][0], h);
+    if (lane % LPS == 0) out[NJ * i + lane / LPS] = v[i][0];
+  }
+}
+
+// Ranks j0 to j0 + 15 (those past `rank`: its last one) with the rows `rows` of
+// the tile, a part of K, on the matrix instruction: lane 16 g + r ends up with
+// ranks j0 + 4 g + i of row r.  All loads are whole and unconditional, up to
+// eight chunks of them in flight: rows of other adapters read the first of
+// `rows` (their results are not stored).
+template <typename T>
+__device__ __forceinline__ f32x4 group_dot(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
+                                           int rank, int j0, int part, int parts) {
+  using F = Frag<T>;
+  typedef typename F::V V;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int j = j0 + r < rank ? j0 + r : rank - 1;
+  const int chunks = a.K / F::KC;
+  int ch = chunks * part / parts;
+  const int end = chunks * (part + 1) / parts;
+  const T* xr = static_cast<const T*>(a.x) + (m0 + (rows >> r & 1 ? r : __builtin_ctz(rows))) * a.ldx + g * F::FL;
+  const T* ar = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K + g * F::FL;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto batch = [&](auto n) {
+    V xv[n.value], av[n.value];
+#pragma unroll
+    for (int u = 0; u < n.value; ++u) {
+      av[u] = *reinterpret_cast<const V*>(ar + (ch + u) * F::KC);
+      xv[u] = *reinterpret_cast<const V*>(xr + (ch + u) * F::KC);
     }
-    if (ch < c1) batch(ch, std::integral_constant<int, 1>());
-    red[wave][lane] = acc;
+#pragma unroll
+    for (int u = 0; u < n.value; ++u) acc = F::mma(av[u], xv[u], acc);
+    ch += n.value;
+  };
+  while (ch + 8 <= end) batch(std::integral_constant<int, 8>());
+  if (ch + 4 <= end) batch(std::integral_constant<int, 4>());
+  while (ch < end) batch(std::integral_constant<int, 1>());
+  return acc;
+}
+
+// Workgroup (eight ranks, tile, slot): slot s takes the rows of the adapter that
+// row s of the tile leads, a few of them one by one.  The waves share K; their
+// sums are joined in LDS.
+constexpr int kRowsWaves = 8;
+constexpr int kRowByRow = 3;
+
+template <typename T>
+__global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArgs a) {
+  __shared__ f32x4 red[kRowsWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
+  const int s = blockIdx.z, j0 = 8 * blockIdx.x;
+  if (m0 + s >= a.M) return;
+  const int my = row_adapter(a, m0, lane);
+  const Ranks ranks(a, lane);
+  const int ad = __builtin_amdgcn_readlane(my, s);
+  if (ad < 0) return;
+  unsigned rows = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
+  if (static_cast<int>(__builtin_ctz(rows)) != s) return;  // led by another row
+  const int rank = ranks(a, ad);
+  if (j0 >= rank) return;
+  const int64_t ts = adapter_tstride(a.R);
+  if (__builtin_popcount(rows) > kRowByRow) {
+    if (j0 & 8) return;  // sixteen ranks at a time
+    red[wave][lane] = group_dot<T>(a, m0, rows, ad, rank, j0, wave, kRowsWaves);
     __syncthreads();
     if (wave == 0) {
       f32x4 sum = red[0][lane];
 #pragma unroll
-      for (int w = 1; w < kBlockWaves; ++w) sum += red[w][lane];
-      // Result lane 16 g + r: ranks 16 rb + 4 g + i of row r.
-      if (mine)
-        *reinterpret_cast<f32x4*>(a.t + (static_cast<int64_t>(split) * a.M + m) * adapter_tstride(a.R) +
-                                  16 * rb + 4 * g) = sum;
+      for (int w = 1; w < kRowsWaves; ++w) sum += red[w][lane];
+      if (rows >> (lane & 15) & 1)
+        *reinterpret_cast<f32x4*>(a.t + (m0 + (lane & 15)) * ts + j0 + 4 * (lane >> 4)) = sum;
     }
-    __syncthreads();
+    return;
+  }
+  float* part = reinterpret_cast<float*>(red);  // [kRowsWaves][kRowByRow][8]
+  if (__builtin_popcount(rows) == 1)
+    rows_dot<T, 1>(a, m0, rows, ad, rank, j0, wave, kRowsWaves, part + wave * 8 * kRowByRow);
+  else
+    rows_dot<T, kRowByRow>(a, m0, rows, ad, rank, j0, wave, kRowsWaves, part + wave * 8 * kRowByRow);
+  __syncthreads();
+  const int j = threadIdx.x;
+  for (int i = 0; rows != 0; ++i, rows &= rows - 1) {
+    if (j < 8 && j0 + j < rank) {
+      float sum = part[8 * i + j];
+#pragma unroll
+      for (int w = 1; w < kRowsWaves; ++w) sum += part[(w * kRowByRow + i) * 8 + j];
+      a.t[(m0 + __builtin_ctz(rows)) * ts + j0 + j] = sum;
+    }
   }
 }
 
@@ -189,7 +265,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = tile_row(a);
+  const int64_t m0 = tile_row();
   if (m0 >= a.M) return;
   const int bytes = a.K * static_cast<int>(sizeof(T));
   const int nst = (bytes + RUN - 1) / RUN;
@@ -364,74 +440,85 @@ __device__ __forceinline__ void store_out(float* row, int64_t n, int64_t N, f32x
 // every step the lanes of a pair exchange the half of their columns that the
 // other one keeps, and a lane ends up with one column (or more, where LPC < 8).
 
-// The rows `rows` of the tile at m0 (all of adapter ad, or without one: ad < 0),
-// columns [n0, n0 + 512 / LPC), by one wave.
-template <typename T, int LPC, int S>
-__device__ __forceinline__ void rows_pass(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
-                                          int rank, int64_t n0) {
-  constexpr int PL = 16 / sizeof(T), CPI = 64 / LPC, NI = 8;
-  constexpr int KEEP = LPC < NI ? NI / LPC : 1;  // columns of a lane at the end
+// Columns [n0, n0 + 512 / LPC) of rows of adapter ad (or of none: ad < 0), by one
+// wave.
+template <typename T, int LPC>
+struct RowProducts {
+  static constexpr int PL = 16 / sizeof(T), CPI = 64 / LPC, NI = 8;
+  static constexpr int KEEP = LPC < NI ? NI / LPC : 1;  // columns of a lane at the end
   typedef T V __attribute__((ext_vector_type(PL)));
-  const int lane = threadIdx.x & 63;
-  const int sub = lane % LPC, grp = lane / LPC;
-  const int j0 = sub * PL;
   V b[NI];
   float scale = 1.f;
-  if (ad >= 0) {
-    const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
+  int ad, rank, sub, j0;
+  int64_t n;  // the lane's columns at the end: n + CPI i, i < KEEP
+  bool last = true;  // of the lanes that hold the same column, the one that stores it
+
+  __device__ __forceinline__ RowProducts(const AdapterArgs& a, int ad_, int rank_, int64_t n0)
+      : ad(ad_), rank(rank_) {
+    const int lane = threadIdx.x & 63;
+    const int grp = lane / LPC;
+    sub = lane % LPC;
+    j0 = sub * PL;
+    if (ad >= 0) {
+      const T* bb = static_cast<const T*>(a.Bt) + (static_cast<int64_t>(ad) * a.N + n0) * a.R;
+      const int most = a.N - n0 < 512 ? static_cast<int>(a.N - n0) - 1 : 511;  // last column from n0 on
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int64_t n = n0 + i * CPI + grp;
-      const T* p = bb + (n < a.N ? n : a.N - 1) * a.R;
-      if (a.R % PL == 0) {
-        b[i] = *reinterpret_cast<const V*>(p + (j0 < a.R ? j0 : 0));
-      } else {
+      for (int i = 0; i < NI; ++i) {
+        const int col = i * CPI + grp < most ? i * CPI + grp : most;
+        const T* p = bb + col * a.R;
+        if (sizeof(T) == 2 || a.R % PL == 0) {
+          b[i] = *reinterpret_cast<const V*>(p + (j0 < a.R ? j0 : 0));
+        } else {
 #pragma unroll
-        for (int e = 0; e < PL; ++e) b[i][e] = p[j0 + e < a.R ? j0 + e : 0];
+          for (int e = 0; e < PL; ++e) b[i][e] = p[j0 + e < a.R ? j0 + e : 0];
+        }
+      }
+      if (a.scales) scale = a.scales[ad];
+    }
+    int first = 0;
+#pragma unroll
+    for (int h = LPC / 2, cnt = NI; h >= 1; h /= 2) {
+      if (cnt > 1) {
+        cnt /= 2;
+        if (sub & h) first += cnt;
+      } else if (sub & h) {
+        last = false;
       }
     }
-    if (a.scales) scale = a.scales[ad];
+    n = n0 + CPI * first + grp;
   }
-  // The lane's columns at the end: n0 + CPI (first + i) + grp, i < KEEP.
-  int first = 0;
-  bool last = true;  // of the lanes that hold the same column, the one that stores it
+  // Zeroes what lies past the rank (anything), word by word.
+  __device__ __forceinline__ void mask() {
+    if (rank >= PL * LPC) return;
+    constexpr int EPW = 4 / sizeof(T);
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
 #pragma unroll
-  for (int h = LPC / 2, cnt = NI; h >= 1; h /= 2) {
-    if (cnt > 1) {
-      cnt /= 2;
-      if (sub & h) first += cnt;
-    } else if (sub & h) {
-      last = false;
+    for (int w = 0; w < 4; ++w) {
+      const int left = rank - (j0 + w * EPW);  // elements of this word that count
+      const uint32_t keep = left >= EPW ? ~0u : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        Words v = __builtin_bit_cast(Words, b[i]);
+        v[w] &= keep;
+        b[i] = __builtin_bit_cast(V, v);
+      }
     }
   }
-  const int64_t ts = adapter_tstride(a.R);
-  for (; rows != 0; rows &= rows - 1) {
-    const int64_t m = m0 + __builtin_ctz(rows);
+  // Row m; get(e): t of the lane's rank e, before the scale (past the rank: anything).
+  template <typename Get>
+  __device__ __forceinline__ void row(const AdapterArgs& a, int64_t m, Get get) const {
     float y[KEEP];
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-      const int64_t n = n0 + CPI * (first + i) + grp;
-      y[i] = a.y && n < a.N ? a.y[m * a.ldy + n] : 0.f;
-    }
+    for (int i = 0; i < KEEP; ++i) y[i] = a.y && n + CPI * i < a.N ? a.y[m * a.ldy + n + CPI * i] : 0.f;
     float v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) v[i] = 0.f;
-    if (ad >= 0 && rank > 0) {
-      f32x4 tp[S][PL / 4];
-#pragma unroll
-      for (int q = 0; q < S; ++q)
-#pragma unroll
-        for (int e = 0; e < PL / 4; ++e)
-          tp[q][e] = reinterpret_cast<const f32x4*>(a.t + (q * a.M + m) * ts + (j0 < a.R ? j0 : 0))[e];
+    if (rank > 0) {
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
-        float t = tp[0][e / 4][e % 4];
+        const float t = j0 + e < rank ? get(e) * scale : 0.f;
 #pragma unroll
-        for (int q = 1; q < S; ++q) t += tp[q][e / 4][e % 4];
-        t = j0 + e < rank ? t * scale : 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          v[i] = fmaf(t, j0 + e < rank ? static_cast<float>(b[i][e]) : 0.f, v[i]);
+        for (int i = 0; i < NI; ++i) v[i] = fmaf(t, static_cast<float>(b[i][e]), v[i]);
       }
 #pragma unroll
       for (int h = LPC / 2, cnt = NI; h >= 1; h /= 2) {
@@ -449,21 +536,19 @@ __device__ __forceinline__ void rows_pass(const AdapterArgs& a, int64_t m0, unsi
       }
     }
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-      const int64_t n = n0 + CPI * (first + i) + grp;
-      if (last && n < a.N) a.out[m * a.ldo + n] = y[i] + v[i];
-    }
+    for (int i = 0; i < KEEP; ++i)
+      if (last && n + CPI * i < a.N) a.out[m * a.ldo + n + CPI * i] = y[i] + v[i];
   }
-}
+};
 
 // The same rows, 64 columns from n0, by one wave with the float32 matrix
 // instruction, t as it is (for groups of rows; about eight times the price of
 // the fp16 pair per product, which few rows do not notice).
-template <typename T, int RC, int S>
+template <typename T, int RC>
 __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, unsigned rows, int ad,
                                            int rank, int64_t n0) {
   constexpr int PL = sizeof(T) == 2 && RC > 16 ? 8 : 4;  // ranks of a lane in a chunk
-  constexpr int KC = 4 * PL, NC = RC / KC;
+  constexpr int KC = 4 * PL;
   typedef T V __attribute__((ext_vector_type(PL)));
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
@@ -478,16 +563,15 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
     const T* bb = static_cast<const T*>(a.Bt) + static_cast<int64_t>(ad) * a.N * a.R;
     const float* tp = a.t + (m0 + (rows >> r & 1 ? r : __builtin_ctz(rows))) * ts;
     const float scale = a.scales ? a.scales[ad] : 1.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (c * KC >= rank) break;
+#pragma unroll 1
+    for (int c = 0; c * KC < rank; ++c) {
       const int k = c * KC + PL * g, at = k < a.R ? k : 0;
       V b[4];
-      f32x4 w[S][PL / 4];
+      f32x4 w[PL / 4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const T* p = bb + (n + q < a.N ? n + q : a.N - 1) * a.R;
-        if (a.R % PL == 0) {
+        if (sizeof(T) == 2 || a.R % PL == 0) {
           b[q] = *reinterpret_cast<const V*>(p + at);
         } else {
 #pragma unroll
@@ -495,16 +579,10 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
         }
       }
 #pragma unroll
-      for (int q = 0; q < S; ++q)
-#pragma unroll
-        for (int e = 0; e < PL / 4; ++e)
-          w[q][e] = *reinterpret_cast<const f32x4*>(tp + q * a.M * ts + at + 4 * e);
+      for (int e = 0; e < PL / 4; ++e) w[e] = *reinterpret_cast<const f32x4*>(tp + at + 4 * e);
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
-        float t = w[0][e / 4][e % 4];
-#pragma unroll
-        for (int q = 1; q < S; ++q) t += w[q][e / 4][e % 4];
-        t = k + e < rank ? t * scale : 0.f;  // past the rank: anything
+        const float t = k + e < rank ? w[e / 4][e % 4] * scale : 0.f;  // past the rank: anything
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           d[q] = __builtin_amdgcn_mfma_f32_16x16x4f32(t, k + e < rank ? static_cast<float>(b[q][e]) : 0.f,
@@ -521,9 +599,8 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
 
 // Workgroup (4 x 512 / LPC columns, tile, slot): slot s takes the rows of the
 // adapter that row s of the tile leads, a few of them one by one.
-constexpr int kRowByRow = 3;
 
-template <typename T, int RC, int S>
+template <typename T, int RC>
 __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
   constexpr int LPC = RC * static_cast<int>(sizeof(T)) / 16, COLS = 4 * 512 / LPC;
   const int lane = threadIdx.x & 63;
@@ -542,10 +619,20 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
   const int rank = ad < 0 ? 0 : ranks(a, ad);
   if (__builtin_popcount(rows) <= kRowByRow) {
     const int64_t n = n0 + wave * (COLS / 4);
-    if (n < a.N) rows_pass<T, LPC, S>(a, m0, rows, ad, rank, n);
+    if (n >= a.N) return;
+    RowProducts<T, LPC> p(a, ad, rank, n);
+    p.mask();
+    for (; rows != 0; rows &= rows - 1) {
+      const int64_t m = m0 + __builtin_ctz(rows);
+      f32x4 t[p.PL / 4];
+#pragma unroll
+      for (int e = 0; e < p.PL / 4; ++e)
+        t[e] = reinterpret_cast<const f32x4*>(a.t + m * adapter_tstride(a.R) + (p.j0 < a.R ? p.j0 : 0))[e];
+      p.row(a, m, [&](int e) { return t[e / 4][e % 4]; });
+    }
   } else {
     for (int64_t n = n0 + 64 * wave; n < n0 + COLS && n < a.N; n += 256)
-      group_pass<T, RC, S>(a, m0, rows, ad, rank, n);
+      group_pass<T, RC>(a, m0, rows, ad, rank, n);
   }
 }
 
@@ -556,7 +643,7 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // blocks is matrix column 4 c + q, so that a lane holds four consecutive columns
 // of a row and the loads of y and the stores of out are runs of 256 bytes.  The
 // loads of y and t go out beside those of the rows' adapters.
-// RC: the ranks, rounded up (16, 32, 64, 128).  SHARED: pass p of the tile's
+// RC: the ranks, rounded up (16, 32, ... 256).  SHARED: pass p of the tile's
 // adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
 template <typename T, int RC, bool SHARED>
 __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
@@ -568,7 +655,7 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = tile_row(a);
+  const int64_t m0 = tile_row();
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 256 + 64 * wave;
   if (m0 >= a.M || n0 >= a.N) return;
   const int64_t n = n0 + 4 * r;
@@ -676,67 +763,45 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   }
 }
 
-unsigned slots(int64_t M) { return M < 16 ? static_cast<unsigned>(M) : 16; }
-
-template <typename T, int RC>
-void launch_expand(const AdapterArgs& a, bool many, unsigned gx, hipStream_t st) {
-  if constexpr (RC <= 128) {
-    if (many) {
-      const unsigned gy = static_cast<unsigned>((a.N + 255) / 256);
-      const int64_t share = kShareWorkgroups / (static_cast<int64_t>(gx) * gy);
-      if (share <= 1)
-        hipLaunchKernelGGL((expand_many_kernel<T, RC, false>), dim3(gx, gy), dim3(256), 0, st, a);
-      else
-        hipLaunchKernelGGL((expand_many_kernel<T, RC, true>),
-                           dim3(gx, gy, static_cast<unsigned>(share < 16 ? share : 16)), dim3(256), 0, st, a);
-      return;
-    }
+template <typename T, int RC, int RUN, int NW>
+void launch_rank(const AdapterArgs& a, hipStream_t st) {
+  const unsigned tiles = static_cast<unsigned>((a.M + 15) / 16);
+  if (a.M >= kManyRows) {
+    const unsigned gx = (tiles + 7) / 8 * 8;
+    const unsigned stages = kShareStages / gx;
+    hipLaunchKernelGGL((shrink_stage_kernel<T, RC / 16, RUN, NW>),
+                       dim3(gx, 1, stages < 2 ? 2 : stages > 16 ? 16 : stages), dim3(64 * NW), 0, st, a);
+    const unsigned gy = static_cast<unsigned>((a.N + 255) / 256);
+    const int64_t share = kShareWorkgroups / (static_cast<int64_t>(gx) * gy);
+    if (share <= 1)
+      hipLaunchKernelGGL((expand_many_kernel<T, RC, false>), dim3(gx, gy), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((expand_many_kernel<T, RC, true>),
+                         dim3(gx, gy, static_cast<unsigned>(share < 16 ? share : 16)), dim3(256), 0, st, a);
+    return;
   }
-  constexpr int COLS = 4 * 512 * 16 / (RC * static_cast<int>(sizeof(T)));
-  const dim3 grid(static_cast<unsigned>((a.N + COLS - 1) / COLS), static_cast<unsigned>((a.M + 15) / 16),
-                  slots(a.M));
-  if (a.S == 1)
-    hipLaunchKernelGGL((expand_rows_kernel<T, RC, 1>), grid, dim3(256), 0, st, a);
-  else if constexpr (RC <= 128)
-    hipLaunchKernelGGL((expand_rows_kernel<T, RC, kParts>), grid, dim3(256), 0, st, a);
+  constexpr int WAVE_COLS = 512 * 16 / (RC * static_cast<int>(sizeof(T)));
+  const unsigned slots = static_cast<unsigned>(a.M < 16 ? a.M : 16);
+  hipLaunchKernelGGL((shrink_rows_kernel<T>), dim3(static_cast<unsigned>((a.R + 7) / 8), tiles, slots),
+                     dim3(64 * kRowsWaves), 0, st, a);
+  constexpr int COLS = 4 * WAVE_COLS;
+  hipLaunchKernelGGL((expand_rows_kernel<T, RC>), dim3(static_cast<unsigned>((a.N + COLS - 1) / COLS), tiles, slots),
+                     dim3(256), 0, st, a);
 }
 
-template <typename T, int NT, int RUN, int NW>
-void launch_stage(const AdapterArgs& a, unsigned gx, hipStream_t st) {
-  const unsigned share = kShareStages / gx;
-  hipLaunchKernelGGL((shrink_stage_kernel<T, NT, RUN, NW>), dim3(gx, 1, share < 2 ? 2 : share > 16 ? 16 : share),
-                     dim3(64 * NW), 0, st, a);
-}
-
+// RUN and NW: bytes of a row in a stage, and waves, such that two or three
+// workgroups (rank 64 and below) share a compute unit's LDS.
 template <typename T>
 hipError_t launch_typed(const AdapterArgs& a, hipStream_t st) {
-  const unsigned tiles = static_cast<unsigned>((a.M + 15) / 16);
-  const bool many = adapter_many(a.M, a.R);
-  const unsigned gx = many ? (tiles + 7) / 8 * 8 : tiles;
-  if (many) {
-    if (a.R <= 16) launch_stage<T, 1, 512, 8>(a, gx, st);
-    else if (a.R <= 32) launch_stage<T, 2, 512, 8>(a, gx, st);
-    else if (a.R <= 64) launch_stage<T, 4, 256, 4>(a, gx, st);
-    else launch_stage<T, 8, 256, 4>(a, gx, st);
-  } else {
-    hipLaunchKernelGGL((shrink_block_kernel<T>), dim3(gx, a.S * ((a.R + 15) / 16), slots(a.M)),
-                       dim3(64 * kBlockWaves), 0, st, a);
-  }
-  if (a.R <= 16) launch_expand<T, 16>(a, many, gx, st);
-  else if (a.R <= 32) launch_expand<T, 32>(a, many, gx, st);
-  else if (a.R <= 64) launch_expand<T, 64>(a, many, gx, st);
-  else if (a.R <= 128) launch_expand<T, 128>(a, many, gx, st);
-  else launch_expand<T, 256>(a, many, gx, st);
+  if (a.R <= 16) launch_rank<T, 16, 512, 8>(a, st);
+  else if (a.R <= 32) launch_rank<T, 32, 512, 8>(a, st);
+  else if (a.R <= 64) launch_rank<T, 64, 256, 4>(a, st);
+  else if (a.R <= 128) launch_rank<T, 128, 256, 4>(a, st);
+  else launch_rank<T, 256, 128, 2>(a, st);
   return hipGetLastError();
 }
 
 }  // namespace
-
-// Parts that K is split into: where rows times blocks of ranks are too few
-// workgroups to draw on the chip's bandwidth (at most 16 of them), four.
-int adapter_splits(int64_t M, int64_t K, int64_t rank) {
-  return !adapter_many(M, rank) && M * ((rank + 15) / 16) <= 16 && K >= 512 * kParts && rank <= 128 ? kParts : 1;
-}
 
 hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st) {
   return f16 ? launch_typed<_Float16>(a, st) : launch_typed<float>(a, st);

@@ -40,10 +40,9 @@ extern "C" {
 
 size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank) {
   if (M <= 0 || K <= 0 || rank <= 0) return 0;
-  // The parts of t, and one float32 per row (whole tiles of 16).
-  return static_cast<size_t>(w4a4::adapter_splits(M, K, rank)) * static_cast<size_t>(M) *
-             static_cast<size_t>(w4a4::adapter_tstride(rank)) * 4 +
-         static_cast<size_t>((M + 15) / 16 * 16) * 4;
+  // t, and one float32 per row (whole tiles of 16).
+  return (static_cast<size_t>(M) * static_cast<size_t>(w4a4::adapter_tstride(rank)) +
+          static_cast<size_t>((M + 15) / 16 * 16)) * 4;
 }
 
 int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, const void* Bt,
@@ -76,7 +75,6 @@ int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, co
   a.M = M; a.N = N; a.K = static_cast<int>(K);
   a.y = y; a.ldy = ldy; a.out = out; a.ldo = ldo;
   a.t = static_cast<float*>(workspace);
-  a.S = w4a4::adapter_splits(M, K, rank);
   return status(w4a4::launch_adapter_add(a, x_dtype == W4A4_F16, static_cast<hipStream_t>(stream)));
 }
 

@@ -23,16 +23,14 @@ struct AdapterArgs {
   int64_t ldy;
   float* out;
   int64_t ldo;
-  // x . A.  Few rows: [S, M, adapter_tstride(R)] float32 partial sums, not
-  // scaled, defined up to the row's rank.  Many rows, fp32: [M, tstride],
-  // scaled, zero past the rank; fp16: the same as fp16 pair (hi, then lo), times
-  // a power of two whose inverse follows, one float32 per row.
+  // x . A, [M, adapter_tstride(R)].  Few rows: float32, not scaled, defined up to
+  // the row's rank.  Many rows, fp32: scaled, zero past the rank; fp16: the same
+  // as fp16 pair (hi, then lo), times a power of two whose inverse follows, one
+  // float32 per row.
   float* t;
-  int S;        // parts K is split into
 };
 
-// Parts that K is split into, and the row distance of t.
-int adapter_splits(int64_t M, int64_t K, int64_t rank);
+// The row distance of t.
 __host__ __device__ inline int64_t adapter_tstride(int64_t R) { return (R + 31) / 32 * 32; }
 hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st);
 
