@@ -28,12 +28,14 @@ HEADER = os.path.join(os.path.dirname(_w.PKG), "include", "w4a4_block.h")
 
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+_PARAMS = ("post_weight", "post_bias", "pre_weight", "pre_bias")
 _DT = {torch.float32: _w.F32, torch.float16: _w.F16}
 
 # The raw handle of a device's current stream (torch's own accessor where there
 # is one: the Stream object costs another microsecond).
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                   lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current_device = torch.cuda.current_device
 
 _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _SIGS = {
@@ -46,11 +48,6 @@ _SIGS = {
     "w4a4_gated_activation": (_INT, [_P, _I64, _P, _I64, _INT, _INT, _I64, _I64, _P, _I64, _INT,
                                      _P]),
 }
-# The same calls with their arguments packed in one buffer, which costs a
-# quarter of the host time of converting them one by one.
-_ADAPTER = struct.Struct("=20q")
-_NORM = struct.Struct("=13qd4q2d8q")
-_GATED = struct.Struct("=12q")
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -83,26 +80,21 @@ def _dt(t: torch.Tensor) -> int:
     return d
 
 
-def _device(t: torch.Tensor) -> int:
-    if not t.is_cuda:
-        raise ValueError("the tensors must be device tensors")
-    return t.get_device()
-
-
-def _rows(t: torch.Tensor, name: str, dev: int, M: int, C: int) -> int:
-    """The row distance of a device matrix [M, C] with contiguous rows."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the device of the others")
-    if t.shape != (M, C):
-        raise ValueError(f"{name} must be [{M}, {C}], not {list(t.shape)}")
+def _rows(t: torch.Tensor, name: str, dev: int, shape) -> int:
+    """The row distance of a device matrix of this shape with contiguous rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     s0, s1 = t.stride()
-    if s1 != 1 and C > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if s0 >= C:
+    M, C = shape
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a device tensor, on the device of the others")
+    if s1 == 1 and s0 >= C:
         return s0
-    if M > 1 and C > 0:
+    if C > 1 and s1 != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if M > 1 and C > 0 and s0 < C:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return C
+    return s0 if s0 >= C else C
 
 
 def _whole(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
@@ -118,22 +110,29 @@ def _whole(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
     return t.data_ptr()
 
 
-def _call(fn: str, packed: bytes) -> None:
-    status = getattr(_lib, fn)(packed)
-    if status != _w.OK:
-        raise _w.W4A4Error(fn[5:-7], status)
+class _Entry:
+    """An entry point of the library, called on a device's current stream with
+    its arguments packed in one buffer: a quarter of the host time of
+    converting them one by one."""
+
+    def __init__(self, name: str, form: str):
+        self.name, self.pack, self.f = name, struct.Struct(form).pack, None
+
+    def __call__(self, dev: int, *args) -> None:
+        if self.f is None:
+            self.f = getattr(lib(), f"w4a4_{self.name}_packed")
+        if dev == _current_device():
+            status = self.f(self.pack(*args, _stream(dev)))
+        else:
+            with torch.cuda.device(dev):
+                status = self.f(self.pack(*args, _stream(dev)))
+        if status:
+            raise _w.W4A4Error(self.name, status)
 
 
-def _launch(fn: str, dev: int, form: struct.Struct, *args) -> None:
-    """The packed call on dev's current stream."""
-    if _lib is None:
-        lib()
-    packed = form.pack(*args, _stream(dev))
-    if dev == torch.cuda.current_device():
-        _call(fn, packed)
-    else:
-        with torch.cuda.device(dev):
-            _call(fn, packed)
+_adapter_add = _Entry("adapter_add", "=20q")
+_norm_residual = _Entry("norm_residual", "=13qd4q2d8q")
+_gated_activation = _Entry("gated_activation", "=12q")
 
 
 # ---- low-rank adapters of many requests ---------------------------------------
@@ -159,12 +158,12 @@ def adapter_add(y: Optional[torch.Tensor], x: torch.Tensor, At: torch.Tensor, Bt
     Bt [adapters, N, rank] in fp16 or fp32; y (or None: zero) and out [M, N]
     float32, out may be y; index [M], ranks [adapters] (the columns in use)
     int32, scales [adapters] float32."""
-    dev = _device(x)
+    dev = x.get_device()
     L, R, K = At.shape
     M = x.shape[0]
     N = Bt.shape[1]
     dt = x.dtype
-    ldx = _rows(x, "x", dev, M, K)
+    ldx = _rows(x, "x", dev, (M, K))
     at = _whole(At, "At", dev, dt, (L, R, K))
     bt = _whole(Bt, "Bt", dev, dt, (L, N, R))
     ix = _whole(index, "index", dev, torch.int32, (M,))
@@ -174,21 +173,20 @@ def adapter_add(y: Optional[torch.Tensor], x: torch.Tensor, At: torch.Tensor, Bt
     if y is not None:
         if y.dtype is not torch.float32:
             raise TypeError(f"y must be float32, not {y.dtype}")
-        yp, ldy = y.data_ptr(), _rows(y, "y", dev, M, N)
+        yp, ldy = y.data_ptr(), _rows(y, "y", dev, (M, N))
     ldo = N
     if out is None:
-        out = x.new_empty((M, N), dtype=torch.float32)
+        out = x.new_empty((M, N), dtype=torch.float32) if ldy != N or y is None else torch.empty_like(y)
     else:
         if out.dtype is not torch.float32:
             raise TypeError(f"out must be float32, not {out.dtype}")
-        ldo = _rows(out, "out", dev, M, N)
+        ldo = _rows(out, "out", dev, (M, N))
     if workspace is None:
         workspace = index.new_empty((adapter_workspace_size(M, K, R) + 3) // 4)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the device of the others")
-    _launch("w4a4_adapter_add_packed", dev, _ADAPTER, x.data_ptr(), _dt(x), ldx, at, bt, L, R, ix,
-            rk, sc, M, N, K, yp, ldy, out.data_ptr(), ldo, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    _adapter_add(dev, x.data_ptr(), _dt(x), ldx, at, bt, L, R, ix, rk, sc, M, N, K, yp, ldy,
+                 out.data_ptr(), ldo, workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -213,45 +211,44 @@ def norm_residual(h: Optional[torch.Tensor], y: Optional[torch.Tensor] = None, *
     ref = h if h is not None else y
     if ref is None:
         raise ValueError("h or y must be given")
-    dev = _device(ref)
-    M, C = ref.shape
+    dev, dt = ref.get_device(), ref.dtype
+    shape = M, C = ref.shape
     post, pre = _NORMS.get(post_norm), _NORMS.get(pre_norm)
     if post is None or pre is None:
         raise ValueError('norms are "none", "rms" or "layer"')
     hp, hd, ldh = 0, _dt(ref), C
     if h is not None:
-        hp, ldh = h.data_ptr(), _rows(h, "h", dev, M, C)
+        hp, ldh = h.data_ptr(), _rows(h, "h", dev, shape)
     yp, yd, ldy = 0, _w.F32, C
     if y is not None:
-        yp, yd, ldy = y.data_ptr(), _dt(y), _rows(y, "y", dev, M, C)
-    one = next((t for t in (post_weight, post_bias, pre_weight, pre_bias) if t is not None), None)
-    pd, pdt = (_w.F32, None) if one is None else (_DT.get(one.dtype, -1), one.dtype)
-    pw = 0 if post_weight is None else _whole(post_weight, "post_weight", dev, pdt, (C,))
-    pb = 0 if post_bias is None else _whole(post_bias, "post_bias", dev, pdt, (C,))
-    qw = 0 if pre_weight is None else _whole(pre_weight, "pre_weight", dev, pdt, (C,))
-    qb = 0 if pre_bias is None else _whole(pre_bias, "pre_bias", dev, pdt, (C,))
+        yp, yd, ldy = y.data_ptr(), _dt(y), _rows(y, "y", dev, shape)
+    pdt, p = None, [0, 0, 0, 0]
+    for i, t in enumerate((post_weight, post_bias, pre_weight, pre_bias)):
+        if t is not None:
+            pdt = pdt or t.dtype
+            p[i] = _whole(t, _PARAMS[i], dev, pdt, (C,))
     gp, gd, ldg = 0, _w.F32, C
     if gate is not None:
         if gate_rows < 1:
             raise ValueError("gate_rows must be positive")
-        gp, gd, ldg = gate.data_ptr(), _dt(gate), _rows(gate, "gate", dev, -(-M // gate_rows), C)
+        gp, gd, ldg = gate.data_ptr(), _dt(gate), _rows(gate, "gate", dev, (-(-M // gate_rows), C))
     op, ldho = 0, C
     if h_out is not None:
-        if h_out.dtype is not ref.dtype:
+        if h_out.dtype is not dt:
             raise TypeError("h_out must have h's dtype (y's without h)")
-        op, ldho = h_out.data_ptr(), _rows(h_out, "h_out", dev, M, C)
+        op, ldho = h_out.data_ptr(), _rows(h_out, "h_out", dev, shape)
     elif want_h or (want_h is None and y is not None):
-        h_out = ref.new_empty((M, C))
+        h_out = ref.new_empty(shape)
         op = h_out.data_ptr()
     xp, xd, ldx = 0, _w.F32, C
     if x_out is not None:
-        xp, xd, ldx = x_out.data_ptr(), _dt(x_out), _rows(x_out, "x_out", dev, M, C)
+        xp, xd, ldx = x_out.data_ptr(), _dt(x_out), _rows(x_out, "x_out", dev, shape)
     elif x_dtype is not None:
-        x_out = ref.new_empty((M, C), dtype=x_dtype)
+        x_out = ref.new_empty(shape, dtype=x_dtype)
         xp, xd = x_out.data_ptr(), _dt(x_out)
-    _launch("w4a4_norm_residual_packed", dev, _NORM, hp, hd, ldh, yp, yd, ldy, post, pw, pb, gp, gd,
-            ldg, gate_rows, residual_scale, pre, qw, qb, pd, weight_offset, eps, M, C, op, ldho, xp,
-            xd, ldx)
+    _norm_residual(dev, hp, hd, ldh, yp, yd, ldy, post, p[0], p[1], gp, gd, ldg, gate_rows,
+                   residual_scale, pre, p[2], p[3], _DT.get(pdt, _w.F32 if pdt is None else -1),
+                   weight_offset, eps, M, C, op, ldho, xp, xd, ldx)
     return h_out, x_out
 
 
@@ -265,19 +262,19 @@ def gated_activation(gate: torch.Tensor, up: Optional[torch.Tensor], act: str = 
     a = _ACTS.get(act)
     if a is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    dev = _device(gate)
-    M, F = gate.shape
-    ldg = _rows(gate, "gate", dev, M, F)
+    dev = gate.get_device()
+    shape = M, F = gate.shape
+    ldg = _rows(gate, "gate", dev, shape)
     up_ptr, ldu = 0, F
     if up is not None:
-        up_ptr, ldu = up.data_ptr(), _rows(up, "up", dev, M, F)
+        up_ptr, ldu = up.data_ptr(), _rows(up, "up", dev, shape)
         if up.dtype is not gate.dtype:
             raise TypeError("gate and up must have one dtype")
     ldo = F
     if out is None:
-        out = gate.new_empty((M, F), dtype=out_dtype)
+        out = gate.new_empty(shape, dtype=out_dtype)
     else:
-        ldo = _rows(out, "out", dev, M, F)
-    _launch("w4a4_gated_activation_packed", dev, _GATED, gate.data_ptr(), ldg, up_ptr, ldu,
-            _dt(gate), a, M, F, out.data_ptr(), ldo, _dt(out))
+        ldo = _rows(out, "out", dev, shape)
+    _gated_activation(dev, gate.data_ptr(), ldg, up_ptr, ldu, _dt(gate), a, M, F, out.data_ptr(),
+                      ldo, _dt(out))
     return out

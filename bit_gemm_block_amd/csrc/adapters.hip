@@ -789,13 +789,16 @@ void launch_rank(const AdapterArgs& a, hipStream_t st) {
                      dim3(256), 0, st, a);
 }
 
-// RUN and NW: bytes of a row in a stage, and waves, such that two or three
-// workgroups (rank 64 and below) share a compute unit's LDS.
+// RUN and NW: bytes of a row in a stage, and waves.  Up to rank 32 three stages
+// leave room for a second workgroup on a compute unit; where there is no second
+// one (few tiles), the double run halves the stages' latencies (512 rows,
+// K = 14336, rank 16: 25.0 -> 20.9 us; 4096 rows, rank 32: 74.8 -> 78.1 us).
 template <typename T>
 hipError_t launch_typed(const AdapterArgs& a, hipStream_t st) {
-  if (a.R <= 16) launch_rank<T, 16, 512, 8>(a, st);
-  else if (a.R <= 32) launch_rank<T, 32, 512, 8>(a, st);
-  else if (a.R <= 64) launch_rank<T, 64, 256, 4>(a, st);
+  const bool alone = a.M <= 16 * 128;
+  if (a.R <= 16) alone ? launch_rank<T, 16, 1024, 8>(a, st) : launch_rank<T, 16, 512, 8>(a, st);
+  else if (a.R <= 32) alone ? launch_rank<T, 32, 1024, 8>(a, st) : launch_rank<T, 32, 512, 8>(a, st);
+  else if (a.R <= 64) launch_rank<T, 64, 512, 8>(a, st);
   else if (a.R <= 128) launch_rank<T, 128, 256, 4>(a, st);
   else launch_rank<T, 256, 128, 2>(a, st);
   return hipGetLastError();
