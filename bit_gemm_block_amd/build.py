@@ -1,4 +1,6 @@
-"""Builds libw4a4.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Builds libw4a4.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and
+_block.so, the Python binding of its operators beside the layer (host code
+against torch's headers).
 
     python -m bit_gemm_block_amd.build
 """
@@ -16,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a4.so")
+BINDING = os.path.join(PKG, "_block.so")
 
 SOURCES = ["api.cpp", "rotq.hip", "rotq_mfma.hip", "qgemm.hip", "qgemm_f6.hip", "lowrank.hip", "offq.hip",
            "noalloc.hip", "block_api.cpp", "adapters.hip", "norm_residual.hip", "gated.hip"]
@@ -47,19 +50,51 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _binding() -> str:
+    """Object file of the binding."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD_DIR, "block_binding.cpp.o")
+    rocm = os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE]
+    for i in cpp_extension.include_paths() + [sysconfig.get_paths()["include"], rocm]:
+        cmd += ["-isystem", i]
+    cmd += ["-c", os.path.join(CSRC, "block_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiler failed for block_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link(out: str, args: list[str]) -> None:
+    tmp = out + ".tmp"
+    cmd = [hipcc(), "-shared", "-fPIC", "-o", tmp] + args
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
+def link_binding(obj: str) -> None:
+    """_block.so beside libw4a4.so, which it calls."""
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _link(BINDING, [obj, "-L", PKG, "-l:libw4a4.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+                    "-ltorch_cpu", "-lc10", "-lc10_hip"])
+
+
 def build(extra: list[str] | None = None, save_temps: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra or [])
     if save_temps:
         extra += ["-save-temps=obj"]
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        _link(LIB, ["--offload-arch=gfx950"] + objs)
+        link_binding(binding.result())
     return LIB
 
 

@@ -5,7 +5,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstring>
 
 #include "block_internal.h"
 #include "w4a4_internal.h"
@@ -21,18 +20,6 @@ uintptr_t esize(int dtype) { return dtype == W4A4_F16 ? 2 : 4; }
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int status(hipError_t e) { return e == hipSuccess ? W4A4_OK : w4a4::hip_status(e); }
-
-// Words of a packed argument list.
-template <typename T = void>
-T* ptr(int64_t v) {
-  return reinterpret_cast<T*>(static_cast<uintptr_t>(v));
-}
-int as_int(int64_t v) { return v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int>(v); }
-float as_float(int64_t v) {
-  double d;
-  std::memcpy(&d, &v, sizeof d);
-  return static_cast<float>(d);
-}
 
 }  // namespace
 
@@ -138,30 +125,6 @@ int w4a4_gated_activation(const void* gate, int64_t ldg, const void* up, int64_t
   w4a4::GatedArgs a{gate, ldg, up, ldu, out, ldo, M, F};
   return status(w4a4::launch_gated_activation(a, in_dtype == W4A4_F16, out_dtype == W4A4_F16, act,
                                               static_cast<hipStream_t>(stream)));
-}
-
-// The Python binding's form of the calls above: their arguments one after
-// another, every integer and pointer as an 8-byte word, every float as a
-// double.  (ctypes converts 20 to 28 separate arguments in 1.7 to 2.3 us of
-// host time, one packed buffer in 0.5 us.)
-int w4a4_adapter_add_packed(const int64_t* v) {
-  return w4a4_adapter_add(ptr(v[0]), as_int(v[1]), v[2], ptr(v[3]), ptr(v[4]), v[5], v[6],
-                          ptr<int32_t>(v[7]), ptr<int32_t>(v[8]), ptr<float>(v[9]), v[10], v[11],
-                          v[12], ptr<float>(v[13]), v[14], ptr<float>(v[15]), v[16], ptr(v[17]),
-                          static_cast<size_t>(v[18]), ptr(v[19]));
-}
-
-int w4a4_norm_residual_packed(const int64_t* v) {
-  return w4a4_norm_residual(ptr(v[0]), as_int(v[1]), v[2], ptr(v[3]), as_int(v[4]), v[5],
-                            as_int(v[6]), ptr(v[7]), ptr(v[8]), ptr(v[9]), as_int(v[10]), v[11],
-                            v[12], as_float(v[13]), as_int(v[14]), ptr(v[15]), ptr(v[16]),
-                            as_int(v[17]), as_float(v[18]), as_float(v[19]), v[20], v[21],
-                            ptr(v[22]), v[23], ptr(v[24]), as_int(v[25]), v[26], ptr(v[27]));
-}
-
-int w4a4_gated_activation_packed(const int64_t* v) {
-  return w4a4_gated_activation(ptr(v[0]), v[1], ptr(v[2]), v[3], as_int(v[4]), as_int(v[5]), v[6],
-                               v[7], ptr(v[8]), v[9], as_int(v[10]), ptr(v[11]));
 }
 
 }  // extern "C"
