@@ -47,6 +47,11 @@ struct Frag<float> {
 // Rows from which a call is taken as one of prompts: x . A staged, the rows'
 // products on the matrix instruction.
 constexpr int64_t kManyRows = 128;
+// Rows from which two tiles of 16 share the factors' stages: with a tile for
+// about every compute unit, half as many wide ones move fewer bytes through each
+// (x . A of 4096 rows, K = 14336, rank 64: 65.5 -> 51.3 us, rank 32: 40.5 ->
+// 37.8 us; 2048 rows, rank 32: 16.7 -> 21.4 us).
+constexpr int64_t kWideTileRows = 2816;
 // Workgroups up to which a tile's adapters are shared out among several of them
 // (tiles of one adapter leave the others with nothing to do).
 constexpr unsigned kShareStages = 1024;
@@ -54,17 +59,17 @@ constexpr int64_t kShareWorkgroups = 2048;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The first row of a workgroup's tile.  Consecutive workgroups go to the eight
+// The first row of a workgroup's tile of `rows`.  Consecutive workgroups go to the eight
 // XCDs in turn (grid.x is a multiple of eight); each XCD takes a contiguous
 // eighth of the tiles, so that its L2 holds the factors of the few requests there.
 // The grid's padding falls past the last row.
-__device__ __forceinline__ int64_t tile_row() {
-  return (static_cast<int64_t>(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) * 16;
+__device__ __forceinline__ int64_t tile_row(int rows) {
+  return (static_cast<int64_t>(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) * rows;
 }
 
-// The adapter of row m0 + (lane & 15), -1 where there is none.
-__device__ __forceinline__ int row_adapter(const AdapterArgs& a, int64_t m0, int lane) {
-  const int64_t m = m0 + (lane & 15);
+// The adapter of row m0 + lane % rows, -1 where there is none.
+__device__ __forceinline__ int row_adapter(const AdapterArgs& a, int64_t m0, int lane, int rows = 16) {
+  const int64_t m = m0 + (lane & (rows - 1));
   const int v = a.index[m < a.M ? m : a.M - 1];
   return m < a.M && v >= 0 && v < a.L ? v : -1;
 }
@@ -238,19 +243,18 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 }
 
 // ---- t = x . At^T: many rows, one adapter for most tiles ------------------------
-// A workgroup owns 16 rows and all (up to 16 NT) ranks of an adapter in them,
-// and streams K through LDS: stage s holds RUN bytes of each of the
-// 16 rows of x and the 16 NT rows of At, every row one contiguous run that
-// direct-to-LDS copies bring in (register loads of the matrix operands read 16
+// A workgroup owns 16 RT rows and all (up to 16 NT) ranks of an adapter in them,
+// and streams K through LDS: stage s holds RUN bytes of each of the 16 RT rows of
+// x and the 16 NT rows of At, every row one contiguous run that direct-to-LDS copies bring in (register loads of the matrix operands read 16
 // rows x 64 bytes per instruction, which the caches serve at a fraction of the
 // rate).  Three stages are in flight.  A row's 16-byte units are stored in the
 // order u ^ (row & 15), chosen by the copies' addresses, so that the reads of
 // one unit of 16 rows fall in distinct banks.
-template <typename T, int NT, int RUN, int NW>
+template <typename T, int RT, int NT, int RUN, int NW>
 __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
-  constexpr int ROWS = 16 + 16 * NT;
+  constexpr int XR = 16 * RT, ROWS = XR + 16 * NT;
   constexpr int UNITS = RUN / 16;          // 16-byte units of a row in a stage
   constexpr int SW = UNITS < 16 ? UNITS - 1 : 15;
   constexpr int RPC = 1024 / RUN;          // rows of one copy
@@ -265,18 +269,19 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = tile_row();
+  const int64_t m0 = tile_row(XR);
   if (m0 >= a.M) return;
   const int bytes = a.K * static_cast<int>(sizeof(T));
   const int nst = (bytes + RUN - 1) / RUN;
-  const int my = row_adapter(a, m0, lane);
+  const int my = row_adapter(a, m0, lane, XR);
   const Ranks ranks(a, lane);
-  unsigned rest = static_cast<unsigned>(__ballot(my >= 0)) & 0xffffu;
+  constexpr unsigned ALL = static_cast<unsigned>((uint64_t{1} << XR) - 1);
+  unsigned rest = static_cast<unsigned>(__ballot(my >= 0)) & ALL;
   // Pass p of the tile's adapters runs in workgroup p mod grid.z.
   for (unsigned pass = 0; rest != 0; ++pass) {
     const int ad = __builtin_amdgcn_readlane(my, __builtin_ctz(rest));
-    const bool mine = my == ad;
-    rest &= ~static_cast<unsigned>(__ballot(mine));
+    const unsigned same = static_cast<unsigned>(__ballot(my == ad)) & ALL;
+    rest &= ~same;
     if (pass % gridDim.z != blockIdx.z) continue;
     const int rank = ranks(a, ad);
     if (rank == 0) continue;
@@ -289,11 +294,11 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
       const int row = RPC * (wave + NW * q) + lane / UNITS;
       off[q] = 16 * ((lane % UNITS) ^ (row & SW));
       const T* p;
-      if (row < 16) {
+      if (row < XR) {
         const int64_t m = m0 + row < a.M ? m0 + row : a.M - 1;
         p = static_cast<const T*>(a.x) + m * a.ldx;
       } else {
-        const int j = row - 16 < rank ? row - 16 : rank - 1;
+        const int j = row - XR < rank ? row - XR : rank - 1;
         p = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K;
       }
       src[q] = reinterpret_cast<const uint8_t*>(p);
@@ -305,9 +310,11 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
       for (int q = 0; q < CPW; ++q)
         dma16(src[q] + s * RUN + (off[q] < left ? off[q] : 0), b + 1024 * (wave + NW * q));
     };
-    f32x4 acc[NT];
+    f32x4 acc[RT][NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const uint8_t* buf, int s) {
       const int valid = (bytes - s * RUN) / 64;
 #pragma unroll
@@ -315,12 +322,15 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
         const int ch = u * NW + wave;
         if (ch >= CHUNKS || ch >= valid) break;
         const int at = r * RUN + 16 * ((4 * ch + g) ^ (r & SW));  // row & SW is r & SW for every block of 16
-        const V xv = *reinterpret_cast<const V*>(buf + at);
-        V av[NT];
+        V xv[RT], av[NT];
 #pragma unroll
-        for (int c = 0; c < NT; ++c) av[c] = *reinterpret_cast<const V*>(buf + (16 + 16 * c) * RUN + at);
+        for (int t = 0; t < RT; ++t) xv[t] = *reinterpret_cast<const V*>(buf + 16 * t * RUN + at);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) acc[c] = F::mma(av[c], xv, acc[c]);
+        for (int c = 0; c < NT; ++c) av[c] = *reinterpret_cast<const V*>(buf + (XR + 16 * c) * RUN + at);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int c = 0; c < NT; ++c) acc[t][c] = F::mma(av[c], xv[t], acc[t][c]);
       }
     };
     // Stage s: once it has landed and the barrier has retired every wave's
@@ -343,69 +353,74 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
       if (s0 + 2 < nst) iterate(s0 + 2, 2);
     }
 
-    // The waves' sums, over the first stage's buffer.
-    static_assert(NW * NT * 1024 <= ROWS * RUN, "sums fit a stage");
-    f32x4 (*red)[NT][64] = reinterpret_cast<f32x4 (*)[NT][64]>(st0);
-    __syncthreads();  // every wave's last reads of the stages
+    // The waves' sums, over the first stage's buffer, 16 rows at a time.
 #pragma unroll
-    for (int c = 0; c < NT; ++c) red[wave][c][lane] = acc[c];
-    __syncthreads();
-    // Lane 16 g + r: ranks 16 c + 4 g + i of row r, scaled, zero past the rank.
-    const float scale = a.scales ? a.scales[ad] : 1.f;
-    f32x4 (*joined)[64] = reinterpret_cast<f32x4 (*)[64]>(st1);
-    for (int c = wave; c < NT; c += NW) {
-      f32x4 sum = red[0][c][lane];
+    for (int t = 0; t < RT; ++t) {
+      static_assert(NW * NT * 1024 <= ROWS * RUN, "sums fit a stage");
+      f32x4 (*red)[NT][64] = reinterpret_cast<f32x4 (*)[NT][64]>(st0);
+      __syncthreads();  // every wave's last reads of the stages
 #pragma unroll
-      for (int w = 1; w < NW; ++w) sum += red[w][c][lane];
+      for (int c = 0; c < NT; ++c) red[wave][c][lane] = acc[t][c];
+      __syncthreads();
+      // Lane 16 g + r: ranks 16 c + 4 g + i of row 16 t + r, scaled, zero past the rank.
+      const bool mine = same >> (16 * t + r) & 1;
+      const int64_t m = m0 + 16 * t + r;
+      const float scale = a.scales ? a.scales[ad] : 1.f;
+      f32x4 (*joined)[64] = reinterpret_cast<f32x4 (*)[64]>(st1);
+      for (int c = wave; c < NT; c += NW) {
+        f32x4 sum = red[0][c][lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] = 16 * c + 4 * g + i < rank ? sum[i] * scale : 0.f;
-      joined[c][lane] = sum;
-    }
-    __syncthreads();
-    const int64_t ts = adapter_tstride(a.R);
-    if constexpr (sizeof(T) == 2) {
-      // t as fp16 pair, hi + lo: the row's largest finite |t| is moved to
-      // [2^13, 2^14), so that the pair holds about 22 bits whatever its size.
-      float big = 0.f;
+        for (int w = 1; w < NW; ++w) sum += red[w][c][lane];
 #pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = fabsf(joined[c][lane][i]);
-          big = fmaxf(big, v < INFINITY ? v : 0.f);
-        }
-      big = fmaxf(big, __shfl_xor(big, 16));
-      big = fmaxf(big, __shfl_xor(big, 32));
-      int e = 0;
-      if (big > 0.f) {
-        (void)frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
-        e = 14 - e;
-        e = e > 120 ? 120 : e;
+        for (int i = 0; i < 4; ++i) sum[i] = 16 * c + 4 * g + i < rank ? sum[i] * scale : 0.f;
+        joined[c][lane] = sum;
       }
-      _Float16* hi = reinterpret_cast<_Float16*>(a.t) + (m0 + r) * ts + 4 * g;
-      for (int c = wave; 16 * c < ts; c += NW) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (c < NT) v = joined[c][lane];
-        half4 h, l;
+      __syncthreads();
+      const int64_t ts = adapter_tstride(a.R);
+      if constexpr (sizeof(T) == 2) {
+        // t as fp16 pair, hi + lo: the row's largest finite |t| is moved to
+        // [2^13, 2^14), so that the pair holds about 22 bits whatever its size.
+        float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = ldexpf(v[i], e);
-          h[i] = static_cast<_Float16>(u);
-          const float d = u - static_cast<float>(h[i]);
-          l[i] = static_cast<_Float16>(fabsf(u) < INFINITY ? d : 0.f);
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = fabsf(joined[c][lane][i]);
+            big = fmaxf(big, v < INFINITY ? v : 0.f);
+          }
+        big = fmaxf(big, __shfl_xor(big, 16));
+        big = fmaxf(big, __shfl_xor(big, 32));
+        int e = 0;
+        if (big > 0.f) {
+          (void)frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
+          e = 14 - e;
+          e = e > 120 ? 120 : e;
         }
-        if (mine) {
-          *reinterpret_cast<half4*>(hi + 16 * c) = h;
-          *reinterpret_cast<half4*>(hi + a.M * ts + 16 * c) = l;
+        _Float16* hi = reinterpret_cast<_Float16*>(a.t) + m * ts + 4 * g;
+        for (int c = wave; 16 * c < ts; c += NW) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+          if (c < NT) v = joined[c][lane];
+          half4 h, l;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u = ldexpf(v[i], e);
+            h[i] = static_cast<_Float16>(u);
+            const float d = u - static_cast<float>(h[i]);
+            l[i] = static_cast<_Float16>(fabsf(u) < INFINITY ? d : 0.f);
+          }
+          if (mine) {
+            *reinterpret_cast<half4*>(hi + 16 * c) = h;
+            *reinterpret_cast<half4*>(hi + a.M * ts + 16 * c) = l;
+          }
         }
-      }
-      if (mine && wave == 0 && g == 0) a.t[a.M * ts + m0 + r] = ldexpf(1.f, -e);
-    } else {
-      float* tp = a.t + (m0 + r) * ts + 4 * g;
-      for (int c = wave; 16 * c < ts; c += NW) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (c < NT) v = joined[c][lane];
-        if (mine) *reinterpret_cast<f32x4*>(tp + 16 * c) = v;
+        if (mine && wave == 0 && g == 0) a.t[a.M * ts + m] = ldexpf(1.f, -e);
+      } else {
+        float* tp = a.t + m * ts + 4 * g;
+        for (int c = wave; 16 * c < ts; c += NW) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+          if (c < NT) v = joined[c][lane];
+          if (mine) *reinterpret_cast<f32x4*>(tp + 16 * c) = v;
+        }
       }
     }
     __syncthreads();  // the sums are read before the next adapter's stages
@@ -655,7 +670,7 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = tile_row();
+  const int64_t m0 = tile_row(16);
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 256 + 64 * wave;
   if (m0 >= a.M || n0 >= a.N) return;
   const int64_t n = n0 + 4 * r;
@@ -763,14 +778,27 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   }
 }
 
+template <typename T, int RT, int NT, int RUN, int NW>
+void launch_stage(const AdapterArgs& a, hipStream_t st) {
+  const unsigned gx = static_cast<unsigned>(((a.M + 16 * RT - 1) / (16 * RT) + 7) / 8 * 8);
+  const unsigned share = kShareStages / gx;
+  hipLaunchKernelGGL((shrink_stage_kernel<T, RT, NT, RUN, NW>),
+                     dim3(gx, 1, share < 2 ? 2 : share > 16 ? 16 : share), dim3(64 * NW), 0, st, a);
+}
+
 template <typename T, int RC, int RUN, int NW>
 void launch_rank(const AdapterArgs& a, hipStream_t st) {
   const unsigned tiles = static_cast<unsigned>((a.M + 15) / 16);
   if (a.M >= kManyRows) {
+    if constexpr (RC == 32 || RC == 64) {
+      if (a.M >= kWideTileRows)
+        launch_stage<T, 2, RC / 16, 512, 8>(a, st);
+      else
+        launch_stage<T, 1, RC / 16, RUN, NW>(a, st);
+    } else {
+      launch_stage<T, 1, RC / 16, RUN, NW>(a, st);
+    }
     const unsigned gx = (tiles + 7) / 8 * 8;
-    const unsigned stages = kShareStages / gx;
-    hipLaunchKernelGGL((shrink_stage_kernel<T, RC / 16, RUN, NW>),
-                       dim3(gx, 1, stages < 2 ? 2 : stages > 16 ? 16 : stages), dim3(64 * NW), 0, st, a);
     const unsigned gy = static_cast<unsigned>((a.N + 255) / 256);
     const int64_t share = kShareWorkgroups / (static_cast<int64_t>(gx) * gy);
     if (share <= 1)

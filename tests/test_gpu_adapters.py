@@ -56,6 +56,9 @@ SHAPES = [  # M, K, N, adapters, rank, dtype, order
     (257, 576, 515, 6, 48, "f16", "runs"), (1009, 128, 70, 4, 16, "f16", "mixed"),
     (1040, 640, 260, 5, 72, "f16", "runs"), (2100, 192, 129, 3, 8, "f32", "runs"),
     (1500, 1024, 516, 6, 32, "f16", "runs"), (2049, 64, 33, 2, 200, "f16", "mixed"),
+    (2900, 320, 70, 3, 32, "f16", "runs"), (2833, 192, 65, 5, 40, "f16", "mixed"),
+    (2848, 64, 33, 2, 24, "f32", "runs"), (3001, 128, 40, 4, 64, "f32", "mixed"),
+    (130, 2112, 36, 2, 128, "f16", "runs"), (128, 64, 300, 40, 16, "f32", "mixed"),
 ]
 
 
