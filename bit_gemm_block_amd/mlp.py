@@ -163,7 +163,7 @@ def main() -> None:
     a = ap.parse_args()
     mlp, w = random_block(a.hidden, a.ffn, a.adapters, a.rank, w_layout=a.layout)
     h = torch.randn((a.tokens, a.hidden), device="cuda")
-    index = (torch.arange(a.tokens) % (a.adapters + 1) - 1).int().cuda()
+    index = (torch.arange(a.tokens) * (a.adapters + 1) // a.tokens - 1).int().cuda()
     x = mlp.enter(h, mlp.pre_weight)
     buf, out = mlp.buffers(a.tokens), torch.empty_like(h)
     got, x_next = mlp(h, x, index, buf, out)
