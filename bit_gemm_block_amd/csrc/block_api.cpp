@@ -13,6 +13,10 @@ namespace {
 
 constexpr int64_t kMaxK = 16384;
 constexpr int64_t kMaxRank = 256;
+// The grids' limits: tiles of 16 rows along x, 512 threads each, below 2^32
+// threads; 256 columns a workgroup along y, 65535 of them.
+constexpr int64_t kMaxM = int64_t{8388600} * 16;
+constexpr int64_t kMaxN = 65535 * 256;
 constexpr int64_t kMaxC = 16384;
 
 bool dtype_ok(int d) { return d == W4A4_F32 || d == W4A4_F16; }
@@ -41,7 +45,7 @@ int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, co
       ldo < N || (y && ldy < N))
     return W4A4_ERR_INVALID_ARG;
   if (K % 64 != 0 || K > kMaxK || rank > kMaxRank || (x_dtype == W4A4_F16 && rank % 8 != 0) ||
-      adapters > INT32_MAX)
+      adapters > INT32_MAX || M > kMaxM || N > kMaxN)
     return W4A4_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return W4A4_OK;
   if (!x || !index || !out || !workspace || (adapters > 0 && (!At || !Bt)))

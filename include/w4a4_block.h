@@ -43,7 +43,8 @@ size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank);
  *   x       [M, K] in x_dtype; rows aligned to 16 bytes (x and ldx).
  *           K a positive multiple of 64, at most 16384, as in the layer.
  *   At      [adapters, rank, K], Bt [adapters, N, rank] in x_dtype; rank in
- *           [1, 256], for fp16 a multiple of 8 (the layer's own limits).
+ *           [1, 256], for fp16 a multiple of 8 (the layer's own limits);
+ *           M at most 134217600, N at most 16776960.
  *   index   [M] int32 in device memory, any order; a value outside
  *           [0, adapters) means no adapter.
  *   ranks   [adapters] int32, or NULL (all `rank`).  Values are clamped to
@@ -52,9 +53,13 @@ size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank);
  *   scales  [adapters] float32, or NULL (all 1).
  *   y       [M, N] float32, or NULL (zero).  out [M, N] float32; out may
  *           equal y when ldo equals ldy.
- *   t and both sums are float32 (t is not rounded to the factors' type).  A
- *   row's result depends on its own inputs only (not on the other rows'
- *   values) and is the same from call to call.
+ *   Both sums are float32 and t is not rounded to the factors' type: it stays
+ *   float32, except that with 128 rows or more and fp16 factors the second
+ *   product takes scales[a] t as a pair of fp16 values, hi + lo, under one power
+ *   of two per row (the row's largest |t| keeps 22 bits, the others an absolute
+ *   error of 2^-23 of it or less).  A row's result depends on its own inputs
+ *   only (not on the other rows' values; M and index choose the order of its
+ *   sums) and is the same from call to call.
  *   workspace: at least w4a4_adapter_workspace_size(M, K, rank) bytes.
  */
 int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, const void* Bt,

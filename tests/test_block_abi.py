@@ -59,6 +59,18 @@ def test_adapter_add_argument_errors(lib):
     assert f(*changed(ok, _11=0)) == W.OK
 
 
+def test_adapter_add_grid_limits(lib):
+    f = lib.w4a4_adapter_add
+    # The first sizes whose grids could not be launched; the limits themselves
+    # pass this check and reach the next one (the workspace is too small).
+    ok = [P, W.F16, 64, P, P, 4, 16, P, P, P, 16, 32, 64, P, 32, P, 32, P, 0, None]
+    assert f(*changed(ok, _10=134217601)) == W.ERR_UNSUPPORTED
+    assert f(*changed(ok, _10=134217600)) == W.ERR_WORKSPACE
+    n = 16776960
+    assert f(*changed(ok, _11=n + 1, _14=n + 1, _16=n + 1)) == W.ERR_UNSUPPORTED
+    assert f(*changed(ok, _11=n, _14=n, _16=n)) == W.ERR_WORKSPACE
+
+
 def test_norm_residual_argument_errors(lib):
     f = lib.w4a4_norm_residual
     # h dt ldh y dt ldy post w b gate dt ldg rows rs pre w b pdt off eps M C hout ld xout dt ld st
