@@ -1,9 +1,10 @@
 // adapters.hip — low-rank adapters of many requests beside one projection:
 //   out[m] = y[m] + s_a (x[m] At[a]^T) Bt[a]^T,  a = index[m].
 //
-// Two launches: the first writes t = x At^T in S parts of K (float32, one
-// partial sum per part), the second joins the parts in order and adds
-// s_a t Bt^T to y.  No atomics: a row's result is the same from call to call.
+// Two launches: the first writes t = x At^T, the second adds s_a t Bt^T to y.
+// Sums over K that several workgroups share are written apart and joined in
+// order by the second launch.  No atomics: a row's result is the same from call
+// to call.
 //
 // Rows are taken in tiles of 16, the row count of the matrix instruction.  A
 // tile may hold rows of several adapters: every adapter in it is one pass, led
@@ -44,9 +45,16 @@ struct Frag<float> {
   }
 };
 
-// Rows from which a call is taken as one of prompts: x . A staged, the rows'
-// products on the matrix instruction.
-constexpr int64_t kManyRows = 128;
+// Bytes of a row of x from which a call of few rows takes K in kParts parts: of
+// every row (more workgroups for long rows: one row, K = 14336, rank 16: 7.8 ->
+// 6.9 us; 64 rows of mixed adapters 20.8 -> 15.2 us; K = 4096, rank 64: 18.0 ->
+// 23.5 us), and of groups of rows (whose slots have workgroups to spare: 100 rows
+// of four adapters, K = 4096, rank 32: 15.4 -> 10.0 us; K = 64: 10.3 -> 12.0 us).
+constexpr int kPartsBytes = 16384;
+constexpr int kGroupPartsBytes = 2048;
+// Rows of one adapter in a tile up to which they are multiplied one by one.
+constexpr int kRowByRow = 3;
+static_assert(kParts == kRowByRow + 1 && kPartsBytes >= kGroupPartsBytes, "a group has a row for every part");
 // Rows from which two tiles of 16 share the factors' stages: with a tile for
 // about every compute unit, half as many wide ones move fewer bytes through each
 // (x . A of 4096 rows, K = 14336, rank 64: 65.5 -> 51.3 us, rank 32: 40.5 ->
@@ -189,11 +197,10 @@ __device__ __forceinline__ f32x4 group_dot(const AdapterArgs& a, int64_t m0, uns
   return acc;
 }
 
-// Workgroup (eight ranks, tile, slot): slot s takes the rows of the adapter that
-// row s of the tile leads, a few of them one by one.  The waves share K; their
-// sums are joined in LDS.
+// Workgroup (eight ranks and part of K, tile, slot): slot s takes the rows of the
+// adapter that row s of the tile leads, a few of them one by one.  The waves share
+// the part; their sums are joined in LDS.
 constexpr int kRowsWaves = 8;
-constexpr int kRowByRow = 3;
 
 template <typename T>
 __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArgs a) {
@@ -201,43 +208,54 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
-  const int s = blockIdx.z, j0 = 8 * blockIdx.x;
+  const int s = blockIdx.z;
+  const int j0 = 8 * (a.parts > 1 ? blockIdx.x / kParts : blockIdx.x);
+  int p = a.parts > 1 ? blockIdx.x % kParts : 0;
   if (m0 + s >= a.M) return;
   const int my = row_adapter(a, m0, lane);
   const Ranks ranks(a, lane);
   const int ad = __builtin_amdgcn_readlane(my, s);
   if (ad < 0) return;
   unsigned rows = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
-  if (static_cast<int>(__builtin_ctz(rows)) != s) return;  // led by another row
+  const bool group = __builtin_popcount(rows) > kRowByRow;
+  const int before = __builtin_popcount(rows & ((1u << s) - 1));  // rows that lead row s
+  const int parts = group && a.K * sizeof(T) >= kGroupPartsBytes ? kParts : a.parts;
+  if (group && (j0 & 8)) return;  // groups take sixteen ranks at a time
+  if (parts > a.parts)
+    p = before;  // the parts of a group: its first rows' slots
+  else if (before != 0)
+    return;
+  if (p >= parts) return;
   const int rank = ranks(a, ad);
   if (j0 >= rank) return;
   const int64_t ts = adapter_tstride(a.R);
-  if (__builtin_popcount(rows) > kRowByRow) {
-    if (j0 & 8) return;  // sixteen ranks at a time
-    red[wave][lane] = group_dot<T>(a, m0, rows, ad, rank, j0, wave, kRowsWaves);
+  float* t = a.t + p * a.M * ts;
+  const int first = kRowsWaves * p + wave, step = kRowsWaves * parts;
+  if (group) {
+    red[wave][lane] = group_dot<T>(a, m0, rows, ad, rank, j0, first, step);
     __syncthreads();
     if (wave == 0) {
       f32x4 sum = red[0][lane];
 #pragma unroll
       for (int w = 1; w < kRowsWaves; ++w) sum += red[w][lane];
       if (rows >> (lane & 15) & 1)
-        *reinterpret_cast<f32x4*>(a.t + (m0 + (lane & 15)) * ts + j0 + 4 * (lane >> 4)) = sum;
+        *reinterpret_cast<f32x4*>(t + (m0 + (lane & 15)) * ts + j0 + 4 * (lane >> 4)) = sum;
     }
     return;
   }
-  float* part = reinterpret_cast<float*>(red);  // [kRowsWaves][kRowByRow][8]
+  float* sums = reinterpret_cast<float*>(red);  // [kRowsWaves][kRowByRow][8]
   if (__builtin_popcount(rows) == 1)
-    rows_dot<T, 1>(a, m0, rows, ad, rank, j0, wave, kRowsWaves, part + wave * 8 * kRowByRow);
+    rows_dot<T, 1>(a, m0, rows, ad, rank, j0, first, step, sums + wave * 8 * kRowByRow);
   else
-    rows_dot<T, kRowByRow>(a, m0, rows, ad, rank, j0, wave, kRowsWaves, part + wave * 8 * kRowByRow);
+    rows_dot<T, kRowByRow>(a, m0, rows, ad, rank, j0, first, step, sums + wave * 8 * kRowByRow);
   __syncthreads();
   const int j = threadIdx.x;
   for (int i = 0; rows != 0; ++i, rows &= rows - 1) {
     if (j < 8 && j0 + j < rank) {
-      float sum = part[8 * i + j];
+      float sum = sums[8 * i + j];
 #pragma unroll
-      for (int w = 1; w < kRowsWaves; ++w) sum += part[(w * kRowByRow + i) * 8 + j];
-      a.t[(m0 + __builtin_ctz(rows)) * ts + j0 + j] = sum;
+      for (int w = 1; w < kRowsWaves; ++w) sum += sums[(w * kRowByRow + i) * 8 + j];
+      t[(m0 + __builtin_ctz(rows)) * ts + j0 + j] = sum;
     }
   }
 }
@@ -556,6 +574,19 @@ struct RowProducts {
   }
 };
 
+// Four of a row's t, from `at` on: of the sum of kParts parts, or as it is.
+__device__ __forceinline__ f32x4 load_t(const AdapterArgs& a, const float* at, int64_t ts, bool parts) {
+  f32x4 t = *reinterpret_cast<const f32x4*>(at);
+  if (parts) {
+    f32x4 p[kParts - 1];
+#pragma unroll
+    for (int i = 0; i < kParts - 1; ++i) p[i] = *reinterpret_cast<const f32x4*>(at + (i + 1) * a.M * ts);
+#pragma unroll
+    for (int i = 0; i < kParts - 1; ++i) t += p[i];
+  }
+  return t;
+}
+
 // The same rows, 64 columns from n0, by one wave with the float32 matrix
 // instruction, t as it is (for groups of rows; about eight times the price of
 // the fp16 pair per product, which few rows do not notice).
@@ -568,6 +599,7 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int64_t n = n0 + 4 * r, ts = adapter_tstride(a.R);
+  const bool parts = a.K * sizeof(T) >= kGroupPartsBytes;
   f32x4 yv[4], d[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -594,7 +626,7 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
         }
       }
 #pragma unroll
-      for (int e = 0; e < PL / 4; ++e) w[e] = *reinterpret_cast<const f32x4*>(tp + at + 4 * e);
+      for (int e = 0; e < PL / 4; ++e) w[e] = load_t(a, tp + at + 4 * e, ts, parts);
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
         const float t = k + e < rank ? w[e / 4][e % 4] * scale : 0.f;  // past the rank: anything
@@ -613,8 +645,9 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
 }
 
 // Workgroup (4 x 512 / LPC columns, tile, slot): slot s takes the rows of the
-// adapter that row s of the tile leads, a few of them one by one.
-
+// adapter that row s of the tile leads, a few of them one by one.  Larger groups
+// share their columns, 256 at a time, among their rows' slots (100 rows of four
+// adapters, N = 6144, rank 16: 22.1 -> 14.5 us with K = 4096).
 template <typename T, int RC>
 __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
   constexpr int LPC = RC * static_cast<int>(sizeof(T)) / 16, COLS = 4 * 512 / LPC;
@@ -629,24 +662,27 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
   const int ad = __builtin_amdgcn_readlane(my, s);
   unsigned rows = static_cast<unsigned>(__ballot(my == ad)) & 0xffffu;
   if (a.M - m0 < 16) rows &= (1u << (a.M - m0)) - 1;
-  if (static_cast<int>(__builtin_ctz(rows)) != s) return;  // led by another row
-  if (ad < 0 && a.y == a.out) return;                      // in place, nothing to add
+  if (ad < 0 && a.y == a.out) return;  // in place, nothing to add
   const int rank = ad < 0 ? 0 : ranks(a, ad);
-  if (__builtin_popcount(rows) <= kRowByRow) {
+  const int count = __builtin_popcount(rows);
+  const int before = __builtin_popcount(rows & ((1u << s) - 1));  // rows that lead row s
+  if (count <= kRowByRow) {
+    if (before != 0) return;
     const int64_t n = n0 + wave * (COLS / 4);
     if (n >= a.N) return;
     RowProducts<T, LPC> p(a, ad, rank, n);
+    const int64_t ts = adapter_tstride(a.R);
     p.mask();
     for (; rows != 0; rows &= rows - 1) {
       const int64_t m = m0 + __builtin_ctz(rows);
       f32x4 t[p.PL / 4];
 #pragma unroll
       for (int e = 0; e < p.PL / 4; ++e)
-        t[e] = reinterpret_cast<const f32x4*>(a.t + m * adapter_tstride(a.R) + (p.j0 < a.R ? p.j0 : 0))[e];
+        t[e] = load_t(a, a.t + m * ts + (p.j0 < a.R ? p.j0 : 0) + 4 * e, ts, a.parts > 1);
       p.row(a, m, [&](int e) { return t[e / 4][e % 4]; });
     }
   } else {
-    for (int64_t n = n0 + 64 * wave; n < n0 + COLS && n < a.N; n += 256)
+    for (int64_t n = n0 + 256 * before + 64 * wave; n < n0 + COLS && n < a.N; n += 256 * count)
       group_pass<T, RC>(a, m0, rows, ad, rank, n);
   }
 }
@@ -810,7 +846,7 @@ void launch_rank(const AdapterArgs& a, hipStream_t st) {
   }
   constexpr int WAVE_COLS = 512 * 16 / (RC * static_cast<int>(sizeof(T)));
   const unsigned slots = static_cast<unsigned>(a.M < 16 ? a.M : 16);
-  hipLaunchKernelGGL((shrink_rows_kernel<T>), dim3(static_cast<unsigned>((a.R + 7) / 8), tiles, slots),
+  hipLaunchKernelGGL((shrink_rows_kernel<T>), dim3(static_cast<unsigned>((a.R + 7) / 8 * a.parts), tiles, slots),
                      dim3(64 * kRowsWaves), 0, st, a);
   constexpr int COLS = 4 * WAVE_COLS;
   hipLaunchKernelGGL((expand_rows_kernel<T, RC>), dim3(static_cast<unsigned>((a.N + COLS - 1) / COLS), tiles, slots),
@@ -835,7 +871,9 @@ hipError_t launch_typed(const AdapterArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st) {
-  return f16 ? launch_typed<_Float16>(a, st) : launch_typed<float>(a, st);
+  AdapterArgs b = a;
+  b.parts = a.M < kManyRows && a.K * (f16 ? 2 : 4) >= kPartsBytes ? kParts : 1;
+  return f16 ? launch_typed<_Float16>(b, st) : launch_typed<float>(b, st);
 }
 
 }  // namespace w4a4

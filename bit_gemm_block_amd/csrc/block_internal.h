@@ -23,12 +23,18 @@ struct AdapterArgs {
   int64_t ldy;
   float* out;
   int64_t ldo;
-  // x . A, [M, adapter_tstride(R)].  Few rows: float32, not scaled, defined up to
-  // the row's rank.  Many rows, fp32: scaled, zero past the rank; fp16: the same
+  // x . A, [M, adapter_tstride(R)].  Few rows: `parts` such matrices of float32 to
+  // be added up, not scaled, defined up to the row's rank.  Many rows, fp32: scaled, zero past the rank; fp16: the same
   // as fp16 pair (hi, then lo), times a power of two whose inverse follows, one
   // float32 per row.
   float* t;
+  int parts;
 };
+
+// Rows from which a call is taken as one of prompts.
+constexpr int64_t kManyRows = 128;
+// Parts of K of a call of few rows with long rows.
+constexpr int kParts = 4;
 
 // The row distance of t.
 __host__ __device__ inline int64_t adapter_tstride(int64_t R) { return (R + 31) / 32 * 32; }

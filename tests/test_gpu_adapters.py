@@ -305,3 +305,33 @@ def test_binding_refusals():
         B.adapter_add(good["y"], torch.zeros((M, K + 4), dtype=F16, device=DEV)[:, :K], good["At"],
                       good["Bt"], good["index"])
     assert e.value.status == W.ERR_MISALIGNED
+
+
+PARTS = [  # M, K, N, adapters, rank, dtype, order: few rows, K taken whole or in parts
+    (3, 8192, 70, 1, 8, "f16", "runs"), (4, 8128, 70, 1, 16, "f16", "runs"),
+    (4, 8192, 33, 1, 24, "f16", "runs"), (16, 16384, 1030, 2, 64, "f16", "runs"),
+    (16, 960, 2060, 1, 8, "f16", "runs"), (16, 1024, 2060, 1, 8, "f16", "runs"),
+    (31, 8192, 515, 40, 40, "f16", "mixed"), (100, 8256, 300, 4, 256, "f16", "runs"),
+    (127, 9664, 130, 3, 128, "f16", "mixed"), (4, 448, 5, 1, 3, "f32", "runs"),
+    (4, 512, 1100, 1, 12, "f32", "runs"), (19, 4032, 65, 2, 33, "f32", "runs"),
+    (19, 4096, 65, 5, 33, "f32", "mixed"), (127, 4160, 40, 3, 200, "f32", "runs"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,dt,order", PARTS)
+def test_few_rows_with_long_rows(M, K, N, L, R, dt, order):
+    print("adapters, parts of K", M, K, N, L, R, dt, order, flush=True)
+    c = case(M, K, N, L, R, dt, order, M + K + N + 2, True)
+    assert np.array_equal(host(B.adapter_add(*[dev(a) for a in c])), O.adapter_add(*c).astype(np.float32))
+    c = case(M, K, N, L, R, dt, order, M + K + N + 3, False)
+    ref, tol = bound(c)
+    ws = B.adapter_workspace(M, K, R, DEV)
+    ws.view(torch.float32).fill_(float("nan"))           # what no part writes is not read
+    got = host(B.adapter_add(*[dev(a) for a in c], workspace=ws))
+    assert np.all(np.abs(got - ref) <= tol), float(np.max(np.abs(got - ref) / tol))
+
+
+def test_a_workspace_for_more_rows_serves_fewer():
+    for R in (8, 24, 256):
+        sizes = [B.adapter_workspace_size(M, 16384, R) for M in (1, 3, 64, 127, 128, 400, 600, 4096)]
+        assert sizes == sorted(sizes)
