@@ -62,8 +62,24 @@ static_assert(kParts == kRowByRow + 1 && kPartsBytes >= kGroupPartsBytes, "a gro
 constexpr int64_t kWideTileRows = 2816;
 // Workgroups up to which a tile's adapters are shared out among several of them
 // (tiles of one adapter leave the others with nothing to do).
-constexpr unsigned kShareStages = 1024;
-constexpr int64_t kShareWorkgroups = 2048;
+constexpr unsigned kShareStages = 512;
+constexpr int64_t kShareWorkgroups = 1024;
+
+// P ranks of a row of Bt from rank k on (those past R: anything of the row).
+// fp32 rows of any length: whole loads need only an element's alignment.
+template <typename T, int P>
+__device__ __forceinline__ void load_ranks(const T* row, int k, int R, T __attribute__((ext_vector_type(P)))& b) {
+  typedef T V __attribute__((ext_vector_type(P)));
+  typedef V VU __attribute__((aligned(sizeof(T) == 2 ? sizeof(V) : 4)));
+  if constexpr (sizeof(T) == 2) {
+    b = *reinterpret_cast<const VU*>(row + (k < R ? k : 0));
+  } else if (k + P <= R) {
+    b = *reinterpret_cast<const VU*>(row + k);
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; ++e) b[e] = row[k + e < R ? k + e : 0];
+  }
+}
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -499,12 +515,7 @@ struct RowProducts {
       for (int i = 0; i < NI; ++i) {
         const int col = i * CPI + grp < most ? i * CPI + grp : most;
         const T* p = bb + col * a.R;
-        if (sizeof(T) == 2 || a.R % PL == 0) {
-          b[i] = *reinterpret_cast<const V*>(p + (j0 < a.R ? j0 : 0));
-        } else {
-#pragma unroll
-          for (int e = 0; e < PL; ++e) b[i][e] = p[j0 + e < a.R ? j0 + e : 0];
-        }
+        load_ranks<T, PL>(p, j0, a.R, b[i]);
       }
       if (a.scales) scale = a.scales[ad];
     }
@@ -618,12 +629,7 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const T* p = bb + (n + q < a.N ? n + q : a.N - 1) * a.R;
-        if (sizeof(T) == 2 || a.R % PL == 0) {
-          b[q] = *reinterpret_cast<const V*>(p + at);
-        } else {
-#pragma unroll
-          for (int e = 0; e < PL; ++e) b[q][e] = p[k + e < a.R ? k + e : 0];
-        }
+        load_ranks<T, PL>(p, k, a.R, b[q]);
       }
 #pragma unroll
       for (int e = 0; e < PL / 4; ++e) w[e] = load_t(a, tp + at + 4 * e, ts, parts);
@@ -703,6 +709,10 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   constexpr bool F16 = sizeof(T) == 2;
   constexpr bool BOTH = F16 && RC == 16;  // hi in ranks 0 .. 15 of an operand, lo in 16 .. 31
   constexpr int NC = BOTH ? 1 : RC / F::KC;
+  // A stage: RS ranks (UNITS units of 16 bytes, CS operands) of a wave's columns.
+  constexpr int ROW = RC * static_cast<int>(sizeof(T)), UNITS = ROW < 128 ? ROW / 16 : 8;
+  constexpr int RS = UNITS * 16 / static_cast<int>(sizeof(T)), CS = BOTH ? 1 : UNITS / 4;
+  __shared__ __attribute__((aligned(16))) uint8_t staged[4 * 64 * 16 * UNITS];
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -711,6 +721,7 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   if (m0 >= a.M || n0 >= a.N) return;
   const int64_t n = n0 + 4 * r;
   const int64_t ts = adapter_tstride(a.R);
+  const uint32_t own = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(staged)) + 1024 * UNITS * wave;
   // Bit r of `rows`: row r is written here; of `todo`: and has an adapter.
   unsigned rows = a.M - m0 >= 16 ? 0xffffu : (1u << (a.M - m0)) - 1;
 
@@ -772,22 +783,10 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
     f32x4 d[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int k = c * F::KC + j;
-      if (c * F::KC >= rank) break;
-      V b[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const T* p = bb + (n + q < a.N ? n + q : a.N - 1) * a.R;
-        if (F16 || a.R % F::FL == 0) {
-          b[q] = *reinterpret_cast<const V*>(p + (k < a.R ? k : 0));
-        } else {
-#pragma unroll
-          for (int e = 0; e < F::FL; ++e) b[q][e] = p[k + e < a.R ? k + e : 0];
-        }
-      }
-      if (c * F::KC + (BOTH ? 16 : F::KC) > rank) {  // past the rank: anything
+    // Chunk c's operands b: what lies past the rank may be anything.
+    auto multiply = [&](int c, V(&b)[4]) {
+      if (c * F::KC + (BOTH ? 16 : F::KC) > rank) {
+        const int k = c * F::KC + j;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -797,6 +796,42 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
       for (int q = 0; q < 4; ++q) {
         d[q] = F::mma(hi[c], b[q], d[q]);
         if constexpr (F16 && !BOTH) d[q] = F::mma(lo[c], b[q], d[q]);
+      }
+    };
+    if (F16 || a.R % F::FL == 0) {
+#pragma unroll
+      for (int h = 0; h < RC / RS; ++h) {
+        if (RS * h >= rank) break;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last reads of the stage have returned
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+          const int row = (64 * i + lane) / UNITS, u = (lane % UNITS) ^ (row & (UNITS - 1));
+          const int64_t col = n0 + 4 * (row & 15) + (row >> 4);
+          const int k = RS * h + F::FL * u;
+          dma16(reinterpret_cast<const uint8_t*>(bb + (col < a.N ? col : a.N - 1) * a.R + (k < a.R ? k : 0)), own + 1024 * i);
+        }
+        wait_vmcnt<0>();
+#pragma unroll
+        for (int c = CS * h; c < CS * (h + 1); ++c) {
+          if (c * F::KC >= rank) break;
+          V b[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int u = BOTH ? g & 1 : 4 * (c % CS) + g;
+            b[q] = *reinterpret_cast<const V*>(staged + 1024 * UNITS * wave + 16 * (UNITS * (16 * q + r) + (u ^ (r & (UNITS - 1)))));
+          }
+          multiply(c, b);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (c * F::KC >= rank) break;
+        V b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          load_ranks<T, F::FL>(bb + (n + q < a.N ? n + q : a.N - 1) * a.R, c * F::KC + j, a.R, b[q]);
+        multiply(c, b);
       }
     }
     // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].

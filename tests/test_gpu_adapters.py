@@ -335,3 +335,25 @@ def test_a_workspace_for_more_rows_serves_fewer():
     for R in (8, 24, 256):
         sizes = [B.adapter_workspace_size(M, 16384, R) for M in (1, 3, 64, 127, 128, 400, 600, 4096)]
         assert sizes == sorted(sizes)
+
+
+MANY = [  # M, K, N, adapters, rank, dtype, order: many rows at every width of the ranks
+    (128, 2112, 257, 2, 16, "f16", "runs"), (300, 64, 1000, 9, 8, "f16", "mixed"),
+    (300, 576, 67, 3, 24, "f16", "mixed"), (300, 128, 1031, 4, 64, "f16", "mixed"),
+    (300, 2112, 36, 2, 128, "f16", "runs"), (270, 192, 300, 5, 104, "f16", "mixed"),
+    (257, 1088, 130, 3, 256, "f16", "runs"), (300, 64, 515, 40, 12, "f32", "mixed"),
+    (300, 576, 261, 3, 13, "f32", "runs"), (140, 192, 1031, 4, 52, "f32", "mixed"),
+    (300, 320, 65, 2, 128, "f32", "runs"), (130, 128, 300, 3, 253, "f32", "mixed"),
+    (1500, 128, 2100, 4, 16, "f16", "mixed"), (1500, 64, 2100, 4, 40, "f16", "runs"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,dt,order", MANY)
+def test_many_rows_at_every_width(M, K, N, L, R, dt, order):
+    print("adapters, many rows", M, K, N, L, R, dt, order, flush=True)
+    c = case(M, K, N, L, R, dt, order, M + K + N + 4, True)
+    assert np.array_equal(host(B.adapter_add(*[dev(a) for a in c])), O.adapter_add(*c).astype(np.float32))
+    c = case(M, K, N, L, R, dt, order, M + K + N + 5, False)
+    ref, tol = bound(c)
+    got = host(B.adapter_add(*[dev(a) for a in c]))
+    assert np.all(np.abs(got - ref) <= tol), float(np.max(np.abs(got - ref) / tol))
