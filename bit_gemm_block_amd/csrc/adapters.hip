@@ -61,7 +61,12 @@ static_assert(kParts == kRowByRow + 1 && kPartsBytes >= kGroupPartsBytes, "a gro
 // 37.8 us; 2048 rows, rank 32: 16.7 -> 21.4 us).
 constexpr int64_t kWideTileRows = 2816;
 // Workgroups up to which a tile's adapters are shared out among several of them
-// (tiles of one adapter leave the others with nothing to do).
+// (tiles of one adapter leave the others with nothing to do).  x . A, 512 against
+// 1024: 1000 rows of eight mixed adapters, K = 4096, rank 16: 24.3 against 27.2 us;
+// 2048 rows of eight requests, rank 32: 24.4 against 26.0 us.  t . B, 1024 against
+// 2048: 300 rows of mixed adapters, N = 2048, rank 64: 12.5 against 14.5 us, 1000
+// rows, N = 4096, rank 32: 34.5 against 38.3 us; 4096 costs the larger calls more
+// (2048 rows: 51 -> 60 us).
 constexpr unsigned kShareStages = 512;
 constexpr int64_t kShareWorkgroups = 1024;
 
@@ -698,8 +703,19 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // t comes ready as matrix operand (fp16: the pair, two products; one where
 // both parts fit an operand of 32 ranks).  Column q of a wave's four column
 // blocks is matrix column 4 c + q, so that a lane holds four consecutive columns
-// of a row and the loads of y and the stores of out are runs of 256 bytes.  The
-// loads of y and t go out beside those of the rows' adapters.
+// of a row and the loads of y and the stores of out are runs of 256 bytes.
+// Each wave brings its columns of Bt into its own part of LDS with direct copies,
+// 128 bytes of every column at a time: matrix operands put neighbouring lanes
+// into different columns, and loaded from memory as they are, each of a load's 64
+// pieces of 16 bytes is a line of its own (2048 x 64 -> 28672 of 16 mixed adapters
+// of rank 16: 325 -> 188 us; 4096 x 4096 -> 4096, one adapter in most tiles, rank
+// 16 / 64 / 256: 40.6 / 58.1 / 209 -> 37.5 / 50.2 / 170 us).  Column 4 r + q lies
+// at row 16 q + r, its units in the order u ^ r, so that an operand's reads fall in
+// distinct banks.  No barriers: a wave waits for its own copies.
+// What bounds it: y and out (4096 x 28672, rank 16: 940 MB in 165 us, 5.7 TB/s);
+// with ranks of 64 and more the passes of Bt through the L2.  Blocks of 64 rows and
+// float32 products were slower (266 and 218 us where this kernel's first form took
+// 191).
 // RC: the ranks, rounded up (16, 32, ... 256).  SHARED: pass p of the tile's
 // adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
 template <typename T, int RC, bool SHARED>

@@ -31,7 +31,10 @@ struct AdapterArgs {
   int parts;
 };
 
-// Rows from which a call is taken as one of prompts.
+// Rows from which x . A is staged and t enters as a matrix operand.  Above and
+// below it, K = 4096: 256 rows of eight requests, rank 64: 17.1 us staged against
+// 24.0, 256 rows of mixed adapters 22.3 against 31.7; 64 rows of mixed adapters,
+// N = 6144, rank 64: 25.6 against 18.2, N = 28672, rank 16: 22.2 against 17.4 us.
 constexpr int64_t kManyRows = 128;
 // Parts of K of a call of few rows with long rows.
 constexpr int kParts = 4;
