@@ -55,11 +55,17 @@ constexpr int kGroupPartsBytes = 2048;
 // Rows of one adapter in a tile up to which they are multiplied one by one.
 constexpr int kRowByRow = 3;
 static_assert(kParts == kRowByRow + 1 && kPartsBytes >= kGroupPartsBytes, "a group has a row for every part");
-// Rows from which two tiles of 16 share the factors' stages: with a tile for
-// about every compute unit, half as many wide ones move fewer bytes through each
-// (x . A of 4096 rows, K = 14336, rank 64: 65.5 -> 51.3 us, rank 32: 40.5 ->
+// Rows (times groups of 64 ranks) from which two tiles of 16 share the factors'
+// stages: with a tile for about every compute unit, half as many wide ones move
+// fewer bytes through each (x . A of 4096 rows, K = 14336, rank 64: 65.5 -> 51.3 us, rank 32: 40.5 ->
 // 37.8 us; 2048 rows, rank 32: 16.7 -> 21.4 us).
 constexpr int64_t kWideTileRows = 2816;
+// A workgroup of x . A takes up to 64 ranks of its rows (all 256 of them in one:
+// 1000 rows, K = 4096: 72.5 -> 52.2 us, 4096 rows 169 -> 157 us).  Tiles (times such
+// groups of ranks) up to which it takes 32: 592 rows, K = 12224, rank 40: 30.8 -> 22.0
+// us, 256 rows, K = 14336, rank 64: 33.9 -> 24.1 us; with 128 tiles, K = 4096, rank
+// 64: 31.4 -> 34.0 us.
+constexpr int64_t kNarrowTiles = 64;
 // Workgroups up to which a tile's adapters are shared out among several of them
 // (tiles of one adapter leave the others with nothing to do).  x . A, 512 against
 // 1024: 1000 rows of eight mixed adapters, K = 4096, rank 16: 24.3 against 27.2 us;
@@ -282,8 +288,8 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 }
 
 // ---- t = x . At^T: many rows, one adapter for most tiles ------------------------
-// A workgroup owns 16 RT rows and all (up to 16 NT) ranks of an adapter in them,
-// and streams K through LDS: stage s holds RUN bytes of each of the 16 RT rows of
+// A workgroup owns 16 RT rows and 16 NT ranks of an adapter in them (blockIdx.y
+// says which), and streams K through LDS: stage s holds RUN bytes of each of the 16 RT rows of
 // x and the 16 NT rows of At, every row one contiguous run that direct-to-LDS copies bring in (register loads of the matrix operands read 16
 // rows x 64 bytes per instruction, which the caches serve at a fraction of the
 // rate).  Three stages are in flight.  A row's 16-byte units are stored in the
@@ -299,6 +305,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   constexpr int RPC = 1024 / RUN;          // rows of one copy
   constexpr int CPW = ROWS / RPC / NW;     // copies per wave and stage
   constexpr int CHUNKS = RUN / 64;         // matrix operands of a stage
+  constexpr int WRITTEN = NT > 2 ? NT : 2;  // t is written in whole 32 ranks
   static_assert(ROWS % (RPC * NW) == 0, "whole copies per wave");
   static_assert(CPW < 32, "copies in flight");
   __shared__ __attribute__((aligned(16))) uint8_t st0[ROWS * RUN];
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   const int r = lane & 15, g = lane >> 4;
   const int64_t m0 = tile_row(XR);
   if (m0 >= a.M) return;
+  const int j0 = 16 * NT * blockIdx.y;
   const int bytes = a.K * static_cast<int>(sizeof(T));
   const int nst = (bytes + RUN - 1) / RUN;
   const int my = row_adapter(a, m0, lane, XR);
@@ -322,8 +330,8 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
     const unsigned same = static_cast<unsigned>(__ballot(my == ad)) & ALL;
     rest &= ~same;
     if (pass % gridDim.z != blockIdx.z) continue;
-    const int rank = ranks(a, ad);
-    if (rank == 0) continue;
+    const int rank = ranks(a, ad) - j0;  // of those from j0 on
+    if (rank <= 0) continue;
 
     // Copy q of this wave: rows RPC (wave + NW q) to + RPC - 1 of the stage.
     const uint8_t* src[CPW];
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
         p = static_cast<const T*>(a.x) + m * a.ldx;
       } else {
         const int j = row - XR < rank ? row - XR : rank - 1;
-        p = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j) * a.K;
+        p = static_cast<const T*>(a.At) + (static_cast<int64_t>(ad) * a.R + j0 + j) * a.K;
       }
       src[q] = reinterpret_cast<const uint8_t*>(p);
     }
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
       __syncthreads();
       const int64_t ts = adapter_tstride(a.R);
       if constexpr (sizeof(T) == 2) {
-        // t as fp16 pair, hi + lo: the row's largest finite |t| is moved to
+        // t as fp16 pair, hi + lo: the row's largest finite |t| here is moved to
         // [2^13, 2^14), so that the pair holds about 22 bits whatever its size.
         float big = 0.f;
 #pragma unroll
@@ -435,8 +443,8 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
           e = 14 - e;
           e = e > 120 ? 120 : e;
         }
-        _Float16* hi = reinterpret_cast<_Float16*>(a.t) + m * ts + 4 * g;
-        for (int c = wave; 16 * c < ts; c += NW) {
+        _Float16* hi = reinterpret_cast<_Float16*>(a.t) + m * ts + j0 + 4 * g;
+        for (int c = wave; c < WRITTEN && j0 + 16 * c < ts; c += NW) {
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
           if (c < NT) v = joined[c][lane];
           half4 h, l;
@@ -452,10 +460,11 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
             *reinterpret_cast<half4*>(hi + a.M * ts + 16 * c) = l;
           }
         }
-        if (mine && wave == 0 && g == 0) a.t[a.M * ts + m] = ldexpf(1.f, -e);
+        if (mine && wave == 0 && 32 * g < 16 * WRITTEN && j0 + 32 * g < ts)
+          a.t[a.M * ts + (j0 / 32 + g) * adapter_urows(a.M) + m] = ldexpf(1.f, -e);
       } else {
-        float* tp = a.t + m * ts + 4 * g;
-        for (int c = wave; 16 * c < ts; c += NW) {
+        float* tp = a.t + m * ts + j0 + 4 * g;
+        for (int c = wave; c < WRITTEN && j0 + 16 * c < ts; c += NW) {
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
           if (c < NT) v = joined[c][lane];
           if (mine) *reinterpret_cast<f32x4*>(tp + 16 * c) = v;
@@ -716,10 +725,11 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // with ranks of 64 and more the passes of Bt through the L2.  Blocks of 64 rows and
 // float32 products were slower (266 and 218 us where this kernel's first form took
 // 191).
-// RC: the ranks, rounded up (16, 32, ... 256).  SHARED: pass p of the tile's
-// adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
+// RC: the ranks, rounded up (16, 32, ... 256).  Rank 64 is kept within the registers
+// of four waves a SIMD (512 x 4096 -> 4096: 18.2 -> 16.9 us; the other widths are
+// within the next lower or far above).  SHARED: pass p of the tile's adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
 template <typename T, int RC, bool SHARED>
-__global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
+__global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
   constexpr bool F16 = sizeof(T) == 2;
@@ -752,7 +762,6 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   if constexpr (!SHARED) load_rows(rows);
   // Row r's t (of a row without an adapter: anything, and not used).
   V hi[NC], lo[NC];
-  f32x4 un = {1.f, 1.f, 1.f, 1.f};
   const int64_t mt = m0 + r < a.M ? m0 + r : a.M - 1;
   const int j = BOTH ? 8 * (g & 1) : F::FL * g;  // the lane's first rank in a chunk
   const T* tp = reinterpret_cast<const T*>(a.t) + mt * ts + j;
@@ -766,7 +775,12 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
       if constexpr (F16) lo[c] = *reinterpret_cast<const V*>(tp + a.M * ts + at);
     }
   }
-  if constexpr (F16) un = *reinterpret_cast<const f32x4*>(a.t + a.M * ts + m0 + 4 * g);
+  f32x4 un[F16 ? NC : 1];
+  if constexpr (F16) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      un[c] = *reinterpret_cast<const f32x4*>(a.t + a.M * ts + (32 * c < ts ? c : 0) * adapter_urows(a.M) + m0 + 4 * g);
+  }
   const int my = row_adapter(a, m0, lane);
   const Ranks ranks(a, lane);
   const unsigned todo = static_cast<unsigned>(__ballot(my >= 0)) & 0xffffu;
@@ -796,9 +810,6 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
     const int rank = ranks(a, ad);
     rest &= ~same;
     if (rank == 0) continue;  // t was not written
-    f32x4 d[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
     // Chunk c's operands b: what lies past the rank may be anything.
     auto multiply = [&](int c, V(&b)[4]) {
       if (c * F::KC + (BOTH ? 16 : F::KC) > rank) {
@@ -808,10 +819,19 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
 #pragma unroll
           for (int e = 0; e < F::FL; ++e) b[q][e] = k + e < rank ? b[q][e] : static_cast<T>(0.f);
       }
+      f32x4 d[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        d[q] = F::mma(hi[c], b[q], d[q]);
+        d[q] = F::mma(hi[c], b[q], f32x4{0.f, 0.f, 0.f, 0.f});
         if constexpr (F16 && !BOTH) d[q] = F::mma(lo[c], b[q], d[q]);
+      }
+      // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool of = same >> (4 * g + i) & 1;  // other rows' values may be anything
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[i][q] = !of ? acc[i][q] : F16 ? fmaf(d[q][i], un[F16 ? c : 0][i], acc[i][q]) : acc[i][q] + d[q][i];
       }
     };
     if (F16 || a.R % F::FL == 0) {
@@ -850,13 +870,6 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
         multiply(c, b);
       }
     }
-    // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool of = same >> (4 * g + i) & 1;  // other rows' values may be anything
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][q] = of ? d[q][i] * un[i] : acc[i][q];
-    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -865,26 +878,41 @@ __global__ void __launch_bounds__(256) expand_many_kernel(AdapterArgs a) {
   }
 }
 
-template <typename T, int RT, int NT, int RUN, int NW>
+template <typename T, int RT, int NT, int RUN>
 void launch_stage(const AdapterArgs& a, hipStream_t st) {
   const unsigned gx = static_cast<unsigned>(((a.M + 16 * RT - 1) / (16 * RT) + 7) / 8 * 8);
-  const unsigned share = kShareStages / gx;
-  hipLaunchKernelGGL((shrink_stage_kernel<T, RT, NT, RUN, NW>),
-                     dim3(gx, 1, share < 2 ? 2 : share > 16 ? 16 : share), dim3(64 * NW), 0, st, a);
+  const unsigned gy = static_cast<unsigned>((a.R + 16 * NT - 1) / (16 * NT));
+  const unsigned share = kShareStages / (gx * gy);
+  hipLaunchKernelGGL((shrink_stage_kernel<T, RT, NT, RUN, 8>),
+                     dim3(gx, gy, share < 2 ? 2 : share > 16 ? 16 : share), dim3(512), 0, st, a);
 }
 
-template <typename T, int RC, int RUN, int NW>
+// Up to rank 32 three stages of 512 bytes a row leave room for a second workgroup
+// on a compute unit; where there is no second one (few tiles), the double run
+// halves the stages' latencies (512 rows, K = 14336, rank 16: 25.0 -> 20.9 us; 4096
+// rows, rank 32: 74.8 -> 78.1 us).
+template <typename T, int RC>
+void launch_shrink(const AdapterArgs& a, hipStream_t st) {
+  const int64_t tiles = (a.M + 15) / 16;
+  if constexpr (RC <= 32) {
+    if (a.M <= 16 * 128) return launch_stage<T, 1, RC / 16, 1024>(a, st);
+    if constexpr (RC == 32) {
+      if (a.M >= kWideTileRows) return launch_stage<T, 2, 2, 512>(a, st);
+    }
+    launch_stage<T, 1, RC / 16, 512>(a, st);
+  } else {
+    const int64_t groups = (a.R + 63) / 64;
+    if (a.M * groups >= kWideTileRows) launch_stage<T, 2, 4, 512>(a, st);
+    else if (tiles * groups <= kNarrowTiles) launch_stage<T, 1, 2, 1024>(a, st);
+    else launch_stage<T, 1, 4, 512>(a, st);
+  }
+}
+
+template <typename T, int RC>
 void launch_rank(const AdapterArgs& a, hipStream_t st) {
   const unsigned tiles = static_cast<unsigned>((a.M + 15) / 16);
   if (a.M >= kManyRows) {
-    if constexpr (RC == 32 || RC == 64) {
-      if (a.M >= kWideTileRows)
-        launch_stage<T, 2, RC / 16, 512, 8>(a, st);
-      else
-        launch_stage<T, 1, RC / 16, RUN, NW>(a, st);
-    } else {
-      launch_stage<T, 1, RC / 16, RUN, NW>(a, st);
-    }
+    launch_shrink<T, RC>(a, st);
     const unsigned gx = (tiles + 7) / 8 * 8;
     const unsigned gy = static_cast<unsigned>((a.N + 255) / 256);
     const int64_t share = kShareWorkgroups / (static_cast<int64_t>(gx) * gy);
@@ -904,18 +932,13 @@ void launch_rank(const AdapterArgs& a, hipStream_t st) {
                      dim3(256), 0, st, a);
 }
 
-// RUN and NW: bytes of a row in a stage, and waves.  Up to rank 32 three stages
-// leave room for a second workgroup on a compute unit; where there is no second
-// one (few tiles), the double run halves the stages' latencies (512 rows,
-// K = 14336, rank 16: 25.0 -> 20.9 us; 4096 rows, rank 32: 74.8 -> 78.1 us).
 template <typename T>
 hipError_t launch_typed(const AdapterArgs& a, hipStream_t st) {
-  const bool alone = a.M <= 16 * 128;
-  if (a.R <= 16) alone ? launch_rank<T, 16, 1024, 8>(a, st) : launch_rank<T, 16, 512, 8>(a, st);
-  else if (a.R <= 32) alone ? launch_rank<T, 32, 1024, 8>(a, st) : launch_rank<T, 32, 512, 8>(a, st);
-  else if (a.R <= 64) launch_rank<T, 64, 512, 8>(a, st);
-  else if (a.R <= 128) launch_rank<T, 128, 256, 4>(a, st);
-  else launch_rank<T, 256, 128, 2>(a, st);
+  if (a.R <= 16) launch_rank<T, 16>(a, st);
+  else if (a.R <= 32) launch_rank<T, 32>(a, st);
+  else if (a.R <= 64) launch_rank<T, 64>(a, st);
+  else if (a.R <= 128) launch_rank<T, 128>(a, st);
+  else launch_rank<T, 256>(a, st);
   return hipGetLastError();
 }
 

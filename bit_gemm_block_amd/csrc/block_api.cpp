@@ -31,11 +31,11 @@ extern "C" {
 
 size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank) {
   if (M <= 0 || K <= 0 || rank <= 0) return 0;
-  // t (of few rows: of every part of K), and one float32 per row (whole tiles of
-  // 16).  What serves M rows serves fewer.
+  // t (of few rows: of every part of K), and one float32 for 32 ranks of a row
+  // (whole tiles of 16 rows).  What serves M rows serves fewer.
   const int64_t few = w4a4::kParts * (M < w4a4::kManyRows ? M : w4a4::kManyRows - 1);
   return (static_cast<size_t>(M > few ? M : few) * static_cast<size_t>(w4a4::adapter_tstride(rank)) +
-          static_cast<size_t>((M + 15) / 16 * 16)) * 4;
+          static_cast<size_t>(w4a4::adapter_urows(M) * w4a4::adapter_tstride(rank) / 32)) * 4;
 }
 
 int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, const void* Bt,

@@ -26,7 +26,7 @@ struct AdapterArgs {
   // x . A, [M, adapter_tstride(R)].  Few rows: `parts` such matrices of float32 to
   // be added up, not scaled, defined up to the row's rank.  Many rows, fp32: scaled, zero past the rank; fp16: the same
   // as fp16 pair (hi, then lo), times a power of two whose inverse follows, one
-  // float32 per row.
+  // float32 per row for every 32 ranks: [adapter_tstride(R) / 32][adapter_urows(M)].
   float* t;
   int parts;
 };
@@ -41,6 +41,8 @@ constexpr int kParts = 4;
 
 // The row distance of t.
 __host__ __device__ inline int64_t adapter_tstride(int64_t R) { return (R + 31) / 32 * 32; }
+// The row distance of the powers of two: whole tiles of 16.
+__host__ __device__ inline int64_t adapter_urows(int64_t M) { return (M + 15) / 16 * 16; }
 hipError_t launch_adapter_add(const AdapterArgs& a, bool f16, hipStream_t st);
 
 // ---- norms joined with gate and residual (norm_residual.hip) -----------------
