@@ -11,7 +11,13 @@
 // |2u|) roundings of the result, so what the argument's rounding loses is
 // carried to first order: erfc(z + d) = erfc(z) (1 - 2 z d) for z > 0 to
 // within d / z, e^-(p + d) = e^-p (1 - d).
-// Everything is float32 between one read and one rounding of the result.
+// Everything is float32 between one read and one rounding of the result (fp64 for
+// the cubic argument of gelu_tanh alone).
+//
+// What bounds it: memory.  Every element is read and written once, eight to a
+// thread, past the caches (4096 x 14336 silu, fp32 to fp16: 587 MB in 96 us, 6.1
+// TB/s; 102.7 us with cached loads, 105 with cached stores as well).  Short calls
+// are one launch (8 x 14336: 2.5 us).
 #include "block_internal.h"
 #include "vec_io.h"
 

@@ -5,6 +5,14 @@
 // each), so y and h are read once and h' and x written once; the statistics
 // are float32 sums over the row, the variance of a layer norm over the
 // centred values (a second sum over registers, not a second read).
+//
+// What bounds it: long calls by memory (4096 x 4096, fp32 rows, fp16 x: 235 MB in
+// 44 us, 5.3 TB/s; 4096 x 16384, fp16 rows, fp32 y, a gate: 671 MB in 141 us, 4.8
+// TB/s), short ones by latency (8 x 4096: 3.8 us, of which an empty launch is 1.6):
+// a load, two or four sums over the workgroup and the parameters' loads follow
+// one another.  The parameters are not loaded before the sums: kept in registers
+// they spill at 1024 threads (4096 x 16384: 150 -> 269 us), and brought early into
+// the caches they gain nothing (8 x 4096: 4.16 -> 4.25 us).
 #include "block_internal.h"
 #include "vec_io.h"
 
@@ -193,11 +201,15 @@ void launch_shape(const NormArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, EVEN, H, Y, P>), grid, block, 0, st, a);
 }
 
+// The waves that a row needs with one chunk each, two from eight waves on: four
+// waves for C <= 512 cost 10.4 us instead of 5.3 (4096 x 512), and for C = 8192
+// sixteen with one chunk 88.8 instead of 77.3; for C = 4096 four with two cost 40.4
+// instead of 39.0, and for C = 16384 eight with four 150 instead of 147.
 template <typename H, typename Y, typename P>
 void launch_types(const NormArgs& a, hipStream_t st) {
   if (a.C <= 512) return launch_shape<1, 1, H, Y, P>(a, st);
   if (a.C <= 2048) return launch_shape<4, 1, H, Y, P>(a, st);
-  if (a.C <= 4096) return launch_shape<4, 2, H, Y, P>(a, st);
+  if (a.C <= 4096) return launch_shape<8, 1, H, Y, P>(a, st);
   if (a.C <= 8192) return launch_shape<8, 2, H, Y, P>(a, st);
   return launch_shape<16, 2, H, Y, P>(a, st);
 }
