@@ -129,7 +129,11 @@ struct Ranks {
 // the eight sums are joined by halving: in each of the first three steps the
 // lanes of a pair exchange the half of the sums that the other one keeps, after
 // which a lane has one sum left and joins it with seven neighbours.  Larger
-// groups of rows go to the matrix instruction.
+// groups of rows go to the matrix instruction (eight rows at a time in vector
+// registers: 8 rows, K = 14336, 25.7 -> 16.4 us, but one row 7.7 -> 9.9 us).
+// What bounds it: latency, a chain of index, factors and sums (one row, K = 4096,
+// rank 16: 4.0 us with its launch; 64 rows of 32 mixed adapters of rank 64: 7.4 us
+// for about 10 MB of factors).  Four or sixteen waves share K no better than eight.
 
 // Ranks j0 to j0 + 7 (those past `rank`: its last one) of adapter ad with the
 // first MR rows of `rows` (its last one again, if there are fewer), over chunks
@@ -295,6 +299,10 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 // rate).  Three stages are in flight.  A row's 16-byte units are stored in the
 // order u ^ (row & 15), chosen by the copies' addresses, so that the reads of
 // one unit of 16 rows fall in distinct banks.
+// What bounds it: the copies, one workgroup (or two) to a compute unit (4096 rows,
+// K = 14336, rank 32: 117 MB of x in 37 us, where copies of x alone take 25 to 29;
+// tiles with rows of two adapters stream their rows twice, about 10 us of it).  Four
+// and five stages, staggered ones and non-temporal copies of x were level or slower.
 template <typename T, int RT, int NT, int RUN, int NW>
 __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
   using F = Frag<T>;
@@ -502,6 +510,9 @@ __device__ __forceinline__ void store_out(float* row, int64_t n, int64_t N, f32x
 // of them in flight.  The dot products' parts are joined by halving: in
 // every step the lanes of a pair exchange the half of their columns that the
 // other one keeps, and a lane ends up with one column (or more, where LPC < 8).
+// What bounds it: latency up to a few MB (one row, N = 4096, rank 16: 4.0 us with its
+// launch), then the stream of Bt (64 rows of 32 mixed adapters of rank 64, N = 6144:
+// about 20 MB in 9 us).
 
 // Columns [n0, n0 + 512 / LPC) of rows of adapter ad (or of none: ad < 0), by one
 // wave.
@@ -721,7 +732,7 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // 16 / 64 / 256: 40.6 / 58.1 / 209 -> 37.5 / 50.2 / 170 us).  Column 4 r + q lies
 // at row 16 q + r, its units in the order u ^ r, so that an operand's reads fall in
 // distinct banks.  No barriers: a wave waits for its own copies.
-// What bounds it: y and out (4096 x 28672, rank 16: 940 MB in 165 us, 5.7 TB/s);
+// What bounds it: y and out (4096 x 28672, rank 16: 940 MB in 165 to 188 us);
 // with ranks of 64 and more the passes of Bt through the L2.  Blocks of 64 rows and
 // float32 products were slower (266 and 218 us where this kernel's first form took
 // 191).
