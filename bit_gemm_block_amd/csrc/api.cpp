@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "block_internal.h"
 #include "w4a4_internal.h"
 
 namespace {

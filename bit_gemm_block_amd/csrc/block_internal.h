@@ -7,6 +7,9 @@
 
 namespace w4a4 {
 
+// W4A4_OK if the current device is a gfx950, else W4A4_ERR_UNSUPPORTED (api.cpp).
+int device_status();
+
 // ---- low-rank adapters of many requests (adapters.hip) ----------------------
 struct AdapterArgs {
   const void* x;  // [M, K], row distance ldx

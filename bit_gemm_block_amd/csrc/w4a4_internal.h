@@ -151,8 +151,6 @@ int qlinear_impl(const void* x, int x_dtype, const uint8_t* wq, int w_layout,
                  int qmax);
 // Records e as the HIP error behind a W4A4_ERR_HIP and returns that status.
 int hip_status(hipError_t e);
-// W4A4_OK if the current device is a gfx950, else W4A4_ERR_UNSUPPORTED.
-int device_status();
 
 // ---- weight group sums (offq.hip) ------------------------------------------
 // out[n, g] = sum of the signed weight codes of row n over K-group g
