@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 
 // ---- t = x . At^T: many rows, one adapter for most tiles ------------------------
 // A workgroup owns 16 RT rows and 16 NT ranks of an adapter in them (blockIdx.y
-// says which), and streams K through LDS: stage s holds RUN bytes of each of the 16 RT rows of
-// x and the 16 NT rows of At, every row one contiguous run that direct-to-LDS copies bring in (register loads of the matrix operands read 16
+// says which), and streams K through LDS: stage s holds RUN bytes of each of the
+// 16 RT rows of x and the 16 NT rows of At, every row one contiguous run that
+// direct-to-LDS copies bring in (loads of the matrix operands themselves read 16
 // rows x 64 bytes per instruction, which the caches serve at a fraction of the
 // rate).  Three stages are in flight.  A row's 16-byte units are stored in the
 // order u ^ (row & 15), chosen by the copies' addresses, so that the reads of
@@ -303,18 +304,18 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 // K = 14336, rank 32: 117 MB of x in 37 us, where copies of x alone take 25 to 29;
 // tiles with rows of two adapters stream their rows twice, about 10 us of it).  Four
 // and five stages, staggered ones and non-temporal copies of x were level or slower.
-template <typename T, int RT, int NT, int RUN, int NW>
-__global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
+template <typename T, int RT, int NT, int RUN>
+__global__ void __launch_bounds__(512) shrink_stage_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
-  constexpr int XR = 16 * RT, ROWS = XR + 16 * NT;
+  constexpr int NW = 8, XR = 16 * RT, ROWS = XR + 16 * NT;
   constexpr int UNITS = RUN / 16;          // 16-byte units of a row in a stage
-  constexpr int SW = UNITS < 16 ? UNITS - 1 : 15;
   constexpr int RPC = 1024 / RUN;          // rows of one copy
   constexpr int CPW = ROWS / RPC / NW;     // copies per wave and stage
   constexpr int CHUNKS = RUN / 64;         // matrix operands of a stage
   constexpr int WRITTEN = NT > 2 ? NT : 2;  // t is written in whole 32 ranks
   static_assert(ROWS % (RPC * NW) == 0, "whole copies per wave");
+  static_assert(UNITS >= 16 && CHUNKS % NW == 0, "units of distinct banks, whole rounds of the waves");
   static_assert(CPW < 32, "copies in flight");
   __shared__ __attribute__((aligned(16))) uint8_t st0[ROWS * RUN];
   __shared__ __attribute__((aligned(16))) uint8_t st1[ROWS * RUN];
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
 #pragma unroll
     for (int q = 0; q < CPW; ++q) {
       const int row = RPC * (wave + NW * q) + lane / UNITS;
-      off[q] = 16 * ((lane % UNITS) ^ (row & SW));
+      off[q] = 16 * ((lane % UNITS) ^ (row & 15));
       const T* p;
       if (row < XR) {
         const int64_t m = m0 + row < a.M ? m0 + row : a.M - 1;
@@ -373,10 +374,10 @@ __global__ void __launch_bounds__(64 * NW) shrink_stage_kernel(AdapterArgs a) {
     auto compute = [&](const uint8_t* buf, int s) {
       const int valid = (bytes - s * RUN) / 64;
 #pragma unroll
-      for (int u = 0; u < (CHUNKS + NW - 1) / NW; ++u) {
+      for (int u = 0; u < CHUNKS / NW; ++u) {
         const int ch = u * NW + wave;
-        if (ch >= CHUNKS || ch >= valid) break;
-        const int at = r * RUN + 16 * ((4 * ch + g) ^ (r & SW));  // row & SW is r & SW for every block of 16
+        if (ch >= valid) break;
+        const int at = r * RUN + 16 * ((4 * ch + g) ^ r);
         V xv[RT], av[NT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) xv[t] = *reinterpret_cast<const V*>(buf + 16 * t * RUN + at);
@@ -678,7 +679,7 @@ __device__ __forceinline__ void group_pass(const AdapterArgs& a, int64_t m0, uns
 // Workgroup (4 x 512 / LPC columns, tile, slot): slot s takes the rows of the
 // adapter that row s of the tile leads, a few of them one by one.  Larger groups
 // share their columns, 256 at a time, among their rows' slots (100 rows of four
-// adapters, N = 6144, rank 16: 22.1 -> 14.5 us with K = 4096).
+// adapters, K = 4096, N = 6144, rank 16: 22.1 -> 14.5 us).
 template <typename T, int RC>
 __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
   constexpr int LPC = RC * static_cast<int>(sizeof(T)) / 16, COLS = 4 * 512 / LPC;
@@ -894,7 +895,7 @@ void launch_stage(const AdapterArgs& a, hipStream_t st) {
   const unsigned gx = static_cast<unsigned>(((a.M + 16 * RT - 1) / (16 * RT) + 7) / 8 * 8);
   const unsigned gy = static_cast<unsigned>((a.R + 16 * NT - 1) / (16 * NT));
   const unsigned share = kShareStages / (gx * gy);
-  hipLaunchKernelGGL((shrink_stage_kernel<T, RT, NT, RUN, 8>),
+  hipLaunchKernelGGL((shrink_stage_kernel<T, RT, NT, RUN>),
                      dim3(gx, gy, share < 2 ? 2 : share > 16 ? 16 : share), dim3(512), 0, st, a);
 }
 
