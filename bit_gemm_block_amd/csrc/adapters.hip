@@ -76,6 +76,9 @@ constexpr int64_t kNarrowTiles = 64;
 constexpr unsigned kShareStages = 512;
 constexpr int64_t kShareWorkgroups = 1024;
 
+// What the low half of a pair is moved up by (see shrink_stage_kernel).
+constexpr float kLowUp = 2048.f;
+
 // P ranks of a row of Bt from rank k on (those past R: anything of the row).
 // fp32 rows of any length: whole loads need only an element's alignment.
 template <typename T, int P>
@@ -434,8 +437,12 @@ __global__ void __launch_bounds__(512) shrink_stage_kernel(AdapterArgs a) {
       __syncthreads();
       const int64_t ts = adapter_tstride(a.R);
       if constexpr (sizeof(T) == 2) {
-        // t as fp16 pair, hi + lo: the row's largest finite |t| here is moved to
-        // [2^13, 2^14), so that the pair holds about 22 bits whatever its size.
+        // t as fp16 pair, hi + 2^-11 lo: the row's largest finite |t| here is moved
+        // to [2^13, 2^14), and what hi leaves, at most 2^-11 of the value, up by
+        // 2^11, so that it meets fp16's subnormal numbers no earlier than the value
+        // itself does.  Every t keeps 22 bits down to 2^-27 of the row's largest,
+        // smaller ones an error of 2^-49 of it or less.  (Under one power of two for
+        // both halves a t 2^-21 of the largest kept 18 bits.)
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < NT; ++c)
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(512) shrink_stage_kernel(AdapterArgs a) {
             const float u = ldexpf(v[i], e);
             h[i] = static_cast<_Float16>(u);
             const float d = u - static_cast<float>(h[i]);
-            l[i] = static_cast<_Float16>(fabsf(u) < INFINITY ? d : 0.f);
+            l[i] = static_cast<_Float16>(fabsf(u) < INFINITY ? kLowUp * d : 0.f);
           }
           if (mine) {
             *reinterpret_cast<half4*>(hi + 16 * c) = h;
@@ -721,8 +728,8 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 
 // ---- out = y + s t . Bt^T: many rows -------------------------------------------
 // A workgroup of four waves takes 16 rows and 256 columns, a wave 64 of them;
-// t comes ready as matrix operand (fp16: the pair, two products; one where
-// both parts fit an operand of 32 ranks).  Column q of a wave's four column
+// t comes ready as matrix operand (fp16: the pair, a product each, as the halves
+// have powers of two of their own).  Column q of a wave's four column
 // blocks is matrix column 4 c + q, so that a lane holds four consecutive columns
 // of a row and the loads of y and the stores of out are runs of 256 bytes.
 // Each wave brings its columns of Bt into its own part of LDS with direct copies,
@@ -738,14 +745,16 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // float32 products were slower (266 and 218 us where this kernel's first form took
 // 191).
 // RC: the ranks, rounded up (16, 32, ... 256).  Rank 64 is kept within the registers
-// of four waves a SIMD (512 x 4096 -> 4096: 18.2 -> 16.9 us; the other widths are
-// within the next lower or far above).  SHARED: pass p of the tile's adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
+// of four waves a SIMD (512 x 4096 -> 4096: 18.2 -> 16.9 us), fp16 of rank 16 within
+// those of five (4096 x 4096 -> 28672: 202 -> 197 us); the other widths are within the
+// next lower or far above.  SHARED: pass p of the tile's adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
 template <typename T, int RC, bool SHARED>
-__global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(AdapterArgs a) {
+__global__ void __launch_bounds__(256, RC == 64 ? 4 : RC == 16 && sizeof(T) == 2 ? 5 : 1) expand_many_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
   constexpr bool F16 = sizeof(T) == 2;
-  constexpr bool BOTH = F16 && RC == 16;  // hi in ranks 0 .. 15 of an operand, lo in 16 .. 31
+  // One load brings hi as ranks 0 .. 15 of an operand and lo as 16 .. 31.
+  constexpr bool BOTH = F16 && RC == 16;
   constexpr int NC = BOTH ? 1 : RC / F::KC;
   // A stage: RS ranks (UNITS units of 16 bytes, CS operands) of a wave's columns.
   constexpr int ROW = RC * static_cast<int>(sizeof(T)), UNITS = ROW < 128 ? ROW / 16 : 8;
@@ -778,7 +787,9 @@ __global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(Adap
   const int j = BOTH ? 8 * (g & 1) : F::FL * g;  // the lane's first rank in a chunk
   const T* tp = reinterpret_cast<const T*>(a.t) + mt * ts + j;
   if constexpr (BOTH) {
-    hi[0] = *reinterpret_cast<const V*>(tp + (g >> 1) * a.M * ts);
+    const V v = *reinterpret_cast<const V*>(tp + (g >> 1) * a.M * ts), zero = {};
+    hi[0] = g < 2 ? v : zero;
+    lo[0] = g < 2 ? zero : v;
   } else {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -822,6 +833,9 @@ __global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(Adap
     const int rank = ranks(a, ad);
     rest &= ~same;
     if (rank == 0) continue;  // t was not written
+    f32x4 sum[4];  // of the adapter's rows; the other rows' may be anything
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     // Chunk c's operands b: what lies past the rank may be anything.
     auto multiply = [&](int c, V(&b)[4]) {
       if (c * F::KC + (BOTH ? 16 : F::KC) > rank) {
@@ -835,16 +849,18 @@ __global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(Adap
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         d[q] = F::mma(hi[c], b[q], f32x4{0.f, 0.f, 0.f, 0.f});
-        if constexpr (F16 && !BOTH) d[q] = F::mma(lo[c], b[q], d[q]);
+        if constexpr (F16) {
+          const f32x4 low = F::mma(lo[c], b[q], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[q][i] = fmaf(low[i], 1.f / kLowUp, d[q][i]);
+        }
       }
       // Result lane 16 g + c: row 4 g + i, column n0 + 4 c + q in d[q][i].
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool of = same >> (4 * g + i) & 1;  // other rows' values may be anything
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          acc[i][q] = !of ? acc[i][q] : F16 ? fmaf(d[q][i], un[F16 ? c : 0][i], acc[i][q]) : acc[i][q] + d[q][i];
-      }
+          sum[i][q] = F16 ? fmaf(d[q][i], un[F16 ? c : 0][i], sum[i][q]) : sum[i][q] + d[q][i];
     };
     if (F16 || a.R % F::FL == 0) {
 #pragma unroll
@@ -882,6 +898,9 @@ __global__ void __launch_bounds__(256, RC == 64 ? 4 : 1) expand_many_kernel(Adap
         multiply(c, b);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (same >> (4 * g + i) & 1) acc[i] = sum[i];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -27,9 +27,10 @@ struct AdapterArgs {
   float* out;
   int64_t ldo;
   // x . A, [M, adapter_tstride(R)].  Few rows: `parts` such matrices of float32 to
-  // be added up, not scaled, defined up to the row's rank.  Many rows, fp32: scaled, zero past the rank; fp16: the same
-  // as fp16 pair (hi, then lo), times a power of two whose inverse follows, one
-  // float32 per row for every 32 ranks: [adapter_tstride(R) / 32][adapter_urows(M)].
+  // be added up, not scaled, defined up to the row's rank.  Many rows, fp32: scaled,
+  // zero past the rank; fp16: the same as fp16 pair (hi, then 2^11 times what hi
+  // leaves), times a power of two whose inverse follows, one float32 per row for
+  // every 32 ranks: [adapter_tstride(R) / 32][adapter_urows(M)].
   float* t;
   int parts;
 };

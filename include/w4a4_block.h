@@ -55,9 +55,9 @@ size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank);
  *           equal y when ldo equals ldy.
  *   Both sums are float32 and t is not rounded to the factors' type: it stays
  *   float32, except that with 128 rows or more and fp16 factors the second
- *   product takes scales[a] t as a pair of fp16 values, hi + lo, under a power
- *   of two per row and 32 or 64 ranks (their largest |t| keeps 22 bits, the others
- *   an absolute error of 2^-22 of it or less).  A row's result depends on its own inputs
+ *   product takes scales[a] t as a pair of fp16 values under powers of two per
+ *   row and 32 or 64 ranks: off by 2^-22 of itself, or 2^-49 of the largest |t|
+ *   of these ranks, whichever is more (float32's own rounding is 2^-24).  A row's result depends on its own inputs
  *   only (not on the other rows' values; M and index choose the order of its
  *   sums) and is the same from call to call.
  *   workspace: at least w4a4_adapter_workspace_size(M, K, rank) bytes.
