@@ -744,12 +744,17 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // with ranks of 64 and more the passes of Bt through the L2.  Blocks of 64 rows and
 // float32 products were slower (266 and 218 us where this kernel's first form took
 // 191).
-// RC: the ranks, rounded up (16, 32, ... 256).  Rank 64 is kept within the registers
-// of four waves a SIMD (512 x 4096 -> 4096: 18.2 -> 16.9 us), fp16 of rank 16 within
-// those of five (4096 x 4096 -> 28672: 202 -> 197 us); the other widths are within the
-// next lower or far above.  SHARED: pass p of the tile's adapters runs in workgroup p mod grid.z, which then loads y for its rows only.
+// RC: the ranks, rounded up (16, 32, ... 256).  SHARED: pass p of the tile's adapters
+// runs in workgroup p mod grid.z, which then loads y for its rows only.
+// Waves a SIMD whose registers a kernel keeps within: fp16 of rank 64 four (512 x 4096
+// -> 4096: 18.2 -> 16.9 us), of rank 16 five (4096 x 4096 -> 28672: 202 -> 197 us); the
+// other widths are within the next lower or far above.  fp32 is left alone: held to
+// four waves, rank 64 kept about fifty registers in memory (4096 x 1024 -> 14336: 345
+// against 203 us, 512 x 4096 -> 4096: 42.7 against 32.7 us).
+template <typename T, int RC>
+constexpr int kWaves = sizeof(T) != 2 ? 1 : RC == 16 ? 5 : RC == 64 ? 4 : 1;
 template <typename T, int RC, bool SHARED>
-__global__ void __launch_bounds__(256, RC == 64 ? 4 : RC == 16 && sizeof(T) == 2 ? 5 : 1) expand_many_kernel(AdapterArgs a) {
+__global__ void __launch_bounds__(256, (kWaves<T, RC>)) expand_many_kernel(AdapterArgs a) {
   using F = Frag<T>;
   typedef typename F::V V;
   constexpr bool F16 = sizeof(T) == 2;
