@@ -1,6 +1,6 @@
-"""Builds libw4a4.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and
-_block.so, the Python binding of its operators beside the layer (host code
-against torch's headers).
+"""Builds libw4a4.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and,
+where torch is installed, _block.so, the Python binding of its operators beside
+the layer (host code against torch's headers).
 
     python -m bit_gemm_block_amd.build
 """
@@ -50,14 +50,20 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-def _binding() -> str:
-    """Object file of the binding."""
+def _binding() -> str | None:
+    """Object file of the binding (None without torch)."""
     import sysconfig
 
-    from torch.utils import cpp_extension
+    try:
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        print(f"{os.path.basename(BINDING)}, the Python binding of the operators beside the layer, needs torch "
+              f"and is not built ({e})")
+        return None
     obj = os.path.join(BUILD_DIR, "block_binding.cpp.o")
     rocm = os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    cxx = os.environ.get("CXX") or shutil.which("g++") or hipcc()
+    cmd = [cxx, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE]
     for i in cpp_extension.include_paths() + [sysconfig.get_paths()["include"], rocm]:
         cmd += ["-isystem", i]
@@ -94,7 +100,9 @@ def build(extra: list[str] | None = None, save_temps: bool = False) -> str:
         binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
         _link(LIB, ["--offload-arch=gfx950"] + objs)
-        link_binding(binding.result())
+        obj = binding.result()
+        if obj:
+            link_binding(obj)
     return LIB
 
 
