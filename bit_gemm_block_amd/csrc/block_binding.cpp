@@ -49,15 +49,16 @@ int64_t device_index(const Tensor& t) {
   return t.get_device();
 }
 
-// The row distance of a device matrix [M, C] with contiguous rows.
+// The row distance of a device matrix [M, C] with contiguous rows.  A single row's
+// is C: the distance to a next row, which may be any (and off 16 bytes), is not used.
 int64_t rows(const Tensor& t, const char* name, int64_t dev, int64_t M, int64_t C) {
   on_device(t, name, dev);
   if (t.dim() != 2 || t.size(0) != M || t.size(1) != C)
     throw py::value_error(std::string(name) + " must be " + text({M, C}) + ", not " + text(t.sizes()));
   if (C > 1 && t.stride(1) != 1) throw py::value_error(std::string(name) + " must have contiguous rows");
-  if (t.stride(0) >= C) return t.stride(0);
-  if (M > 1 && C > 0) throw py::value_error(std::string(name) + " must have rows that do not overlap");
-  return C;
+  if (M < 2) return C;
+  if (t.stride(0) < C) throw py::value_error(std::string(name) + " must have rows that do not overlap");
+  return t.stride(0);
 }
 
 // The address of a contiguous device tensor of this dtype and shape.
