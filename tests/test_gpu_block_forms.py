@@ -1,9 +1,12 @@
 """Forms of the operators beside the layer that ordinary sizes do not reach, on
-the GPU: a single row cut from a wider matrix."""
+the GPU: a single row cut from a wider matrix, more adapters than a wave has
+lanes, more rows than a launch has workgroups, and more than 2^31 elements.
+Bars as in the operators' own tests."""
 import numpy as np
 import pytest
 import torch
 
+import test_gpu_block_seams as seams
 from bit_gemm_block_amd import block as B
 from oracle import block_oracle as O
 
@@ -49,3 +52,62 @@ def test_one_row_of_a_wider_matrix(dt):
     want = host(B.norm_residual(h.contiguous(), pre_norm="rms", x_dtype=F32)[1])
     B.norm_residual(h, pre_norm="rms", h_out=torch.as_strided(y, (1, 100), (100, 1)), x_out=out)
     assert np.array_equal(host(out), want)
+
+
+@pytest.mark.parametrize("M,K,N,L,R,dt", [(1, 64, 40, 65, 8, "f16"), (40, 128, 100, 100, 16, "f16"),
+                                          (100, 64, 70, 300, 5, "f32"), (300, 128, 70, 200, 24, "f16"),
+                                          (200, 64, 300, 130, 16, "f32"), (130, 192, 40, 4000, 8, "f16")])
+def test_more_than_64_adapters(M, K, N, L, R, dt):
+    print("many adapters", M, K, N, L, R, dt, flush=True)
+    c = whole_numbers(M, K, N, L, R, dt, M + L)
+    c[4][-1] = L - 1
+    c[4][0] = L - 1 if M == 1 else 64
+    c[5][[64, L - 1]] = R, max(R // 2, 1)
+    assert np.array_equal(host(B.adapter_add(*[dev(a) for a in c])), O.adapter_add(*c).astype(np.float32))
+    assert np.array_equal(host(B.adapter_add(*[dev(a) for a in c[:5]])), O.adapter_add(*c[:5]).astype(np.float32))
+
+
+@pytest.mark.parametrize("M,C", [(4 * 2 ** 20 + 9, 16), (2 ** 20 + 5, 520)])
+def test_norms_of_more_rows_than_workgroups(M, C):
+    # Three sums a row: a workgroup's second row starts on the other slot.
+    print("norms, long loop", M, C, flush=True)
+    step = 2 ** 20 if C > 512 else 4 * 2 ** 20
+    h = torch.randn((M, C), dtype=F16, device=DEV)
+    y = torch.randn((M, C), dtype=F16, device=DEV)
+    rows = np.array([0, 1, 2, 3, 4, 1000, step - 2, step - 1, step, step + 1, step + 2, step + 3, step + 4, M - 1])
+    at = torch.from_numpy(rows).to(DEV)
+    size = torch.tensor([1, 300, 0.01, 40, 2, 1, 7, 500, 300, 0.01, 200, 0, 100, 3], device=DEV)[:, None]
+    h[at] = (h[at].float() * size).half()
+    y[at] = (y[at].float() * size.flip(0) + size).half()
+    rng = np.random.default_rng(2)
+    p = {k: rng.uniform(0.5, 1.5, C).astype(np.float32) for k in ("post_w", "pre_w")}
+    kw = dict(p, post="layer", pre="rms", rs=0.5, eps=1e-5)
+    h0, y0 = host(h[at]), host(y[at])
+    gh, gx = B.norm_residual(h, y, post_norm="layer", pre_norm="rms", residual_scale=0.5, eps=1e-5,
+                             post_weight=dev(p["post_w"]), pre_weight=dev(p["pre_w"]), x_dtype=F32)
+    seams.check(h0, y0, kw, np.float16, np.float32, (host(gh[at]), host(gx[at])))
+
+
+def test_norms_past_2_31_elements():
+    M, C = 131080, 16384
+    print("norms, offsets", M, C, flush=True)
+    h = torch.empty((M, C), dtype=F16, device=DEV).normal_()
+    rows = np.array([0, 1, 65535, 65536, 131071, 131072, 131073, M - 1])
+    at = torch.from_numpy(rows).to(DEV)
+    gx = B.norm_residual(h, pre_norm="rms", eps=1e-5)[1]
+    seams.check(host(h[at]), None, dict(pre="rms", eps=1e-5), np.float16, np.float16, (None, host(gx[at])))
+
+
+@pytest.mark.parametrize("M,F,gap", [(40000, 24, 8), (40000, 23, 5), (70000, 30700, 0), (131080, 16390, 10)])
+def test_gated_rows_and_offsets(M, F, gap):
+    # More rows than the grid has, and both forms past 2^31 elements.
+    print("gated, rows", M, F, gap, flush=True)
+    g = torch.empty((M, F + gap), dtype=F16, device=DEV).normal_()[:, :F]
+    at = {0, 1, 32767, 32768, 32769, M - 2, M - 1} | {min(2 ** 31 // (F + gap) + i, M - 1) for i in (-1, 0, 1)}
+    at = torch.tensor(sorted(at), device=DEV)
+    out = torch.full((M, F + gap), 7.0, dtype=F16, device=DEV)
+    B.gated_activation(g, None, "silu", out=out[:, :F])
+    gr, got = host(g[at]), host(out[at])
+    ref = O.activation(gr, "silu")
+    assert np.all(np.abs(got[:, :F] - ref) <= seams.act_bound(gr, ref, np.float16, None))
+    assert np.all(got[:, F:] == 7.0)
