@@ -136,23 +136,36 @@ def random_block(C: int, F: int, adapters: int, rank: int, seed: int = 0, w_layo
 
 
 def reference(mlp: GatedMLP, w: Dict[str, torch.Tensor], h: torch.Tensor, x: torch.Tensor,
-              index: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+              index: Optional[torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
     """The block in float64 without quantization (the weights w)."""
     def project(v, weight, a):
         y = v @ weight.double().t()
-        if a is not None:
+        if a is not None and index is not None:
             for i in range(a.At.shape[0]):
                 rows = index == i
-                y[rows] += a.scales[i].double() * ((v[rows] @ a.At[i].double().t()) @ a.Bt[i].double().t())
+                r = a.At.shape[1] if a.ranks is None else min(max(int(a.ranks[i]), 0), a.At.shape[1])
+                s = 1.0 if a.scales is None else float(a.scales[i])
+                y[rows] += s * ((v[rows] @ a.At[i, :r].double().t()) @ a.Bt[i, :, :r].double().t())
         return y
 
-    def rms(v, weight):
+    def norm(v, weight):
+        if mlp.norm == "layer":
+            v = v - v.mean(1, keepdim=True)
         return v / (v.square().mean(1, keepdim=True) + mlp.eps).sqrt() * weight.double()
+
+    def act(g):
+        f = torch.nn.functional
+        return {"silu": f.silu, "gelu": f.gelu, "relu": f.relu,
+                "gelu_tanh": lambda v: f.gelu(v, approximate="tanh")}[mlp.act](g)
     y = project(x.double(), w["gate_up"], mlp.gate_up.adapters)
     F = y.shape[1] // 2
-    y = project(torch.nn.functional.silu(y[:, :F]) * y[:, F:], w["down"], mlp.down.adapters)
-    out = h.double() + mlp.residual_scale * rms(y, mlp.post_weight)
-    return out, rms(out, mlp.pre_weight)
+    y = project(act(y[:, :F]) * y[:, F:], w["down"], mlp.down.adapters)
+    if mlp.post_weight is not None:
+        y = norm(y, mlp.post_weight)
+    if mlp.gate is not None:
+        y = y * mlp.gate.double()[torch.arange(y.shape[0], device=y.device) // mlp.gate_rows]
+    out = h.double() + mlp.residual_scale * y
+    return out, norm(out, mlp.pre_weight)
 
 
 def main() -> None:
