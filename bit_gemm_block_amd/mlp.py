@@ -8,8 +8,8 @@
     y += adapters of each row's request                       (adapter_add)
     h' = h + scale * gate * norm(y),  x' = norm(h')           (norm_residual)
 
-Every step enqueues on the current stream; with buffers() made once, a step
-allocates nothing and can be captured into a HIP graph.
+Every step enqueues on the current stream and can be captured into a HIP graph;
+with buffers() made once and h_out given, a step allocates nothing.
 
     python -m bit_gemm_block_amd.mlp [--tokens M] [--hidden C] [--ffn F] ...
 
@@ -102,7 +102,7 @@ class GatedMLP:
                  h_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(h', x') from the residual stream h, the normed stream x (fp16) and the
         adapter of every row (int32, outside the adapters: none).  With buffers,
-        x' is theirs."""
+        x' is theirs; h' is h_out (which may be h), a new tensor without one."""
         buf = self._none if buf is None else buf
         y = self.gate_up(x, index, buf, "gate_up")
         F = y.shape[1] // 2

@@ -8,6 +8,7 @@ import torch
 
 import test_gpu_block_seams as seams
 from bit_gemm_block_amd import block as B
+from bit_gemm_block_amd import mlp as MLP
 from oracle import block_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +112,19 @@ def test_gated_rows_and_offsets(M, F, gap):
     ref = O.activation(gr, "silu")
     assert np.all(np.abs(got[:, :F] - ref) <= seams.act_bound(gr, ref, np.float16, None))
     assert np.all(got[:, F:] == 7.0)
+
+
+def test_a_step_with_buffers_and_h_out_allocates_nothing():
+    print("mlp allocations", flush=True)
+    mlp, _ = MLP.random_block(256, 512, 3, 8)
+    h = torch.randn((9, 256), device=DEV)
+    index = torch.randint(-1, 3, (9,), dtype=torch.int32, device=DEV)
+    x, buf, out = mlp.enter(h, mlp.pre_weight), mlp.buffers(9), torch.empty_like(h)
+    want, want_x = mlp(h, x, index)
+    count = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]  # noqa: E731
+    before = count()
+    got, got_x = mlp(h, x, index, buf, out)
+    assert count() == before
+    assert got is out and torch.equal(got, want) and torch.equal(got_x, want_x)
+    got, got_x = mlp(h, x, index, buf, h)                # in place
+    assert got is h and torch.equal(h, want)
