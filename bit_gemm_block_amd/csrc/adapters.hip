@@ -67,7 +67,8 @@ constexpr int64_t kWideTileRows = 2816;
 // 64: 31.4 -> 34.0 us.
 constexpr int64_t kNarrowTiles = 64;
 // Workgroups up to which a tile's adapters are shared out among several of them
-// (tiles of one adapter leave the others with nothing to do).  x . A, 512 against
+// (tiles of one adapter leave the others with nothing to do, and a call of one adapter
+// launches them all the same: the number of adapters is not looked at).  x . A, 512 against
 // 1024: 1000 rows of eight mixed adapters, K = 4096, rank 16: 24.3 against 27.2 us;
 // 2048 rows of eight requests, rank 32: 24.4 against 26.0 us.  t . B, 1024 against
 // 2048: 300 rows of mixed adapters, N = 2048, rank 64: 12.5 against 14.5 us, 1000
@@ -135,8 +136,10 @@ struct Ranks {
 // groups of rows go to the matrix instruction (eight rows at a time in vector
 // registers: 8 rows, K = 14336, 25.7 -> 16.4 us, but one row 7.7 -> 9.9 us).
 // What bounds it: latency, a chain of index, factors and sums (one row, K = 4096,
-// rank 16: 4.0 us with its launch; 64 rows of 32 mixed adapters of rank 64: 7.4 us
-// for about 10 MB of factors).  Four or sixteen waves share K no better than eight.
+// rank 16: 3.9 us with its launch), and factors read once a tile: 64 rows of 32 mixed
+// adapters of rank up to 64 are about 46 groups of rows of 27 adapters, which read 17 MB
+// of At for 10 MB of distinct ones (8.0 us).  Four or sixteen waves share K no better
+// than eight.
 
 // Ranks j0 to j0 + 7 (those past `rank`: its last one) of adapter ad with the
 // first MR rows of `rows` (its last one again, if there are fewer), over chunks
@@ -303,10 +306,11 @@ __global__ void __launch_bounds__(64 * kRowsWaves) shrink_rows_kernel(AdapterArg
 // rate).  Three stages are in flight.  A row's 16-byte units are stored in the
 // order u ^ (row & 15), chosen by the copies' addresses, so that the reads of
 // one unit of 16 rows fall in distinct banks.
-// What bounds it: the copies, one workgroup (or two) to a compute unit (4096 rows,
-// K = 14336, rank 32: 117 MB of x in 37 us, where copies of x alone take 25 to 29;
-// tiles with rows of two adapters stream their rows twice, about 10 us of it).  Four
-// and five stages, staggered ones and non-temporal copies of x were level or slower.
+// What bounds it: the copies of the workgroups that there are.  4096 rows, K = 14336,
+// rank 32: 128 tiles of 32 rows, one to a compute unit, so that half of the chip brings
+// 117 MB of x in 38 to 42 us (copies of x alone on the same grid take 25 to 29; tiles with
+// rows of two adapters stream their rows twice, about 10 us of it).  Four and five stages,
+// staggered ones and non-temporal copies of x were level or slower.
 template <typename T, int RT, int NT, int RUN>
 __global__ void __launch_bounds__(512) shrink_stage_kernel(AdapterArgs a) {
   using F = Frag<T>;
@@ -518,9 +522,10 @@ __device__ __forceinline__ void store_out(float* row, int64_t n, int64_t N, f32x
 // of them in flight.  The dot products' parts are joined by halving: in
 // every step the lanes of a pair exchange the half of their columns that the
 // other one keeps, and a lane ends up with one column (or more, where LPC < 8).
-// What bounds it: latency up to a few MB (one row, N = 4096, rank 16: 4.0 us with its
-// launch), then the stream of Bt (64 rows of 32 mixed adapters of rank 64, N = 6144:
-// about 20 MB in 9 us).
+// What bounds it: latency up to a few MB (one row, N = 4096, rank 16: 3.9 us with its
+// launch), then the loads of Bt, which a group of rows reads for itself in every tile,
+// to the call's rank (64 rows of 32 mixed adapters of rank up to 64, N = 6144: 10.3 us
+// for 35 to 40 MB of loads, of which 15 MB are distinct and within the ranks).
 
 // Columns [n0, n0 + 512 / LPC) of rows of adapter ad (or of none: ad < 0), by one
 // wave.
@@ -741,7 +746,8 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(AdapterArgs a) {
 // at row 16 q + r, its units in the order u ^ r, so that an operand's reads fall in
 // distinct banks.  No barriers: a wave waits for its own copies.
 // What bounds it: y and out (4096 x 28672, rank 16: 940 MB in 165 to 188 us);
-// with ranks of 64 and more the passes of Bt through the L2.  Blocks of 64 rows and
+// with ranks of 64 and more the passes of Bt through the L2, one for every 16 rows
+// (4096 x 4096 -> 4096: 36 us at rank 64, 117 us at rank 256).  Blocks of 64 rows and
 // float32 products were slower (266 and 218 us where this kernel's first form took
 // 191).
 // RC: the ranks, rounded up (16, 32, ... 256).  SHARED: pass p of the tile's adapters

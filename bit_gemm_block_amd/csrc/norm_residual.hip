@@ -7,10 +7,12 @@
 // centred values (a second sum over registers, not a second read).
 //
 // What bounds it: long calls by memory (4096 x 4096, fp32 rows, fp16 x: 235 MB in
-// 44 us, 5.3 TB/s; 4096 x 16384, fp16 rows, fp32 y, a gate: 671 MB in 141 us, 4.8
-// TB/s), short ones by latency (8 x 4096: 3.8 us, of which an empty launch is 1.6):
-// a load, two or four sums over the workgroup and the parameters' loads follow
-// one another.  The parameters are not loaded before the sums: kept in registers
+// 45 us, 5.2 TB/s), up to 4096 x 16384, fp16 rows, fp32 y, a gate: 671 MB in 139 to 146
+// us, 4.6 to 4.8 TB/s, where the loads of a 16-wave workgroup, one to a compute unit,
+// pause at its sums.  Short ones by latency (8 x 4096: 3.8 to 4.0 us, of which an empty
+// launch is 1.6): a load, two or four sums over the workgroup, each of six exchanges
+// between lanes that go through LDS and a barrier, and the parameters' loads follow one
+// another.  The parameters are not loaded before the sums: kept in registers
 // they spill at 1024 threads (4096 x 16384: 150 -> 269 us), and brought early into
 // the caches they gain nothing (8 x 4096: 4.16 -> 4.25 us).
 #include "block_internal.h"
@@ -201,10 +203,12 @@ void launch_shape(const NormArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((norm_residual_kernel<WAVES, NC, EVEN, H, Y, P>), grid, block, 0, st, a);
 }
 
-// The waves that a row needs with one chunk each, two from eight waves on: four
-// waves for C <= 512 cost 10.4 us instead of 5.3 (4096 x 512), and for C = 8192
-// sixteen with one chunk 88.8 instead of 77.3; for C = 4096 four with two cost 40.4
-// instead of 39.0, and for C = 16384 eight with four 150 instead of 147.
+// The waves that a row needs with one chunk each, two from C = 4096 on.  Both sides, three
+// sets of inputs in turn: four waves for C <= 512 cost 11.8 us instead of 7.5 (4096 x
+// 512); for C = 4096 four with two chunks 4.15 instead of 3.97 (8 rows), 4.95 instead of
+// 4.74 (256) and the same 45.2 (4096); for C = 8192 sixteen with one chunk 5.07 instead
+// of 4.69 (8) and 105 instead of 86.5 (4096); for C = 16384 eight with four 6.2 instead
+// of 6.0 (8) and 146 instead of 139 (4096).
 template <typename H, typename Y, typename P>
 void launch_types(const NormArgs& a, hipStream_t st) {
   if (a.C <= 512) return launch_shape<1, 1, H, Y, P>(a, st);
