@@ -57,10 +57,11 @@ size_t w4a4_adapter_workspace_size(int64_t M, int64_t K, int64_t rank);
  *   float32, except that with 128 rows or more and fp16 factors the second
  *   product takes scales[a] t as a pair of fp16 values under powers of two per
  *   row and 32 or 64 ranks: off by 2^-22 of itself, or 2^-49 of the largest |t|
- *   of these ranks, whichever is more (float32's own rounding is 2^-24).  There an
- *   infinity among the factors in use may come out as NaN.  A row's result depends on its own inputs
- *   only (not on the other rows' values; M and index choose the order of its
- *   sums) and is the same from call to call.
+ *   of these ranks, whichever is more (float32's own rounding is 2^-24).  There
+ *   an infinity among the factors in use may come out as NaN.
+ *   A row's result depends on its own inputs only (not on the other rows'
+ *   values; M and index choose the order of its sums) and is the same from call
+ *   to call.
  *   workspace: at least w4a4_adapter_workspace_size(M, K, rank) bytes.
  */
 int w4a4_adapter_add(const void* x, int x_dtype, int64_t ldx, const void* At, const void* Bt,

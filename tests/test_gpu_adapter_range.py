@@ -54,7 +54,7 @@ def reference(y, x, At, Bt, index, scales, t_exact):
     return ref, tol + 3 * U * (np.abs(ref) + (0.0 if y is None else np.abs(y)))
 
 
-FORMS = [(M, R, dt) for M in (20, 130, 2900) for R in (16, 64, 200) for dt in ("f16", "f32")]
+FORMS = [(M, R, dt) for M in (20, 130, 1100, 2900) for R in (16, 64, 200) for dt in ("f16", "f32")]
 
 
 @pytest.mark.parametrize("M,R,dt", FORMS)
