@@ -1,0 +1,425 @@
+"""Measured cases of the operators of a decoding step.
+
+Four operators: products of a few rows with 4-bit weights and group scales,
+the activations not quantized (`qlinear_w4a16`); keys and values quantized to
+4 or 8 bits as they are written into a paged cache (`cache_write`, with its
+reading back) and read from it (`cache_read`); attention of a batch over that
+cache, in which a prefix that all sequences share is computed once for all
+(`cache_attention`).  Each case is one call on data that a serving step has in
+hand.  `run` computes it in plain torch operations, or through the package's
+entry points when `own` is set.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+# --------------------------------------------------------------------------
+# Cases
+# --------------------------------------------------------------------------
+def _linear(name, M, K, N, group, layout, x, y):
+    """group: channels that share a scale (0: one scale per output channel)."""
+    return {"name": name, "op": "qlinear_w4a16", "M": M, "K": K, "N": N, "group": group, "layout": layout, "x": x, "y": y}
+
+
+def _cache(name, op, T, heads, D, bits, page, dtype, absent):
+    """absent: the share of tokens without a slot (padding of a batch)."""
+    return {"name": name, "op": op, "T": T, "heads": heads, "D": D, "bits": bits, "page": page, "dtype": dtype,
+            "absent": absent}
+
+
+def _attention(name, S, q_lo, q_hi, heads, group, D, bits, page, lo, hi, prefix, q, out):
+    """S sequences of q_lo to q_hi new tokens each, the last of lo to hi in the
+    cache; `group` query heads share each of `heads` heads; `prefix` tokens in
+    front that all sequences share."""
+    return {"name": name, "op": "cache_attention", "S": S, "q_lo": q_lo, "q_hi": q_hi, "heads": heads, "group": group,
+            "D": D, "bits": bits, "page": page, "lo": lo, "hi": hi, "prefix": prefix, "q": q, "out": out}
+
+
+def listed():
+    return [
+        # One token of one request through the qkv projection: the smallest call.
+        _linear("linear_token", 1, 4096, 6144, 128, "tiled", "float16", "float32"),
+        # Eight decoding requests through the gate and up projection.
+        _linear("linear_gateup", 8, 4096, 28672, 128, "tiled", "float16", "float32"),
+        # A decoding batch of 64 through the down projection, one scale per channel.
+        _linear("linear_down", 64, 14336, 4096, 0, "tiled", "float16", "float16"),
+        # Odd sizes, row-major weights with small groups, float32 activations.
+        _linear("linear_odd_f32", 5, 1088, 5007, 64, "rowmajor", "float32", "float32"),
+        # The new tokens of a decoding batch of 64, straight from the projection.
+        _cache("cache_write_decode", "cache_write", 64, 8, 128, 4, 64, "float32", 0.1),
+        # The tokens of a long prompt.
+        _cache("cache_write_prompt", "cache_write", 8192, 8, 128, 4, 64, "float32", 0.0),
+        # A shared prefix of odd length read back, 8 bits, wide heads.
+        _cache("cache_read_8bit", "cache_read", 5003, 4, 256, 8, 32, "float16", 0.0),
+        # A few hundred tokens of small heads.
+        _cache("cache_read_small", "cache_read", 333, 3, 64, 4, 16, "float32", 0.0),
+        # One token of one request with a long context: few rows, a long axis.
+        _attention("attention_token", 1, 1, 1, 8, 4, 128, 4, 64, 16001, 16001, 0, "float32", "float16"),
+        # A decoding batch with contexts of every length: the memory's rate.
+        _attention("attention_decode", 64, 1, 1, 8, 4, 128, 4, 64, 300, 16384, 0, "float32", "float16"),
+        # A decoding batch behind a long system prompt that all requests share.
+        _attention("attention_prefix", 64, 1, 1, 8, 4, 128, 4, 64, 1, 600, 8192, "float32", "float16"),
+        # Chunks of prompts, odd lengths, 8 bits, small pages: the products' rate.
+        _attention("attention_chunks", 3, 37, 1021, 4, 7, 128, 8, 16, 1100, 4099, 0, "float16", "float32"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.999)))))))
+
+
+def draw(rng):
+    """One more case: any operator, sizes over the logarithm of their range."""
+    op = rng.choice(["qlinear_w4a16", "qlinear_w4a16", "cache_write", "cache_read", "cache_attention", "cache_attention",
+                     "cache_attention"])
+    if op == "qlinear_w4a16":
+        layout = rng.choice(["tiled", "tiled", "rowmajor"])
+        unit = 128 if layout == "tiled" else 64
+        K = unit * _log(rng, 1, 14336 // unit)
+        case = _linear("", _log(rng, 1, 64), K, _log(rng, 1, 28672 if K <= 4096 else 4096),
+                       rng.choice([g for g in (0, unit, 128, 256, 512) if K % max(g, 1) == 0]), layout,
+                       rng.choice(["float16", "float16", "float32"]), rng.choice(["float32", "float16"]))
+    elif op != "cache_attention":
+        heads, D = _log(rng, 1, 16), rng.choice([64, 128, 128, 256])
+        case = _cache("", op, min(_log(rng, 1, 8192), 8192 * 8 * 128 // (heads * D)), heads, D, rng.choice([4, 4, 8]),
+                      rng.choice([16, 32, 64, 128]), rng.choice(["float16", "float32"]), rng.choice([0.0, 0.1]))
+    else:
+        heads, group, D, bits = rng.choice([1, 2, 4, 8, 8, 12]), rng.choice([1, 2, 4, 4, 7, 8]), rng.choice([64, 128, 128, 256]), rng.choice([4, 4, 8])
+        kind = rng.choice(["decode", "decode", "prefix", "draft", "chunks"])
+        hi = _log(rng, 64, 16384)
+        lo = _log(rng, 16, hi)
+        S = _log(rng, 1, max(1, min(64, 4_000_000 // (hi * heads * D * bits // 512))))
+        q_lo, q_hi, prefix = 1, 1, 0
+        if kind == "prefix":
+            prefix, hi = _log(rng, 64, 8192), min(hi, 1024)
+            lo = min(lo, hi)
+        elif kind == "draft":
+            q_hi = _log(rng, 2, 8)
+        elif kind == "chunks":
+            S, hi = min(S, 4), min(hi, 4096)
+            q_hi = _log(rng, 16, min(1024, hi))
+            lo = min(max(lo, q_hi), hi)
+        case = _attention("", S, q_lo, q_hi, heads, group, D, bits, rng.choice([16, 32, 64, 128]), lo, hi, prefix,
+                          rng.choice(["float32", "float16"]), rng.choice(["float16", "float32"]))
+        while work(case)["flops"] > 28e9:  # below the largest listed case
+            case["q_hi"] = max(1, case["q_hi"] * 2 // 3)
+    del case["name"]
+    return case
+
+
+# --------------------------------------------------------------------------
+# Inputs
+# --------------------------------------------------------------------------
+def _dt(name):
+    return getattr(torch, name)
+
+
+def _spread(lo, hi, n):
+    """n whole numbers from lo to hi, evenly apart."""
+    return [hi if n == 1 else lo + (hi - lo) * i // (n - 1) for i in range(n)]
+
+
+def _lengths(case):
+    """(new tokens, tokens in the cache) of every sequence, before their order is drawn."""
+    q = _spread(case["q_lo"], case["q_hi"], case["S"])
+    return [(n, max(n, L)) for n, L in zip(q[::-1] if case["S"] % 2 else q, _spread(case["lo"], case["hi"], case["S"]))]
+
+
+def _pack(q, bits):
+    """Whole numbers to the cache's and the weights' bytes, the even element low."""
+    if bits == 8:
+        return q.to(torch.int8).view(torch.uint8)
+    q = q.to(torch.int32) & 15
+    return (q[..., 0::2] | (q[..., 1::2] << 4)).to(torch.uint8)
+
+
+def _unpack(codes, bits):
+    """Those bytes as float32."""
+    if bits == 8:
+        return codes.view(torch.int8).float()
+    b = codes.to(torch.int16)
+    q = torch.stack((b & 15, b >> 4), dim=-1).flatten(-2)
+    return torch.where(q > 7, q - 16, q).float()
+
+
+def _quantize(x, bits):
+    """Codes and scales of rows: s = max|x| / qmax, codes rint(x / s).  Scale and
+    quotient are float32, rounded once: next to a border half an ulp is a code."""
+    qmax = 7.0 if bits == 4 else 127.0
+    s = (x.abs().amax(dim=-1).double() / qmax).float()
+    q = torch.clamp(torch.round((x.double() / s.double()[..., None]).float()), -qmax, qmax)
+    return torch.where(s[..., None] > 0, q, 0.0), s
+
+
+def _keys(gen, shape, gain):
+    """Keys or values: normal, two channels of a head larger by `gain`."""
+    x = torch.randn(shape, generator=gen, device=DEV)
+    x[..., 7::shape[-1] // 2] *= gain
+    return x
+
+
+def _filled(gen, pages, case):
+    """A cache of `pages` pages: codes and scales of keys and values."""
+    out = []
+    shape = (pages, case["heads"], case["page"], case["D"])
+    for gain in (4.0, 1.0):
+        codes = torch.empty(shape[:3] + (case["D"] * case["bits"] // 8,), dtype=torch.uint8, device=DEV)
+        scale = torch.empty(shape[:3], device=DEV)
+        step = max(1, (1 << 26) // (shape[1] * shape[2] * shape[3]))
+        for p in range(0, pages, step):
+            q, scale[p:p + step] = _quantize(_keys(gen, (min(step, pages - p),) + shape[1:], gain), case["bits"])
+            codes[p:p + step] = _pack(q, case["bits"])
+        out.append((codes, scale))
+    return {"k": out[0][0], "k_scale": out[0][1], "v": out[1][0], "v_scale": out[1][1]}
+
+
+def _tile(wq):
+    """Row-major bytes [N, K / 2] to tiles of 16 rows and 128 channels (1 KB each,
+    16 bytes of a row together, rows inside)."""
+    N, B = wq.shape
+    pad = torch.zeros((-N % 16, B), dtype=torch.uint8, device=wq.device)
+    t = torch.cat((wq, pad)).reshape(-1, 16, B // 64, 4, 16)
+    return t.permute(0, 2, 3, 1, 4).contiguous().reshape(-1, B)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    host = torch.Generator().manual_seed(seed * 3 + 1)
+    s = dict(case)
+    if case["op"] == "qlinear_w4a16":
+        M, K, N, group = case["M"], case["K"], case["N"], case["group"]
+        x = torch.randn((M, K), generator=gen, device=DEV)
+        x[:, 7 % K::max(1, K // 4)] *= 30.0  # four massive channels
+        s["x"] = x.to(_dt(case["x"]))
+        wq = _pack(torch.clamp(torch.round(2.5 * torch.randn((N, K), generator=gen, device=DEV)), -7, 7), 4)
+        s["wq"] = _tile(wq) if case["layout"] == "tiled" else wq
+        scale = (0.5 + torch.rand((N, K // group) if group else (N,), generator=gen, device=DEV)) * 0.4 * K ** -0.5
+        s["w_scale"] = scale.to(torch.float16)
+        return s
+    if case["op"] == "cache_attention":
+        lens = _lengths(case)
+        lens = [lens[i] for i in torch.randperm(len(lens), generator=host).tolist()]
+        s["lens"], page = lens, case["page"]
+        need = [-(-L // page) for _, L in lens]
+        front = -(-case["prefix"] // page)
+        order = torch.randperm(sum(need) + front + 3, generator=host).to(torch.int32)  # a pool that others use too
+        tables = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+        at = front
+        for i, n in enumerate(need):
+            tables[i, :n] = order[at:at + n]
+            at += n
+        s.update(_filled(gen, len(order), case))
+        s["tables"] = tables.to(DEV)
+        s["lengths"] = torch.tensor([L for _, L in lens], dtype=torch.int32, device=DEV)
+        starts = [0]
+        for n, _ in lens:
+            starts.append(starts[-1] + n)
+        s["starts"] = starts
+        s["max_q"] = max(n for n, _ in lens)
+        s["q_start"] = torch.tensor(starts, dtype=torch.int32, device=DEV) if s["max_q"] > 1 else None
+        s["prefix_table"] = order[:front].to(DEV) if front else None
+        s["prefix_length"] = torch.tensor([case["prefix"]], dtype=torch.int32, device=DEV) if front else None
+        q = torch.randn((starts[-1], case["heads"] * case["group"] * case["D"]), generator=gen, device=DEV)
+        s["q"] = (1.5 * q).to(_dt(case["q"]))
+    else:
+        T, heads, D, page = case["T"], case["heads"], case["D"], case["page"]
+        pages = -(-T // page) + 3
+        slots = torch.randperm(pages * page, generator=host)[:T].to(torch.int32)
+        if T >= 256:  # long runs lie in whole pages, in any order
+            run = torch.randperm(pages, generator=host)[:-(-T // page)]
+            slots = (run[:, None] * page + torch.arange(page)).flatten()[:T].to(torch.int32)
+        gone = int(case["absent"] * T)
+        if gone:
+            slots[torch.randperm(T, generator=host)[:gone]] = -1
+        s["slots"] = slots.to(DEV)
+        s["slots64"] = slots.long().to(DEV)
+        s.update(_filled(gen, pages, case))
+        if case["op"] == "cache_write":
+            both = torch.cat((_keys(gen, (T, heads, D), 4.0).flatten(1), _keys(gen, (T, heads, D), 1.0).flatten(1)), dim=1)
+            both = both.to(_dt(case["dtype"]))  # the projection's columns, taken as they lie
+            s["new_k"], s["new_v"] = both[:, :heads * D], both[:, heads * D:]
+    if own:
+        from bit_gemm_block_amd import decode
+        s["cache"] = decode.KVCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
+    return s
+
+
+# --------------------------------------------------------------------------
+# One pass
+# --------------------------------------------------------------------------
+def _plain_linear(s):
+    wq, (M, K), N = s["wq"], s["x"].shape, s["N"]
+    if s["layout"] == "tiled":
+        wq = wq.reshape(-1, K // 128, 4, 16, 16).permute(0, 3, 1, 2, 4).reshape(-1, K // 2)[:N]
+    w = _unpack(wq, 4).reshape(N, -1, s["group"] or K) * s["w_scale"].float().reshape(N, -1, 1)
+    return (s["x"].float() @ w.reshape(N, K).t()).to(_dt(s["y"]))
+
+
+def _plain_read(s):
+    """The values at the slots, zero where a token has none."""
+    page, have = s["page"], (s["slots64"] >= 0)[:, None, None]
+    at = s["slots64"].clamp(min=0)
+    out = {}
+    for name in ("k", "v"):
+        codes = s[name][at // page, :, at % page]
+        v = _unpack(codes, s["bits"]) * s[name + "_scale"][at // page, :, at % page][..., None]
+        out[name] = torch.where(have, v, 0.0).flatten(1).to(_dt(s["dtype"]))
+    return out
+
+
+def _plain_write(s):
+    page, at = s["page"], s["slots64"]
+    rows = torch.nonzero(at >= 0).flatten()
+    at = at[rows]
+    for name in ("k", "v"):
+        x = s["new_" + name].float().reshape(s["T"], s["heads"], s["D"])[rows]
+        q, scale = _quantize(x, s["bits"])
+        s[name][at // page, :, at % page] = _pack(q, s["bits"])
+        s[name + "_scale"][at // page, :, at % page] = scale
+
+
+def _plain_tokens(s, name, table, length):
+    """The first `length` tokens of a table's pages, [heads, length, D]."""
+    n = -(-length // s["page"])
+    p = table[:n].long()
+    codes = s[name][p].transpose(0, 1).flatten(1, 2)[:, :length]
+    scale = s[name + "_scale"][p].transpose(0, 1).flatten(1, 2)[:, :length]
+    return _unpack(codes, s["bits"]) * scale[..., None]
+
+
+def _plain_attention(s):
+    H, G, D, P = s["heads"], s["group"], s["D"], s["prefix"]
+    out = torch.empty((s["starts"][-1], H * G * D), dtype=_dt(s["out"]), device=DEV)
+    front = [_plain_tokens(s, name, s["prefix_table"], P) for name in ("k", "v")] if P else None
+    for i, (n, L) in enumerate(s["lens"]):
+        k, v = (_plain_tokens(s, name, s["tables"][i], L) for name in ("k", "v"))
+        if front:
+            k, v = torch.cat((front[0], k), dim=1), torch.cat((front[1], v), dim=1)
+        a, b = s["starts"][i], s["starts"][i + 1]
+        q = s["q"][a:b].float().reshape(n, H, G, D).permute(1, 2, 0, 3).reshape(H, G * n, D)
+        t = (q @ k.transpose(1, 2)) * D ** -0.5
+        if n > 1:
+            past = torch.arange(P + L, device=DEV) > P + L - n + torch.arange(n, device=DEV)[:, None]
+            t = t.masked_fill(past.repeat(G, 1), float("-inf"))
+        t = torch.exp(t - t.amax(dim=-1, keepdim=True))
+        o = (t @ v) / t.sum(dim=-1, keepdim=True)
+        out[a:b] = o.reshape(H, G, n, D).permute(2, 0, 1, 3).reshape(n, H * G * D).to(out.dtype)
+    return out
+
+
+def run(s):
+    if not own:
+        if s["op"] == "qlinear_w4a16":
+            return _plain_linear(s)
+        if s["op"] == "cache_attention":
+            return _plain_attention(s)
+        if s["op"] == "cache_write":
+            _plain_write(s)
+        return _plain_read(s)
+    from bit_gemm_block_amd import decode
+    if s["op"] == "qlinear_w4a16":
+        return decode.qlinear_w4a16(s["x"], s["wq"], s["w_scale"], s["group"], w_layout=s["layout"], out_dtype=_dt(s["y"]))
+    if s["op"] == "cache_attention":
+        return decode.cache_attention(s["q"], s["cache"], s["tables"], s["lengths"], q_start=s["q_start"],
+                                      max_q=s["max_q"], prefix_table=s["prefix_table"], prefix_length=s["prefix_length"],
+                                      out_dtype=_dt(s["out"]))
+    if s["op"] == "cache_write":
+        decode.cache_write(s["cache"], s["new_k"], s["new_v"], s["slots"])
+    k, v = decode.cache_read(s["cache"], s["slots"], out_dtype=_dt(s["dtype"]))
+    return {"k": k, "v": v}
+
+
+# --------------------------------------------------------------------------
+# What a pass cannot do without, and its result in 64 bits
+# --------------------------------------------------------------------------
+def work(case):
+    size = {"float32": 4, "float16": 2}
+    if case["op"] == "qlinear_w4a16":
+        M, K, N = case["M"], case["K"], case["N"]
+        scales = N * (K // case["group"] if case["group"] else 1)
+        return {"bytes": N * K // 2 + 2 * scales + M * K * size[case["x"]] + M * N * size[case["y"]], "flops": 2 * M * N * K}
+    heads, D = case["heads"], case["D"]
+    row = 2 * heads * (D * case["bits"] // 8 + 4)  # of a token in the cache
+    if case["op"] != "cache_attention":
+        T, values = case["T"], 2 * heads * D
+        have = T - int(case["absent"] * T)
+        if case["op"] == "cache_read":
+            return {"bytes": 4 * T + have * row + T * values * size[case["dtype"]], "flops": have * values}
+        return {"bytes": 4 * T + have * 2 * row + (have + T) * values * size[case["dtype"]], "flops": 4 * have * values}
+    lens, P, rows = _lengths(case), case["prefix"], case["group"] * heads
+    tokens = sum(n for n, _ in lens)
+    seen = sum(n * (P + L) - n * (n - 1) // 2 for n, L in lens)
+    return {"bytes": (P + sum(L for _, L in lens)) * row + tokens * rows * D * (size[case["q"]] + size[case["out"]]),
+            "flops": 4 * seen * rows * D}
+
+
+def _exact_codes(codes, bits):
+    """Bytes as whole numbers in 64 bits."""
+    b = codes.to(torch.int64)
+    if bits == 8:
+        return b - 256 * (b >= 128)
+    b = torch.stack((b % 16, b // 16), dim=-1).flatten(-2)
+    return b - 16 * (b >= 8)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "qlinear_w4a16":
+        K, N, group = case["K"], case["N"], case["group"] or case["K"]
+        out = torch.empty((case["M"], N), dtype=torch.float64, device=DEV)
+        x, scale = s["x"].double(), s["w_scale"].double().reshape(N, -1)
+        for n in range(0, N, 1024):
+            hi = min(N, n + 1024)
+            if case["layout"] == "tiled":  # row n is in block n / 16; 16 of its bytes every 256 of the block's
+                r = torch.arange(n, hi, device=DEV)
+                blocks = s["wq"].reshape(-1, K // 32, 16, 16)
+                codes = blocks[r // 16, :, r % 16].reshape(hi - n, K // 2)
+            else:
+                codes = s["wq"][n:hi]
+            w = _exact_codes(codes, 4).double() * torch.repeat_interleave(scale[n:hi], group, dim=1)
+            out[:, n:hi] = (w @ x.t().contiguous()).t()
+        return out
+    if case["op"] == "cache_attention":
+        H, G, D, page, P = case["heads"], case["group"], case["D"], case["page"], case["prefix"]
+        out = torch.empty((s["starts"][-1], H * G * D), dtype=torch.float64, device=DEV)
+
+        def values(name, h, pages, offsets):
+            return _exact_codes(s[name][pages, h, offsets], case["bits"]).double() * s[name + "_scale"][pages, h, offsets].double()[:, None]
+
+        for i, (n, L) in enumerate(s["lens"]):
+            at = torch.arange(L, device=DEV)
+            pages, offsets = s["tables"][i].long()[at // page], at % page
+            if P:
+                at = torch.arange(P, device=DEV)
+                pages = torch.cat((s["prefix_table"].long()[at // page], pages))
+                offsets = torch.cat((at % page, offsets))
+            limit = torch.arange(P + L - n, P + L, device=DEV)[:, None, None]
+            hidden = torch.arange(P + L, device=DEV) > limit
+            a, b = s["starts"][i], s["starts"][i + 1]
+            for h in range(H):
+                k, v = values("k", h, pages, offsets), values("v", h, pages, offsets)
+                q = s["q"][a:b, h * G * D:(h + 1) * G * D].double().reshape(n * G, D)
+                t = ((q @ k.t().contiguous()) / math.sqrt(D)).reshape(n, G, P + L)
+                p = torch.softmax(t.masked_fill(hidden, float("-inf")), dim=-1).reshape(n * G, P + L)
+                out[a:b, h * G * D:(h + 1) * G * D] = (p @ v).reshape(n, G * D)
+        return out
+    slots = s["slots64"]
+    out = {}
+    for name in ("k", "v"):
+        if case["op"] == "cache_write":
+            x = s["new_" + name].double().reshape(case["T"], case["heads"], case["D"])
+            top = 2 ** (case["bits"] - 1) - 1
+            scale = (x.abs().max(dim=2, keepdim=True).values / top).float().double()  # the scale and the quotient are float32 by definition
+            v = torch.clamp(torch.round((x / scale).float()), -top, top).double() * scale
+        else:
+            at = slots.clamp(min=0)
+            pages, offsets = at // case["page"], at % case["page"]
+            v = _exact_codes(s[name][pages, :, offsets], case["bits"]).double() * s[name + "_scale"][pages, :, offsets].double()[..., None]
+        v[slots < 0] = 0.0
+        out[name] = v.reshape(case["T"], -1)
+    return out
