@@ -245,7 +245,7 @@ def prepare(case, seed):
             s["new_k"], s["new_v"] = both[:, :heads * D], both[:, heads * D:]
     if own:
         from bit_gemm_block_amd import decode
-        s["cache"] = decode.KVCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
+        s["cache"] = decode.KVCache(s["k"], s["v"], s["k_scale"], s["v_scale"], s["bits"])
     return s
 
 
