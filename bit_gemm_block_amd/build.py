@@ -1,6 +1,6 @@
 """Builds libw4a4.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and,
 where torch is installed, _block.so, the Python binding of its operators beside
-the layer (host code against torch's headers).
+the layer and of a decoding step (host code against torch's headers).
 
     python -m bit_gemm_block_amd.build
 """
@@ -21,7 +21,9 @@ LIB = os.path.join(PKG, "libw4a4.so")
 BINDING = os.path.join(PKG, "_block.so")
 
 SOURCES = ["api.cpp", "rotq.hip", "rotq_mfma.hip", "qgemm.hip", "qgemm_f6.hip", "lowrank.hip", "offq.hip",
-           "noalloc.hip", "block_api.cpp", "adapters.hip", "norm_residual.hip", "gated.hip"]
+           "noalloc.hip", "block_api.cpp", "adapters.hip", "norm_residual.hip", "gated.hip",
+           "decode_api.cpp", "w4a16.hip", "cache.hip", "attention.hip", "attention_d64.hip", "attention_d128.hip",
+           "attention_d256.hip"]
 
 # No fast-math and no denormal flushing: the quantizer's float32 division and
 # rounding must follow IEEE.  Packed-FP32 instructions are disabled.

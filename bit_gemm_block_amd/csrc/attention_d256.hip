@@ -1,0 +1,12 @@
+// attention_d256.hip — attention_kernel.h for heads of 256 channels (a file each, so
+// that they compile side by side).
+#include "attention_kernel.h"
+
+namespace w4a4 {
+
+void launch_attention_256(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
+                         hipStream_t st) {
+  launch_head_dim<256>(a, c, front, slot0, slots, pair, st);
+}
+
+}  // namespace w4a4

@@ -1,5 +1,5 @@
-// block_binding.cpp — the Python binding of include/w4a4_block.h: checks of the
-// tensors, allocation of the outputs that are not given, and the calls on the
+// block_binding.cpp — the Python binding of include/w4a4_block.h and
+// include/w4a4_decode.h: checks of the tensors, allocation of the outputs that are not given, and the calls on the
 // tensors' current stream.  No arithmetic.  It is compiled against torch
 // because a call's host time is what a small call costs: through ctypes the
 // marshalling of these argument lists took 5 to 8 us beside the launch's 3.
@@ -8,10 +8,12 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
 
 #include "w4a4_block.h"
+#include "w4a4_decode.h"
 
 namespace {
 
@@ -206,6 +208,157 @@ Tensor gated_activation(const Tensor& gate, const OptTensor& up, int act, at::Sc
   return *out;
 }
 
+// ---- operators of a decoding step ---------------------------------------------
+
+// The address of a given contiguous workspace, or of a new one.
+void* workspace_of(OptTensor& workspace, const Tensor& like, size_t need, int64_t dev, size_t* bytes) {
+  if (workspace) {
+    on_device(*workspace, "workspace", dev);
+    if (!workspace->is_contiguous()) throw py::value_error("workspace must be contiguous");
+  } else if (need > 0) {
+    workspace = empty(like, {static_cast<int64_t>(need)}, at::kByte);
+  }
+  *bytes = workspace ? workspace->nbytes() : 0;
+  return workspace ? workspace->data_ptr() : nullptr;
+}
+
+Tensor qlinear_w4a16(const Tensor& x, const Tensor& wq, const Tensor& w_scale, int64_t w_group, int layout,
+                     at::ScalarType out_dtype, OptTensor out, OptTensor workspace) {
+  const int64_t dev = device_index(x);
+  if (x.dim() != 2) throw py::value_error("x must be a matrix");
+  const int64_t M = x.size(0), K = x.size(1);
+  const int64_t ldx = rows(x, "x", dev, M, K);
+  const int xd = dtype_of(x.scalar_type()), sd = dtype_of(w_scale.scalar_type());
+  if (w_scale.dim() != (w_group > 0 ? 2 : 1)) throw py::value_error("w_scale must be [N] or, with w_group, [N, K / w_group]");
+  const int64_t N = w_scale.size(0);
+  if (w_group > 0 && K % w_group != 0) throw py::value_error("w_group must divide K");
+  const void* sw = w_group > 0 ? whole(w_scale, "w_scale", dev, w_scale.scalar_type(), {N, K / w_group})
+                               : whole(w_scale, "w_scale", dev, w_scale.scalar_type(), {N});
+  const int64_t wrows = layout == W4A4_WEIGHTS_ROWMAJOR ? N : (N + 15) / 16 * 16;
+  const void* w = whole(wq, "wq", dev, at::kByte, {wrows, K / 2});
+  const int od = dtype_of(out ? out->scalar_type() : out_dtype);
+  const c10::DeviceGuard guard(x.device());
+  int64_t ldo = N;
+  if (out)
+    ldo = rows(*out, "out", dev, M, N);
+  else
+    out = empty(x, {M, N}, out_dtype);
+  size_t bytes = 0;
+  void* ws = workspace_of(workspace, x, w4a16_qlinear_workspace_size(M, N, K), dev, &bytes);
+  check("qlinear_w4a16", w4a16_qlinear_forward(x.data_ptr(), xd, ldx, static_cast<const uint8_t*>(w), layout, sw, sd, M,
+                                               N, K, w_group, out->data_ptr(), od, ldo, ws, bytes, stream_of(dev)));
+  return *out;
+}
+
+// The cache that four tensors make.
+w4a4_cache cache_of(const Tensor& k, const Tensor& v, const Tensor& k_scale, const Tensor& v_scale, int bits,
+                    int64_t dev) {
+  if (k.dim() != 4) throw py::value_error("the cache's k must be [pages, heads, page_size, head_dim * bits / 8]");
+  if (bits != 4 && bits != 8) throw py::value_error("bits must be 4 or 8");
+  w4a4_cache c{};
+  c.k = static_cast<uint8_t*>(whole(k, "the cache's k", dev, at::kByte, k.sizes()));
+  c.v = static_cast<uint8_t*>(whole(v, "the cache's v", dev, at::kByte, k.sizes()));
+  const at::IntArrayRef rows3 = k.sizes().slice(0, 3);
+  c.k_scale = static_cast<float*>(whole(k_scale, "the cache's k_scale", dev, at::kFloat, rows3));
+  c.v_scale = static_cast<float*>(whole(v_scale, "the cache's v_scale", dev, at::kFloat, rows3));
+  c.pages = k.size(0);
+  c.heads = k.size(1);
+  c.page_size = k.size(2);
+  c.head_dim = k.size(3) * 8 / bits;
+  c.bits = bits;
+  return c;
+}
+
+void cache_write(const Tensor& kc, const Tensor& vc, const Tensor& ks, const Tensor& vs, int bits, const Tensor& k,
+                 const Tensor& v, const Tensor& slots) {
+  const int64_t dev = device_index(kc);
+  const w4a4_cache c = cache_of(kc, vc, ks, vs, bits, dev);
+  if (k.dim() != 2) throw py::value_error("k and v must be matrices");
+  const int64_t T = k.size(0), C = c.heads * c.head_dim;
+  const int64_t ldk = rows(k, "k", dev, T, C), ldv = rows(v, "v", dev, T, C);
+  if (k.scalar_type() != v.scalar_type()) throw py::type_error("k and v must have one dtype");
+  const int dt = dtype_of(k.scalar_type());
+  const void* ix = whole(slots, "slots", dev, at::kInt, {T});
+  const c10::DeviceGuard guard(kc.device());
+  check("cache_write", w4a4_cache_write(&c, k.data_ptr(), ldk, v.data_ptr(), ldv, dt, static_cast<const int32_t*>(ix),
+                                        T, stream_of(dev)));
+}
+
+std::pair<OptTensor, OptTensor> cache_read(const Tensor& kc, const Tensor& vc, const Tensor& ks, const Tensor& vs,
+                                           int bits, const Tensor& slots, at::ScalarType dtype, OptTensor k,
+                                           OptTensor v, bool want_k, bool want_v) {
+  const int64_t dev = device_index(kc);
+  const w4a4_cache c = cache_of(kc, vc, ks, vs, bits, dev);
+  if (slots.dim() != 1) throw py::value_error("slots must be a vector");
+  const int64_t T = slots.size(0), C = c.heads * c.head_dim;
+  const void* ix = whole(slots, "slots", dev, at::kInt, {T});
+  const at::ScalarType dt = k ? k->scalar_type() : v ? v->scalar_type() : dtype;
+  const int d = dtype_of(dt);
+  const c10::DeviceGuard guard(kc.device());
+  int64_t ld[2] = {C, C};
+  auto take = [&](OptTensor& t, const char* name, bool want, int64_t* l) {
+    if (t) {
+      if (t->scalar_type() != dt) throw py::type_error("k and v must have one dtype");
+      *l = rows(*t, name, dev, T, C);
+    } else if (want) {
+      t = empty(kc, {T, C}, dt);
+    }
+  };
+  take(k, "k", want_k, &ld[0]);
+  take(v, "v", want_v, &ld[1]);
+  check("cache_read", w4a4_cache_read(&c, static_cast<const int32_t*>(ix), T, k ? k->data_ptr() : nullptr, ld[0],
+                                      v ? v->data_ptr() : nullptr, ld[1], d, stream_of(dev)));
+  return {k, v};
+}
+
+Tensor cache_attention(const Tensor& q, const Tensor& kc, const Tensor& vc, const Tensor& ks, const Tensor& vs,
+                       int bits, const Tensor& tables, const Tensor& lengths, const OptTensor& q_start, int64_t max_q,
+                       bool causal, const OptTensor& prefix_table, const OptTensor& prefix_length,
+                       std::optional<double> scale, at::ScalarType out_dtype, OptTensor out, OptTensor workspace) {
+  const int64_t dev = device_index(kc);
+  const w4a4_cache c = cache_of(kc, vc, ks, vs, bits, dev);
+  if (q.dim() != 2 || c.head_dim <= 0 || q.size(1) % c.head_dim != 0)
+    throw py::value_error("q must be [tokens, heads * head_dim]");
+  const int64_t T = q.size(0), C = q.size(1);
+  const int64_t ldq = rows(q, "q", dev, T, C);
+  const int qd = dtype_of(q.scalar_type());
+  if (tables.dim() != 2) throw py::value_error("tables must be [sequences, pages]");
+  const int64_t S = tables.size(0), width = tables.size(1);
+  const void* tb = whole(tables, "tables", dev, at::kInt, {S, width});
+  const void* ln = whole(lengths, "lengths", dev, at::kInt, {S});
+  const void* qs = q_start ? whole(*q_start, "q_start", dev, at::kInt, {S + 1}) : nullptr;
+  if (!q_start && (max_q != 1 || T < S))
+    throw py::value_error("without q_start every sequence has one row of q, and max_q is 1");
+  if (prefix_table.has_value() != prefix_length.has_value())
+    throw py::value_error("prefix_table and prefix_length go together");
+  int64_t P = 0;
+  const void *pt = nullptr, *pl = nullptr;
+  if (prefix_table) {
+    if (prefix_table->dim() != 1) throw py::value_error("prefix_table must be a vector");
+    P = prefix_table->size(0);
+    pt = whole(*prefix_table, "prefix_table", dev, at::kInt, {P});
+    pl = whole(*prefix_length, "prefix_length", dev, at::kInt, {1});
+    if (P == 0) pt = pl = nullptr;  // an empty prefix
+  }
+  const int od = dtype_of(out ? out->scalar_type() : out_dtype);
+  const c10::DeviceGuard guard(kc.device());
+  int64_t ldo = C;
+  if (out)
+    ldo = rows(*out, "out", dev, T, C);
+  else
+    out = empty(q, {T, C}, out_dtype);
+  size_t bytes = 0;
+  void* ws = workspace_of(workspace, q, w4a4_cache_attention_workspace_size(&c, T, C / c.head_dim, S, width, max_q, P),
+                          dev, &bytes);
+  const double sc = scale ? *scale : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
+  check("cache_attention",
+        w4a4_cache_attention(&c, q.data_ptr(), qd, ldq, T, C / c.head_dim, static_cast<const int32_t*>(tb), S, width,
+                             static_cast<const int32_t*>(ln), static_cast<const int32_t*>(qs), max_q, causal,
+                             static_cast<const int32_t*>(pt), P, static_cast<const int32_t*>(pl),
+                             static_cast<float>(sc), out->data_ptr(), od, ldo, ws, bytes, stream_of(dev)));
+  return *out;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_block, m) {
@@ -213,4 +366,8 @@ PYBIND11_MODULE(_block, m) {
   m.def("adapter_add", &adapter_add);
   m.def("norm_residual", &norm_residual);
   m.def("gated_activation", &gated_activation);
+  m.def("qlinear_w4a16", &qlinear_w4a16);
+  m.def("cache_write", &cache_write);
+  m.def("cache_read", &cache_read);
+  m.def("cache_attention", &cache_attention);
 }
