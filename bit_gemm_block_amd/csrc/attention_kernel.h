@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
 #pragma unroll
     for (int t = 0; t < R; ++t) {
       float x[8], p[8], wt[8], sum, top;
+      uint32_t hidden = 0;
       auto weigh = [&]() {
         sum = 0.f;
         top = 0.f;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
         if (partly) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (x[i] == kNone) p[i] = wt[i] = 0.f;
+            if (hidden >> i & 1) p[i] = wt[i] = 0.f;  // whatever the scales there are
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -385,7 +386,10 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int tok = tok0 + 16 * (i / 4) + 4 * g + i % 4;
-          if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) x[i] = kNone;
+          if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) {
+            x[i] = kNone;
+            hidden |= 1u << i;
+          }
         }
       }
       weigh();

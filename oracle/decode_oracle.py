@@ -11,7 +11,7 @@ def unpack(codes, bits):
     if bits == 8:
         return codes.view(np.int8).astype(np.int64)
     lo, hi = codes & 15, codes >> 4
-    q = np.stack((lo, hi), axis=-1).reshape(codes.shape[:-1] + (-1,)).astype(np.int64)
+    q = np.stack((lo, hi), axis=-1).reshape(codes.shape[:-1] + (2 * codes.shape[-1],)).astype(np.int64)
     return np.where(q > 7, q - 16, q)
 
 
