@@ -67,8 +67,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttentionArgs a, At
   top = reduce(top, true);
   float sum = 0.f;
   for (int k = threadIdx.x; k < n; k += 256) {
-    const float ref = stats[2 * slot(k)];
-    const float f = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - top);
+    const float f = __builtin_amdgcn_exp2f(stats[2 * slot(k)] - top);
     weight[k] = f;
     sum += f * stats[2 * slot(k) + 1];
   }

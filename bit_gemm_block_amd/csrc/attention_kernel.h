@@ -23,6 +23,8 @@
 // exchanges nothing between lanes and rescales nothing.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_internal.h"
 #include "int4_operands.h"
 #include "vec_io.h"
@@ -37,8 +39,8 @@ __host__ __device__ inline int64_t least64(int64_t a, int64_t b) { return a < b 
 
 // Parts in use of a range of L tokens.
 __host__ __device__ inline int parts_of(int64_t L, int parts, int least) {
-  const int64_t p = (L + least - 1) / least;
-  return static_cast<int>(p < 1 ? 1 : p < parts ? p : parts);
+  const uint32_t p = (static_cast<uint32_t>(L) + least - 1) / static_cast<uint32_t>(least);  // L below 2^30 + 1
+  return static_cast<int>(p < 1 ? 1 : p < static_cast<uint32_t>(parts) ? p : parts);
 }
 
 // What a sequence (own tokens) or the prefix is to its queries.
@@ -89,57 +91,6 @@ __device__ __forceinline__ Span front_span(const AttentionArgs& a) {
   return p;
 }
 
-// Codes and scales of a step: tokens 4 g + i of halves a and b.
-template <int D, int BITS>
-struct StepData {
-  static constexpr int RB = D * BITS / 8;  // bytes of a row
-  static constexpr int KW = RB / 16;       // words of K a lane holds of its token
-  static constexpr int VW = RB >= 64 ? RB / 64 : 1;
-  uint32_t k[2][KW];
-  uint32_t v[8][VW];
-  f4 ks[2], vs[2];
-
-  // rb: the cache rows of the two halves' first tokens.
-  __device__ __forceinline__ void load(const AttentionArgs& a, const int64_t* rb, int r, int g) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* kp = a.k + (rb[h] + r) * RB + g * (RB / 4);
-      if constexpr (KW == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(kp);
-        k[h][0] = w.x;
-        k[h][1] = w.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < KW; i += 4) {
-          const u4 w = *reinterpret_cast<const u4*>(kp + 4 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) k[h][i + e] = w[e];
-        }
-      }
-      ks[h] = *reinterpret_cast<const f4*>(a.ks + rb[h] + 4 * g);
-      vs[h] = *reinterpret_cast<const f4*>(a.vs + rb[h] + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* vp = a.v + (rb[h] + 4 * g + i) * RB + r * (RB / 16);
-        uint32_t* d = v[4 * h + i];
-        if constexpr (RB == 32) {
-          d[0] = *reinterpret_cast<const uint16_t*>(vp);
-        } else if constexpr (VW == 1) {
-          d[0] = *reinterpret_cast<const uint32_t*>(vp);
-        } else if constexpr (VW == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(vp);
-          d[0] = w.x;
-          d[1] = w.y;
-        } else {
-          const u4 w = *reinterpret_cast<const u4*>(vp);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = w[e];
-        }
-      }
-    }
-  }
-};
-
 // Bytes E and F of w (unsigned codes u = q + 128) as fp16, minus 128.
 template <int SEL>
 __device__ __forceinline__ h2 two_bytes(uint32_t w1, uint32_t w0) {
@@ -151,36 +102,131 @@ __device__ __forceinline__ h2 two_bytes(uint32_t w1, uint32_t w0) {
   return v.h - h2{1152.f16, 1152.f16};
 }
 
-// K's codes 8 j to 8 j + 7 of a lane: in the order 0 4 1 5 2 6 3 7 (4 bits) or
-// their own (8 bits).
+// Constants that stay in registers: with two literals the mask and the sign's
+// flip below would be two instructions.
+struct Masks {
+  uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
+  uint32_t key_even = 0x00080008u, key_odd = 0x00800080u;
+  uint32_t value_even = 0x64086408u, value_odd = 0x64806480u;
+  __device__ __forceinline__ Masks() {
+    asm("" : "+s"(even), "+s"(odd), "+v"(key_even), "+v"(key_odd), "+v"(value_even), "+v"(value_odd));
+  }
+};
+
+// The codes and scales of a step's keys or values, tokens 4 g + i of both halves
+// for the scales and the values, token r for the keys.
+template <int D, int BITS>
+struct StepKeys {
+  static constexpr int RB = D * BITS / 8;  // bytes of a row
+  static constexpr int KW = RB / 16;       // words of its token's row a lane holds
+  uint32_t k[2][KW];
+  f4 s[2];
+  __device__ __forceinline__ void load(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* p = a.k + rb[h] * RB + (r * RB + g * (RB / 4));
+      if constexpr (KW == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        k[h][0] = w.x;
+        k[h][1] = w.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < KW; i += 4) {
+          const u4 w = *reinterpret_cast<const u4*>(p + 4 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) k[h][i + e] = w[e];
+        }
+      }
+      s[h] = *reinterpret_cast<const f4*>(a.ks + rb[h] + 4 * g);
+    }
+  }
+};
+
+template <int D, int BITS>
+struct StepValues {
+  static constexpr int RB = D * BITS / 8;
+  static constexpr int VW = RB >= 64 ? RB / 64 : 1;  // words of each of its tokens a lane holds
+  uint32_t v[8][VW];
+  f4 s[2];
+  __device__ __forceinline__ void load(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] = *reinterpret_cast<const f4*>(a.vs + rb[h] + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = a.v + rb[h] * RB + (g * (4 * RB) + r * (RB / 16)) + i * RB;
+        uint32_t* d = v[4 * h + i];
+        if constexpr (RB == 32) {
+          d[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else if constexpr (VW == 1) {
+          d[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (VW == 2) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          d[0] = w.x;
+          d[1] = w.y;
+        } else {
+          const u4 w = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = w[e];
+        }
+      }
+    }
+  }
+};
+
+// K's codes 8 j to 8 j + 7 of a lane, unsigned, as fp16 subnormal numbers u 2^-24
+// (the bits of a small whole number are that times 2^-24): in the order
+// 0 4 1 5 2 6 3 7, the third, fourth, seventh and eighth times 16 (4 bits), or
+// in their own (8 bits).  Their offset, 8 or 128, is taken out of the product
+// by its starting value.
 template <int BITS>
-__device__ __forceinline__ h8 key_operand(const uint32_t* k, int j) {
+__device__ __forceinline__ h8 key_operand(const uint32_t* k, int j, const Masks& m) {
+  Operand o;
   if constexpr (BITS == 4) {
-    return int4_to_f16(k[j]).h;
+    const uint32_t s = k[j] >> 8;
+    o.w[0] = (k[j] & m.even) ^ m.key_even;
+    o.w[1] = (k[j] & m.odd) ^ m.key_odd;
+    o.w[2] = (s & m.even) ^ m.key_even;
+    o.w[3] = (s & m.odd) ^ m.key_odd;
   } else {
     const uint32_t a = k[2 * j] ^ 0x80808080u, b = k[2 * j + 1] ^ 0x80808080u;
-    Operand o;
-    o.p[0] = two_bytes<0x0c010c00>(a, a);
-    o.p[1] = two_bytes<0x0c030c02>(a, a);
-    o.p[2] = two_bytes<0x0c010c00>(b, b);
-    o.p[3] = two_bytes<0x0c030c02>(b, b);
-    return o.h;
+    o.w[0] = __builtin_amdgcn_perm(a, a, 0x0c010c00);
+    o.w[1] = __builtin_amdgcn_perm(a, a, 0x0c030c02);
+    o.w[2] = __builtin_amdgcn_perm(b, b, 0x0c010c00);
+    o.w[3] = __builtin_amdgcn_perm(b, b, 0x0c030c02);
   }
+  return o.h;
+}
+// The channel of the element e of such an operand, and log2 of its factor.
+template <int BITS>
+__device__ constexpr int key_channel(int e) {
+  return BITS == 4 ? (e & 1) * 4 + e / 2 : e;
+}
+template <int BITS>
+__device__ constexpr int key_factor(int e) {
+  return BITS == 4 && (e & 2) ? 4 : 0;
 }
 
-// Four channels of the eight tokens of a lane: channels 4 q to 4 q + 3 of the
-// lane's own.
+// Four channels of the eight tokens of a lane, as fp16: channels 4 q to 4 q + 3
+// of the lane's own.  (An offset of the values cannot wait like the keys': it
+// would be 8 times the sum of the weights, which the result is a small part of.)
 template <int D, int BITS>
-__device__ __forceinline__ void value_operands(const StepData<D, BITS>& s, int q, Operand* o) {
+__device__ __forceinline__ void value_operands(const StepValues<D, BITS>& s, int q, const Masks& m, Operand* o) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     if constexpr (BITS == 4) {
-      const uint32_t w0 = s.v[2 * p][q / 2] ^ 0x88888888u, w1 = s.v[2 * p + 1][q / 2] ^ 0x88888888u;
-      const uint32_t t = __builtin_amdgcn_perm(w1, w0, q % 2 ? 0x07060302u : 0x05040100u);
-      o[0].p[p] = nibbles<false>(t);
-      o[1].p[p] = nibbles<true>(t);
-      o[2].p[p] = nibbles<false>(t >> 8);
-      o[3].p[p] = nibbles<true>(t >> 8);
+      const uint32_t t =
+          __builtin_amdgcn_perm(s.v[2 * p + 1][q / 2], s.v[2 * p][q / 2], q % 2 ? 0x07060302u : 0x05040100u);
+      const uint32_t u = t >> 8;
+      o[0].w[p] = (t & m.even) ^ m.value_even;
+      o[1].w[p] = (t & m.odd) ^ m.value_odd;
+      o[2].w[p] = (u & m.even) ^ m.value_even;
+      o[3].w[p] = (u & m.odd) ^ m.value_odd;
+      const h2 off = {1032.f16, 1032.f16}, sixteenth = {0.0625f16, 0.0625f16}, off16 = {-72.f16, -72.f16};
+      o[0].p[p] -= off;
+      o[1].p[p] = __builtin_elementwise_fma(o[1].p[p], sixteenth, off16);
+      o[2].p[p] -= off;
+      o[3].p[p] = __builtin_elementwise_fma(o[3].p[p], sixteenth, off16);
     } else {
       const uint32_t w0 = s.v[2 * p][q] ^ 0x80808080u, w1 = s.v[2 * p + 1][q] ^ 0x80808080u;
       o[0].p[p] = two_bytes<0x0c040c00>(w1, w0);
@@ -198,12 +244,12 @@ __device__ __forceinline__ float exponent(float v) {
 }
 
 template <int D, int BITS, bool PAIR, int R, bool ROWS>
-__global__ void __launch_bounds__(kAttnWaves * 64, 2)
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * BITS > 512 ? 3 : 4)
     attention_kernel(AttentionArgs a, AttentionCut cut, int front, int slot0, int slots) {
   constexpr int NK = D / 32;   // instructions along a head's channels
   constexpr int NV = D / 16;   // channels of O a lane's row block holds
   constexpr int HALVES = PAIR ? 2 : 1;
-  constexpr float kNone = -INFINITY;
+  constexpr float kUnset = -1e30f;  // of a row that has seen nothing
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -223,92 +269,40 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
   if (part >= eff) return;
   const int row0 = rg * group_rows + (ROWS ? wave * kRows : 0);
 
-  // What each row sees: positions below limit.
-  auto limit_of = [&](int row) -> int64_t {
-    if (front || !a.causal) return span.length;
-    const int64_t l = span.length - span.n + row / a.group + 1;
+  // What the queries see: positions below the limit.
+  const int length = static_cast<int>(span.length);
+  auto limit_of = [&](int query) -> int {
+    if (front || !a.causal) return length;
+    const int l = length - span.n + query + 1;
     return l < 0 ? 0 : l;
   };
+  auto query_of = [&](int row) { return static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.group)); };
   int limit[R];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int row = row0 + 16 * t + r;
-    limit[t] = row < span.rows ? static_cast<int>(limit_of(row)) : 0;
+    limit[t] = row < span.rows ? limit_of(query_of(row)) : 0;
   }
-  const int last = static_cast<int>(least64(row0 + kRows, span.rows)) - 1;       // of this wave
+  const int last = (row0 + kRows < span.rows ? row0 + kRows : span.rows) - 1;  // of this wave
   const int group_last = static_cast<int>(least64(static_cast<int64_t>(rg + 1) * group_rows, span.rows)) - 1;
-  const int wave_end = last >= row0 ? static_cast<int>(limit_of(last)) : 0;
-  const int all_see = row0 + kRows <= span.rows ? static_cast<int>(limit_of(row0)) : 0;  // positions every row sees
-  const int64_t steps = (limit_of(group_last) + kStep - 1) / kStep;
-  const int begin = static_cast<int>(steps * part / eff) + (ROWS ? 0 : wave);
-  const int end = static_cast<int>(least64(steps * (part + 1) / eff, (wave_end + kStep - 1) / kStep));
+  const int wave_end = last >= row0 ? limit_of(last / a.group) : 0;
+  const int all_see = row0 + kRows <= span.rows ? limit_of(row0 / a.group) : 0;  // positions every row sees
+  const int share = static_cast<int>((static_cast<uint32_t>(limit_of(group_last / a.group) + kStep - 1) / kStep + eff - 1) /
+                                     static_cast<uint32_t>(eff));  // steps to a part
+  const int wave_steps = (wave_end + kStep - 1) / kStep;
+  const int begin = part * share + (ROWS ? 0 : wave);
+  const int end = (part + 1) * share < wave_steps ? (part + 1) * share : wave_steps;
   constexpr int kStride = ROWS ? 1 : kAttnWaves;
 
-  // The queries, in the codes' order, and each row's factor of the scores.
-  Operand q[R][NK][HALVES];
-  float c[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int row = row0 + 16 * t + r;
-    const bool have = row < span.rows;
-    const int64_t token = span.first + (have ? row / a.group : 0);
-    const int64_t at = token * a.ldq + static_cast<int64_t>(h * a.group + (have ? row % a.group : 0)) * D + g * (D / 4);
-    c[t] = a.scale * 1.4426950408889634f;
-    if constexpr (PAIR) {
-      Raw8<float> x[NK];
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < NK; ++j) {
-        if (have) x[j].load(static_cast<const float*>(a.q) + at + 8 * j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!have) x[j].set(e, 0.f);
-          m = fmaxf(m, fabsf(x[j].get(e)));
-        }
-      }
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const int up = m > 0.f && m < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;  // the row's largest below 2^14
-      c[t] = ldexpf(c[t], -up);
-#pragma unroll
-      for (int j = 0; j < NK; ++j) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int from = BITS == 4 ? (e & 1) * 4 + e / 2 : e;
-          const float v = ldexpf(x[j].get(from), up);
-          const _Float16 hi = static_cast<_Float16>(v);
-          q[t][j][0].h[e] = hi;
-          q[t][j][1].h[e] = static_cast<_Float16>(v - static_cast<float>(hi));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NK; ++j) {
-        Raw8<_Float16> x;
-        if (have) x.load(static_cast<const _Float16*>(a.q) + at + 8 * j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          q[t][j][0].h[e] = have ? x.a[BITS == 4 ? (e & 1) * 4 + e / 2 : e] : static_cast<_Float16>(0.f);
-      }
-    }
-  }
-
-  f4 o[R][NV];
-  float ref[R], l[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    ref[t] = kNone;
-    l[t] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) o[t][j] = f4{0.f, 0.f, 0.f, 0.f};
-  }
-
   // Cache rows of a step's halves, and whether their pages exist.
-  const int64_t tile_end = span.width << a.page_log2;
-  auto page_of = [&](int step, int half) -> int32_t {
-    int64_t tok = static_cast<int64_t>(step) * kStep + 16 * half;
-    tok = tok < tile_end ? tok : tile_end - 16;
-    return span.table[tok >> a.page_log2];
+  const int tile_end = static_cast<int>(span.width << a.page_log2);
+  auto pages_of = [&](int step, int32_t* page) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      int tok = step * kStep + 16 * half;
+      tok = tok < tile_end ? tok : tile_end - 16;
+      page[half] = span.table[tok >> a.page_log2];
+    }
   };
   auto rows_of = [&](int step, const int32_t* page, int64_t* rb) {
 #pragma unroll
@@ -318,92 +312,164 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
       rb[half] = ((static_cast<int64_t>(p) * a.heads + h) << a.page_log2) + off;
     }
   };
-
-  StepData<D, BITS> next;
-  int32_t page[2] = {0, 0};
+  StepKeys<D, BITS> keys;
+  StepValues<D, BITS> values;
+  int32_t page[2] = {0, 0}, ahead[2] = {0, 0};
   int64_t rb[2];
   if (begin < end) {
-    page[0] = page_of(begin, 0);
-    page[1] = page_of(begin, 1);
+    pages_of(begin, page);
     rows_of(begin, page, rb);
-    next.load(a, rb, r, g);
+    keys.load(a, rb, r, g);
+    values.load(a, rb, r, g);
+    if (begin + kStride < end) pages_of(begin + kStride, ahead);
   }
-  for (int step = begin; step < end; step += kStride) {
-    const StepData<D, BITS> cur = next;
-    const bool bad0 = page[0] < 0 || page[0] >= a.pages, bad1 = page[1] < 0 || page[1] >= a.pages;
-    if (step + kStride < end) {
-      page[0] = page_of(step + kStride, 0);
-      page[1] = page_of(step + kStride, 1);
-      rows_of(step + kStride, page, rb);
-      next.load(a, rb, r, g);
-    }
-    const int tok0 = step * kStep;
-    const bool partly = bad0 || bad1 || tok0 + kStep > all_see;  // some row does not see some token
 
-    f4 sc[R][2];
+  // The queries in the codes' order, under a power of two of the row, go to LDS
+  // as operands, and what makes scores (over log 2) of the products to c.  Waves
+  // that share their rows share the work.
+  constexpr int kOwners = ROWS ? kAttnWaves : 1;
+  __shared__ u4 queries[kOwners][R][NK][HALVES][64];
+  auto& mine = queries[ROWS ? wave : 0];
+  float c[R];
 #pragma unroll
-    for (int t = 0; t < R; ++t) sc[t][0] = sc[t][1] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < R; ++t) {
+    const bool have = row0 + 16 * t + r < span.rows;
+    const int row = have ? row0 + 16 * t + r : 0;
+    const int64_t at = static_cast<int64_t>(span.first + query_of(row)) * a.ldq +
+                       static_cast<int64_t>(h * a.group + row - query_of(row) * a.group) * D + g * (D / 4);
+    using Q = std::conditional_t<PAIR, float, _Float16>;
+    Raw8<Q> x[NK];
+    float m = 0.f;
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
+      x[j].load(static_cast<const Q*>(a.q) + at + 8 * j);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const h8 k = key_operand<BITS>(cur.k[half], j);
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j].get(e)));
+    }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const int up = m > 0.f && m < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;  // the row's largest below 2^14
+    c[t] = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
 #pragma unroll
-        for (int t = 0; t < R; ++t)
+    for (int j = 0; j < NK; ++j) {
+      if (!ROWS && j % kAttnWaves != wave) continue;
+      Operand hi, lo;
 #pragma unroll
-          for (int p = HALVES - 1; p >= 0; --p)
-            sc[t][half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[t][j][p].h, sc[t][half], 0, 0, 0);
+      for (int e = 0; e < 8; e += 2) {
+        const float v0 = ldexpf(x[j].get(key_channel<BITS>(e)), up - key_factor<BITS>(e));
+        const float v1 = ldexpf(x[j].get(key_channel<BITS>(e + 1)), up - key_factor<BITS>(e + 1));
+        hi.p[e / 2] = h2{static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
+        lo.p[e / 2] = h2{static_cast<_Float16>(fmaf(static_cast<float>(hi.p[e / 2][0]), -1.f, v0)),
+                         static_cast<_Float16>(fmaf(static_cast<float>(hi.p[e / 2][1]), -1.f, v1))};
       }
+      mine[t][j][0][lane] = u4{hi.w[0], hi.w[1], hi.w[2], hi.w[3]};
+      if constexpr (PAIR) mine[t][j][1][lane] = u4{lo.w[0], lo.w[1], lo.w[2], lo.w[3]};
+    }
+  }
+  if constexpr (!ROWS) __syncthreads();
+  auto query_operand = [&](int t, int j, int p) { return __builtin_bit_cast(h8, mine[t][j][p][lane]); };
+  // The products start from what the codes' offset adds to them, taken off.
+  f4 start[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    f4 sum = {0.f, 0.f, 0.f, 0.f};
+    Operand offset;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) offset.w[p] = BITS == 8 || p % 2 ? 0x00800080u : 0x00080008u;
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+      for (int p = HALVES - 1; p >= 0; --p)
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset.h, query_operand(t, j, p), sum, 0, 0, 0);
+    start[t] = -sum;
+  }
+
+  f4 o[R][NV];
+  float ref[R], l[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    ref[t] = kUnset;
+    l[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) o[t][j] = f4{0.f, 0.f, 0.f, 0.f};
+  }
+  const Masks masks;
+
+  for (int step = begin; step < end; step += kStride) {
+    const int tok0 = step * kStep;
+    const bool bad0 = page[0] < 0 || page[0] >= a.pages, bad1 = page[1] < 0 || page[1] >= a.pages;
+    const bool partly = bad0 || bad1 || tok0 + kStep > all_see;  // some row does not see some token
+    const bool more = step + kStride < end;
+
+    asm volatile("" ::: "memory");  // the queries are read again, not kept in registers
+    f4 sc[R][2];
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      h8 k[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS>(keys.k[half], j, masks);
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int p = HALVES - 1; p >= 0; --p) {
+          const h8 q = query_operand(t, j, p);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            sc[t][half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                k[half], q, j == 0 && p == HALVES - 1 ? start[t] : sc[t][half], 0, 0, 0);
+        }
+    }
+    const f4 ks[2] = {keys.s[0], keys.s[1]};
+    // The next step's keys take the place of these while the rest is computed.
+    if (more) {
+      page[0] = ahead[0];
+      page[1] = ahead[1];
+      rows_of(step + kStride, page, rb);
+      keys.load(a, rb, r, g);
+      if (step + 2 * kStride < end) pages_of(step + 2 * kStride, ahead);
     }
 
     Operand w[R][2];  // hi, lo
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      float x[8], p[8], wt[8], sum, top;
-      uint32_t hidden = 0;
+      float x[8], kc[8], vs[8], wt[8], sum, top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = sc[t][i / 4][i % 4];
+        kc[i] = ks[i / 4][i % 4] * c[t];
+        vs[i] = values.s[i / 4][i % 4];
+      }
+      if (partly) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = tok0 + 16 * (i / 4) + 4 * g + i % 4;
+          if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) {  // whatever the scales there are
+            x[i] = -INFINITY;
+            kc[i] = 1.f;
+            vs[i] = 0.f;
+          }
+        }
+      }
       auto weigh = [&]() {
         sum = 0.f;
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(x[i] - ref[t]);
-          wt[i] = p[i] * cur.vs[i / 4][i % 4];
-        }
-        if (partly) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (hidden >> i & 1) p[i] = wt[i] = 0.f;  // whatever the scales there are
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum += p[i];
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[i], -ref[t]));
+          wt[i] = p * vs[i];
+          sum += p;
           top = fmaxf(top, wt[i]);
         }
       };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = sc[t][i / 4][i % 4] * (cur.ks[i / 4][i % 4] * c[t]);
-      if (partly) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = tok0 + 16 * (i / 4) + 4 * g + i % 4;
-          if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) {
-            x[i] = kNone;
-            hidden |= 1u << i;
-          }
-        }
-      }
       weigh();
       if (__any(top > 16384.f || sum > 1.15292150e18f)) {
-        float u = kNone;
+        float u = kUnset;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = x[i] + exponent(cur.vs[i / 4][i % 4]);
-          u = fmaxf(u, x[i] == kNone ? kNone : y);
-        }
+        for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[i], exponent(vs[i])));
         u = fmaxf(u, __shfl_xor(u, 16));
         u = fmaxf(u, __shfl_xor(u, 32));
         const float moved = fmaxf(ref[t], u - 8.f);
-        const float f = moved == kNone ? 1.f : __builtin_amdgcn_exp2f(ref[t] - moved);
+        const float f = __builtin_amdgcn_exp2f(ref[t] - moved);
         ref[t] = moved;
         l[t] *= f;
 #pragma unroll
@@ -414,8 +480,8 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const auto hi = __builtin_amdgcn_cvt_pkrtz(wt[2 * i], wt[2 * i + 1]);
-        const auto lo = __builtin_amdgcn_cvt_pkrtz(wt[2 * i] - static_cast<float>(hi[0]),
-                                                   wt[2 * i + 1] - static_cast<float>(hi[1]));
+        const auto lo = __builtin_amdgcn_cvt_pkrtz(fmaf(static_cast<float>(hi[0]), -1.f, wt[2 * i]),
+                                                   fmaf(static_cast<float>(hi[1]), -1.f, wt[2 * i + 1]));
         w[t][0].w[i] = __builtin_bit_cast(uint32_t, hi);
         w[t][1].w[i] = __builtin_bit_cast(uint32_t, lo);
       }
@@ -424,16 +490,16 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
 #pragma unroll
     for (int j = 0; j < NV / 4; ++j) {
       Operand v[4];
-      value_operands<D, BITS>(cur, j, v);
+      value_operands<D, BITS>(values, j, masks, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int p = 1; p >= 0; --p)
 #pragma unroll
-        for (int t = 0; t < R; ++t) {
-          f4& d = o[t][4 * j + e];
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][1].h, d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][0].h, d, 0, 0, 0);
-        }
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int t = 0; t < R; ++t)
+            o[t][4 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][p].h, o[t][4 * j + e], 0, 0, 0);
     }
+    if (more) values.load(a, rb, r, g);
   }
 
 #pragma unroll
@@ -457,16 +523,15 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      float top = kNone;
+      float top = kUnset;
 #pragma unroll
       for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, stat[k][t][r][0]);
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < kAttnWaves; ++k) {
-        const float f = stat[k][t][r][0] == kNone ? 0.f : __builtin_amdgcn_exp2f(stat[k][t][r][0] - top);
-        sum += f * stat[k][t][r][1];
+        sum += __builtin_amdgcn_exp2f(stat[k][t][r][0] - top) * stat[k][t][r][1];
       }
-      const float f = ref[t] == kNone ? 0.f : __builtin_amdgcn_exp2f(ref[t] - top);
+      const float f = __builtin_amdgcn_exp2f(ref[t] - top);
 #pragma unroll
       for (int j = 0; j < NV; ++j) o[t][j] *= f;
       ref[t] = top;
@@ -498,8 +563,8 @@ __global__ void __launch_bounds__(kAttnWaves * 64, 2)
   for (int t = 0; t < R; ++t) {
     const int row = row0 + 16 * t + r;
     if (row >= span.rows) continue;
-    const int64_t token = span.first + row / a.group;
-    const int head = h * a.group + row % a.group;
+    const int64_t token = span.first + query_of(row);
+    const int head = h * a.group + row - query_of(row) * a.group;
     if (whole) {
       const float f = l[t] == 0.f ? 0.f : 1.f / l[t];
       const int64_t at = token * a.ldo + static_cast<int64_t>(head) * D + g * (D / 4);
