@@ -244,7 +244,7 @@ __device__ __forceinline__ float exponent(float v) {
 }
 
 template <int D, int BITS, bool PAIR, int R, bool ROWS>
-__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * BITS > 512 ? 3 : 4)
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
     attention_kernel(AttentionArgs a, AttentionCut cut, int front, int slot0, int slots) {
   constexpr int NK = D / 32;   // instructions along a head's channels
   constexpr int NV = D / 16;   // channels of O a lane's row block holds
@@ -294,34 +294,36 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
   const int end = (part + 1) * share < wave_steps ? (part + 1) * share : wave_steps;
   constexpr int kStride = ROWS ? 1 : kAttnWaves;
 
-  // Cache rows of a step's halves, and whether their pages exist.
+  // Pages come 64 at a time, lane 2 i + half holding that of the half of the
+  // wave's step i (of 32): a step reads its two from the lanes, and no wait
+  // for the table stands between a step and its loads.  -1: no such page.
   const int tile_end = static_cast<int>(span.width << a.page_log2);
-  auto pages_of = [&](int step, int32_t* page) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      int tok = step * kStep + 16 * half;
-      tok = tok < tile_end ? tok : tile_end - 16;
-      page[half] = span.table[tok >> a.page_log2];
-    }
+  auto pages_from = [&](int step) -> int32_t {
+    int tok = (step + (lane >> 1) * kStride) * kStep + 16 * (lane & 1);
+    tok = tok < tile_end && tok >= 0 ? tok : tile_end - 16;
+    const int32_t p = span.table[tok >> a.page_log2];
+    return p >= 0 && p < a.pages ? p : -1;
   };
-  auto rows_of = [&](int step, const int32_t* page, int64_t* rb) {
+  int64_t rb[2];  // cache rows of a step's halves
+  auto rows_of = [&](int step, int32_t p0, int32_t p1) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int off = (step * kStep + 16 * half) & ((1 << a.page_log2) - 1);
-      const int32_t p = page[half] >= 0 && page[half] < a.pages ? page[half] : 0;
-      rb[half] = ((static_cast<int64_t>(p) * a.heads + h) << a.page_log2) + off;
+      const int32_t p = half ? p1 : p0;
+      rb[half] = ((static_cast<int64_t>(p < 0 ? 0 : p) * a.heads + h) << a.page_log2) + off;
     }
   };
   StepKeys<D, BITS> keys;
   StepValues<D, BITS> values;
-  int32_t page[2] = {0, 0}, ahead[2] = {0, 0};
-  int64_t rb[2];
+  int32_t pages = 0;
+  int32_t p0 = 0, p1 = 0;  // of the step whose keys are loaded
   if (begin < end) {
-    pages_of(begin, page);
-    rows_of(begin, page, rb);
+    pages = pages_from(begin);
+    p0 = __builtin_amdgcn_readlane(pages, 0);
+    p1 = __builtin_amdgcn_readlane(pages, 1);
+    rows_of(begin, p0, p1);
     keys.load(a, rb, r, g);
     values.load(a, rb, r, g);
-    if (begin + kStride < end) pages_of(begin + kStride, ahead);
   }
 
   // The queries in the codes' order, under a power of two of the row, go to LDS
@@ -395,11 +397,15 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
   }
   const Masks masks;
 
-  for (int step = begin; step < end; step += kStride) {
+  int turn = 0;  // steps into the 32 whose pages are at hand
+  // A step; all but the last bring the next one's keys in while the softmax and
+  // the second product run, and its values at the end.  (A condition around the
+  // loads would make every wait one for all of them.)
+  auto take = [&](int step, auto last_step) {
+    constexpr bool LAST = decltype(last_step)::value;
     const int tok0 = step * kStep;
-    const bool bad0 = page[0] < 0 || page[0] >= a.pages, bad1 = page[1] < 0 || page[1] >= a.pages;
+    const bool bad0 = p0 < 0, bad1 = p1 < 0;
     const bool partly = bad0 || bad1 || tok0 + kStep > all_see;  // some row does not see some token
-    const bool more = step + kStride < end;
 
     asm volatile("" ::: "memory");  // the queries are read again, not kept in registers
     f4 sc[R][2];
@@ -419,24 +425,29 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
                 k[half], q, j == 0 && p == HALVES - 1 ? start[t] : sc[t][half], 0, 0, 0);
         }
     }
-    const f4 ks[2] = {keys.s[0], keys.s[1]};
-    // The next step's keys take the place of these while the rest is computed.
-    if (more) {
-      page[0] = ahead[0];
-      page[1] = ahead[1];
-      rows_of(step + kStride, page, rb);
+    float kc[R][8];
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) kc[t][i] = keys.s[i / 4][i % 4] * c[t];
+    if constexpr (!LAST) {
+      if (++turn == 32) {
+        pages = pages_from(step + kStride);
+        turn = 0;
+      }
+      p0 = __builtin_amdgcn_readlane(pages, 2 * turn);
+      p1 = __builtin_amdgcn_readlane(pages, 2 * turn + 1);
+      rows_of(step + kStride, p0, p1);
       keys.load(a, rb, r, g);
-      if (step + 2 * kStride < end) pages_of(step + 2 * kStride, ahead);
     }
 
     Operand w[R][2];  // hi, lo
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      float x[8], kc[8], vs[8], wt[8], sum, top;
+      float x[8], vs[8], wt[8], sum, top;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = sc[t][i / 4][i % 4];
-        kc[i] = ks[i / 4][i % 4] * c[t];
         vs[i] = values.s[i / 4][i % 4];
       }
       if (partly) {
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
           const int tok = tok0 + 16 * (i / 4) + 4 * g + i % 4;
           if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) {  // whatever the scales there are
             x[i] = -INFINITY;
-            kc[i] = 1.f;
+            kc[t][i] = 1.f;
             vs[i] = 0.f;
           }
         }
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[i], -ref[t]));
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[t][i], -ref[t]));
           wt[i] = p * vs[i];
           sum += p;
           top = fmaxf(top, wt[i]);
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
       if (__any(top > 16384.f || sum > 1.15292150e18f)) {
         float u = kUnset;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[i], exponent(vs[i])));
+        for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[t][i], exponent(vs[i])));
         u = fmaxf(u, __shfl_xor(u, 16));
         u = fmaxf(u, __shfl_xor(u, 32));
         const float moved = fmaxf(ref[t], u - 8.f);
@@ -499,7 +510,12 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : D * B
           for (int t = 0; t < R; ++t)
             o[t][4 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][p].h, o[t][4 * j + e], 0, 0, 0);
     }
-    if (more) values.load(a, rb, r, g);
+    if constexpr (!LAST) values.load(a, rb, r, g);
+  };
+  if (begin < end) {
+    int step = begin;
+    for (; step + kStride < end; step += kStride) take(step, std::false_type{});
+    take(step, std::true_type{});
   }
 
 #pragma unroll
