@@ -1,88 +1,83 @@
 // attention.hip — how a call of the attention over the quantized cache is cut,
 // and the joining of its parts.
 //
-// A row's tokens (its sequence's own, and the prefix) are cut into parts where
-// there are few rows, each a workgroup's (attention_kernel.h).  A part leaves
-// (ref, l, O) with p = 2^(t - ref) summed to l and p v to O, in float32;
+// Where there are few rows, their tokens (a sequence's own, and the prefix) are
+// shared among workgroups (attention_kernel.h).  Each leaves (ref, l, O) with
+// p = 2^(t - ref) summed to l and p v to O, in float32;
 //   out = sum_i 2^(ref_i - M) O_i / sum_i 2^(ref_i - M) l_i,  M = max ref_i,
-// taken in the order of the parts.
+// taken in the order of the tokens, the prefix last.
 //
-// The lengths are on the device: the host cuts by the tables' capacity, and a
-// workgroup whose sequence is shorter than its part's share ends at once.
+// The lengths are on the device.  For few rows the workgroups add them up and
+// take equal runs; for many the host cuts by the tables' capacity, and a
+// workgroup whose sequence is shorter ends at once.
 #include "attention_kernel.h"
 
 namespace w4a4 {
 namespace {
 
-constexpr int kMaxParts = 256;       // of the own tokens, and of the prefix
 constexpr int64_t kGrid = 1 << 24;   // workgroups of 256 threads: below 2^32 threads
 
-AttentionCut cut_rows(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D) {
+AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D) {
   AttentionCut c{};
   c.rowsplit = rows > 32 || (D == 256 && rows > 16);
-  c.tiles = D < 256 && rows > (c.rowsplit ? 64 : 16) ? 2 : 1;
-  const int64_t group_rows = 16 * c.tiles * (c.rowsplit ? kAttnWaves : 1);
-  c.row_groups = (rows + group_rows - 1) / group_rows;
-  if (c.row_groups < 1) c.row_groups = 1;
-  const int64_t units = seqs > 0 ? seqs * heads * c.row_groups : 1;
-  c.least = c.rowsplit ? 256 : 128;
-  const int64_t most = (capacity + c.least - 1) / c.least;
-  int64_t parts = (4096 + units - 1) / units;
+  c.tiles = !c.rowsplit && rows > 16 ? 2 : 1;
+  if (seqs < 1) seqs = 1;
+  const int64_t resident = 256 * (D == 256 || c.tiles == 2 ? 2 : 3);  // workgroups that fit the chip
+  if (!c.rowsplit) {
+    c.piece_log2 = 8;
+    while ((seqs * capacity >> c.piece_log2) >= int64_t{1} << 30) ++c.piece_log2;
+    const int64_t pieces = seqs * (capacity > 0 ? ((capacity - 1) >> c.piece_log2) + 1 : 1);
+    int64_t groups = (resident + heads - 1) / heads;
+    c.one_piece = groups >= pieces;
+    groups = groups < pieces ? groups : pieces;
+    c.groups = Divisor(static_cast<uint32_t>(groups));
+    return c;
+  }
+  const int64_t groups = (rows + kGroupRows - 1) / kGroupRows;
+  c.groups = Divisor(static_cast<uint32_t>(groups));
+  const int64_t units = seqs * heads * groups;
+  c.piece_log2 = units < resident ? 8 : 10;
+  int64_t parts = units < resident ? (512 + units - 1) / units : 8;
+  const int64_t most = capacity >> c.piece_log2;
   parts = parts < most ? parts : most;
-  c.parts = static_cast<int>(parts < 1 ? 1 : parts < kMaxParts ? parts : kMaxParts);
+  c.parts = Divisor(static_cast<uint32_t>(parts < 1 ? 1 : parts));
   return c;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(AttentionArgs a, AttentionPlan plan) {
-  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  __shared__ float weight[2 * kMaxParts];
-  __shared__ float red[4];
-  __shared__ f4 lds[kGroups][kLanes];
-  const int head = blockIdx.x % a.q_heads;
-  const uint32_t at = blockIdx.x / a.q_heads;
-  const int s = at / static_cast<uint32_t>(a.max_q), i = at % static_cast<uint32_t>(a.max_q);
+// A row's partial results: of its own tokens and of the prefix.
+struct Parts {
+  int own, n, own_first, front_first;
+  int64_t token;
+  int query, head;
+};
+// False where the row has nothing to join: no such query, or stored at once.
+__device__ __forceinline__ bool parts_of_row(const AttentionArgs& a, const AttentionPlan& plan, const Partial& partial,
+                                             uint32_t id, Parts* p) {
+  const uint32_t at = id / static_cast<uint32_t>(a.q_heads);
+  p->head = id - at * a.q_heads;
+  const int s = at / static_cast<uint32_t>(a.max_q);
+  p->query = at - s * a.max_q;
   const Span span = own_span(a, s);
-  if (i >= span.n) return;
-  const int own = parts_of(span.length, plan.own.parts, plan.own.least);
-  if (own == 1 && !a.prefix_table) return;  // stored at once
-  const int front = a.prefix_table ? parts_of(front_span(a).length, plan.front.parts, plan.front.least) : 0;
-  const int n = own + front;
-  const int64_t row = static_cast<int64_t>(span.first + i) * a.q_heads + head;
-  const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
-  const float* stats = a.partial + plan.slots * rows * D;
-  auto slot = [&](int k) -> int64_t { return (k < own ? k : plan.own.parts + k - own) * rows + row; };
-
-  auto reduce = [&](float v, bool max) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = max ? fmaxf(v, __shfl_xor(v, o)) : v + __shfl_xor(v, o);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = max ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
-    __syncthreads();
-    return v;
-  };
-  float top = -INFINITY;
-  for (int k = threadIdx.x; k < n; k += 256) top = fmaxf(top, stats[2 * slot(k)]);
-  top = reduce(top, true);
-  float sum = 0.f;
-  for (int k = threadIdx.x; k < n; k += 256) {
-    const float f = __builtin_amdgcn_exp2f(stats[2 * slot(k)] - top);
-    weight[k] = f;
-    sum += f * stats[2 * slot(k) + 1];
+  if (p->query >= span.n) return false;
+  p->own_first = partial.slots(a, s)[0];
+  p->own = p->n = partial.slots(a, s)[1];
+  p->front_first = 0;
+  if (a.prefix_table) {
+    p->front_first = partial.slots(a, a.seqs)[0];
+    p->n += partial.slots(a, a.seqs)[1];
+  } else if (p->own == 1) {
+    return false;
   }
-  sum = reduce(sum, false);
-  const int c = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  f4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int k = grp; k < n; k += kGroups)
-    o += weight[k] * *reinterpret_cast<const f4*>(a.partial + slot(k) * D + 4 * c);
-  lds[grp][c] = o;
-  __syncthreads();
-  if (grp != 0) return;
-#pragma unroll
-  for (int k = 1; k < kGroups; ++k) o += lds[k][c];
-  o *= sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t to = (span.first + i) * a.ldo + static_cast<int64_t>(head) * D + 4 * c;
+  p->token = span.first + p->query;
+  return true;
+}
+__device__ __forceinline__ int64_t row_of(const AttentionArgs& a, const AttentionPlan& plan, const Partial& partial,
+                                          const Parts& p, int k) {
+  const bool front = k >= p.own;
+  return partial.row(a, plan, front, front ? p.front_first + k - p.own : p.own_first + k, p.token, p.query, p.head);
+}
+__device__ __forceinline__ void store_joined(const AttentionArgs& a, const Parts& p, int c, f4 o) {
+  const int64_t to = p.token * a.ldo + static_cast<int64_t>(p.head) * a.D + c;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (a.out_f16)
@@ -92,48 +87,163 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttentionArgs a, At
   }
 }
 
-void launch_part(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                 hipStream_t st) {
-  if (a.D == 64)
-    launch_attention_64(a, c, front, slot0, slots, pair, st);
-  else if (a.D == 128)
-    launch_attention_128(a, c, front, slot0, slots, pair, st);
+// Many rows: one to a wave, D / 4 lanes to a part, the parts of 64 at a time.
+template <int D>
+__global__ void __launch_bounds__(256) attention_join_rows_kernel(AttentionArgs a, AttentionPlan plan, uint32_t rows) {
+  constexpr int kLanes = D / 4, kGroups = 64 / kLanes;
+  const uint32_t id = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (id >= rows) return;
+  const Partial partial(a, plan);
+  Parts p;
+  if (!parts_of_row(a, plan, partial, id, &p)) return;
+  const int c = lane % kLanes, grp = lane / kLanes;
+  f4 o = {0.f, 0.f, 0.f, 0.f};
+  float top = kUnset, sum = 0.f;
+  for (int base = 0; base < p.n; base += 64) {
+    const int here = p.n - base < 64 ? p.n - base : 64;
+    float ref = kUnset, l = 0.f;
+    if (lane < here) {
+      const float* st = partial.stat(a, row_of(a, plan, partial, p, base + lane));
+      ref = st[0];
+      l = st[1];
+    }
+    float m = fmaxf(top, ref);
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor(m, w));
+    const float back = __builtin_amdgcn_exp2f(top - m);
+    top = m;
+    const float f = lane < here ? __builtin_amdgcn_exp2f(ref - m) : 0.f;
+    float add = f * l;
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) add += __shfl_xor(add, w);
+    sum = sum * back + add;
+    o *= back;
+#pragma unroll 4
+    for (int k = 0; k < here; k += kGroups) {
+      const int mine = k + grp < here ? k + grp : here - 1;
+      const f4 v = *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + mine)) + 4 * c);
+      o += (k + grp < here ? __shfl(f, mine) : 0.f) * v;
+    }
+  }
+#pragma unroll
+  for (int w = kLanes; w < 64; w <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], w);
+  }
+  o *= sum == 0.f ? 0.f : 1.f / sum;
+  if (grp == 0) store_joined(a, p, 4 * c, o);
+}
+
+// Few rows of many parts: 32 channels of a row to a workgroup, eight lanes to a
+// part, the parts of 256 at a time.
+template <int D>
+__global__ void __launch_bounds__(256) attention_join_parts_kernel(AttentionArgs a, AttentionPlan plan) {
+  __shared__ float weight[256];
+  __shared__ float red[8];
+  __shared__ f4 lds[4][8];
+  const uint32_t id = blockIdx.x / (D / 32);
+  const Partial partial(a, plan);
+  Parts p;
+  if (!parts_of_row(a, plan, partial, id, &p)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = static_cast<int>(blockIdx.x % (D / 32)) * 32 + 4 * (threadIdx.x & 7), grp = threadIdx.x >> 3;
+  f4 o = {0.f, 0.f, 0.f, 0.f};
+  float top = kUnset, sum = 0.f;
+  for (int base = 0; base < p.n; base += 256) {
+    const int here = p.n - base < 256 ? p.n - base : 256;
+    float ref = kUnset, l = 0.f;
+    if (static_cast<int>(threadIdx.x) < here) {
+      const float* st = partial.stat(a, row_of(a, plan, partial, p, base + threadIdx.x));
+      ref = st[0];
+      l = st[1];
+    }
+    float m = fmaxf(top, ref);
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor(m, w));
+    if (lane == 0) red[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float back = __builtin_amdgcn_exp2f(top - m);
+    top = m;
+    const float f = static_cast<int>(threadIdx.x) < here ? __builtin_amdgcn_exp2f(ref - m) : 0.f;
+    weight[threadIdx.x] = f;
+    float add = f * l;
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) add += __shfl_xor(add, w);
+    if (lane == 0) red[4 + wave] = add;
+    __syncthreads();
+    sum = sum * back + ((red[4] + red[5]) + (red[6] + red[7]));
+    o *= back;
+#pragma unroll 4
+    for (int k = grp; k < here; k += 32)
+      o += weight[k] * *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + k)) + c);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int w = 8; w < 64; w <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], w);
+  }
+  if (lane < 8) lds[wave][lane] = o;
+  __syncthreads();
+  if (threadIdx.x >= 8) return;
+  o = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+  o *= sum == 0.f ? 0.f : 1.f / sum;
+  store_joined(a, p, c, o);
+}
+
+template <int D>
+void launch_join(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t st) {
+  const uint32_t rows = static_cast<uint32_t>(a.seqs) * a.max_q * a.q_heads;  // below 2^24
+  if (rows < 512 && (plan.own.rowsplit ? plan.own_slots : plan.own.groups.d) + plan.front_slots > 8)
+    hipLaunchKernelGGL((attention_join_parts_kernel<D>), dim3(rows * (D / 32)), dim3(256), 0, st, a, plan);
   else
-    launch_attention_256(a, c, front, slot0, slots, pair, st);
+    hipLaunchKernelGGL((attention_join_rows_kernel<D>), dim3((rows + 3) / 4), dim3(256), 0, st, a, plan, rows);
 }
 
 }  // namespace
 
 bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
-  plan->own = cut_rows(static_cast<int64_t>(a.max_q) * a.group, a.seqs, a.heads, a.width << a.page_log2, a.D);
-  plan->front = AttentionCut{};
-  plan->slots = plan->own.parts > 1 ? plan->own.parts : 0;
+  const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.group.d, front_rows = static_cast<int64_t>(a.tokens) * a.group.d;
+  *plan = AttentionPlan{};
+  AttentionCut& own = plan->own;
+  AttentionCut& front = plan->front;
+  own = cut_tokens(own_rows, a.seqs, a.heads, a.width << a.page_log2, a.D);
+  const int64_t cap = a.width << a.page_log2;
+  const bool split = own.rowsplit ? own.parts.d > 1 : cap > int64_t{1} << own.piece_log2;
+  plan->join = split || a.prefix_width > 0;
+  // Few rows: run w of sequence s is slot w + s.
+  if (plan->join) plan->own_slots = own.rowsplit ? own.parts.d : static_cast<int64_t>(own.groups.d) + a.seqs;
   if (a.prefix_width > 0) {
-    plan->front = cut_rows(static_cast<int64_t>(a.tokens) * a.group, 1, a.heads, a.prefix_width << a.page_log2, a.D);
-    plan->slots = plan->own.parts + plan->front.parts;
+    front = cut_tokens(front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D);
+    plan->front_slots = front.rowsplit ? front.parts.d : front.groups.d;
   }
-  return static_cast<int64_t>(a.seqs) * a.heads * plan->own.row_groups * plan->own.parts < kGrid &&
-         a.heads * plan->front.row_groups * plan->front.parts < kGrid &&
+  return cut_blocks(a, own, a.seqs) + (a.prefix_width > 0 ? cut_blocks(a, front, 1) : 0) < kGrid &&
          static_cast<int64_t>(a.seqs) * a.max_q * a.q_heads < kGrid;
 }
 
 size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& plan) {
-  return static_cast<size_t>(plan.slots) * static_cast<size_t>(a.tokens) * static_cast<size_t>(a.q_heads) *
-         static_cast<size_t>(a.D + 2) * 4;
+  if (!plan.join) return 0;
+  const size_t rows = static_cast<size_t>(plan.own_slots * (plan.own.rowsplit ? a.tokens : a.max_q) +
+                                          plan.front_slots * a.tokens) * static_cast<size_t>(a.q_heads);
+  return rows * static_cast<size_t>(a.D + 2) * 4 + (static_cast<size_t>(a.seqs) + 1) * 8;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, bool q_f16, hipStream_t st) {
-  const int slots = static_cast<int>(plan.slots);
-  if (a.prefix_table) launch_part(a, plan.front, 1, plan.own.parts, slots, !q_f16, st);
-  launch_part(a, plan.own, 0, 0, slots, !q_f16, st);
-  if (slots > 0) {
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.seqs) * a.max_q * a.q_heads)), block(256);
+  if (a.D == 64)
+    launch_attention_64(a, plan, !q_f16, st);
+  else if (a.D == 128)
+    launch_attention_128(a, plan, !q_f16, st);
+  else
+    launch_attention_256(a, plan, !q_f16, st);
+  if (plan.join) {
     if (a.D == 64)
-      hipLaunchKernelGGL((attention_join_kernel<64>), grid, block, 0, st, a, plan);
+      launch_join<64>(a, plan, st);
     else if (a.D == 128)
-      hipLaunchKernelGGL((attention_join_kernel<128>), grid, block, 0, st, a, plan);
+      launch_join<128>(a, plan, st);
     else
-      hipLaunchKernelGGL((attention_join_kernel<256>), grid, block, 0, st, a, plan);
+      launch_join<256>(a, plan, st);
   }
   return hipGetLastError();
 }

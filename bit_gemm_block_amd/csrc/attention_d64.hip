@@ -4,9 +4,8 @@
 
 namespace w4a4 {
 
-void launch_attention_64(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                         hipStream_t st) {
-  launch_head_dim<64>(a, c, front, slot0, slots, pair, st);
+void launch_attention_64(const AttentionArgs& a, const AttentionPlan& plan, bool pair, hipStream_t st) {
+  launch_head_dim<64>(a, plan, pair, st);
 }
 
 }  // namespace w4a4

@@ -37,16 +37,14 @@ constexpr int kAttnWaves = 4;   // of a workgroup
 
 __host__ __device__ inline int64_t least64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// Parts in use of a range of L tokens.
-__host__ __device__ inline int parts_of(int64_t L, int parts, int least) {
-  const uint32_t p = (static_cast<uint32_t>(L) + least - 1) / static_cast<uint32_t>(least);  // L below 2^30 + 1
-  return static_cast<int>(p < 1 ? 1 : p < static_cast<uint32_t>(parts) ? p : parts);
+// Pieces of a range of L tokens (at most 2^30), one at least.
+__host__ __device__ inline int pieces_of(int64_t L, const AttentionCut& c) {
+  const uint32_t p = (static_cast<uint32_t>(L) + (1u << c.piece_log2) - 1) >> c.piece_log2;
+  return static_cast<int>(p < 1 ? 1 : p);
 }
 
 // What a sequence (own tokens) or the prefix is to its queries.
 struct Span {
-  const int32_t* table;
-  int64_t width;
   int64_t length;  // tokens
   int first, n;    // rows of q: the first, how many
   int rows;        // (query, head of the group) pairs that are computed
@@ -59,8 +57,6 @@ __device__ __forceinline__ int64_t clamp_length(int32_t v, int64_t cap) {
 
 __device__ __forceinline__ Span own_span(const AttentionArgs& a, int s) {
   Span p;
-  p.table = a.tables + s * a.width;
-  p.width = a.width;
   p.length = clamp_length(a.lengths[s], a.width << a.page_log2);
   int q0 = s, q1 = s + 1;
   if (a.q_start) {
@@ -71,14 +67,12 @@ __device__ __forceinline__ Span own_span(const AttentionArgs& a, int s) {
   }
   p.first = q0;
   p.n = q1 - q0;
-  p.rows = (p.n < a.max_q ? p.n : a.max_q) * a.group;
+  p.rows = (p.n < a.max_q ? p.n : a.max_q) * static_cast<int>(a.group.d);
   return p;
 }
 
 __device__ __forceinline__ Span front_span(const AttentionArgs& a) {
   Span p;
-  p.table = a.prefix_table;
-  p.width = a.prefix_width;
   p.length = clamp_length(a.prefix_length[0], a.prefix_width << a.page_log2);
   int q1 = a.seqs;
   if (a.q_start) {
@@ -87,7 +81,7 @@ __device__ __forceinline__ Span front_span(const AttentionArgs& a) {
   }
   p.first = 0;
   p.n = q1;
-  p.rows = q1 * a.group;
+  p.rows = q1 * static_cast<int>(a.group.d);
   return p;
 }
 
@@ -113,66 +107,62 @@ struct Masks {
   }
 };
 
-// The codes and scales of a step's keys or values, tokens 4 g + i of both halves
-// for the scales and the values, token r for the keys.
+// A step's codes as a lane holds them: of the keys, its share of token r of both
+// halves; of the values, its channels of tokens 4 g + i of both.
 template <int D, int BITS>
-struct StepKeys {
-  static constexpr int RB = D * BITS / 8;  // bytes of a row
-  static constexpr int KW = RB / 16;       // words of its token's row a lane holds
-  uint32_t k[2][KW];
-  f4 s[2];
-  __device__ __forceinline__ void load(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g) {
+struct Row {
+  static constexpr int kBytes = D * BITS / 8;
+  static constexpr int kKeyWords = kBytes / 16;                        // of each half
+  static constexpr int kValueWords = kBytes >= 64 ? kBytes / 64 : 1;   // of each token
+  static constexpr int kWords = 8 * kValueWords;                       // of either, at most
+};
+template <int WORDS>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* d) {
+  if constexpr (WORDS == 1) {
+    d[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (WORDS == 2) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    d[0] = w.x;
+    d[1] = w.y;
+  } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* p = a.k + rb[h] * RB + (r * RB + g * (RB / 4));
-      if constexpr (KW == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        k[h][0] = w.x;
-        k[h][1] = w.y;
-      } else {
+    for (int i = 0; i < WORDS; i += 4) {
+      const u4 w = *reinterpret_cast<const u4*>(p + 4 * i);
 #pragma unroll
-        for (int i = 0; i < KW; i += 4) {
-          const u4 w = *reinterpret_cast<const u4*>(p + 4 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) k[h][i + e] = w[e];
-        }
-      }
-      s[h] = *reinterpret_cast<const f4*>(a.ks + rb[h] + 4 * g);
+      for (int e = 0; e < 4; ++e) d[i + e] = w[e];
     }
   }
-};
-
+}
+// rb: the cache rows of the halves' first tokens.
 template <int D, int BITS>
-struct StepValues {
-  static constexpr int RB = D * BITS / 8;
-  static constexpr int VW = RB >= 64 ? RB / 64 : 1;  // words of each of its tokens a lane holds
-  uint32_t v[8][VW];
-  f4 s[2];
-  __device__ __forceinline__ void load(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g) {
+__device__ __forceinline__ void load_keys(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* k) {
+  using X = Row<D, BITS>;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] = *reinterpret_cast<const f4*>(a.vs + rb[h] + 4 * g);
+  for (int h = 0; h < 2; ++h)
+    load_words<X::kKeyWords>(a.k + rb[h] * X::kBytes + (r * X::kBytes + g * (X::kBytes / 4)), k + h * X::kKeyWords);
+}
+template <int D, int BITS>
+__device__ __forceinline__ void load_values(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* v) {
+  using X = Row<D, BITS>;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = a.v + rb[h] * RB + (g * (4 * RB) + r * (RB / 16)) + i * RB;
-        uint32_t* d = v[4 * h + i];
-        if constexpr (RB == 32) {
-          d[0] = *reinterpret_cast<const uint16_t*>(p);
-        } else if constexpr (VW == 1) {
-          d[0] = *reinterpret_cast<const uint32_t*>(p);
-        } else if constexpr (VW == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(p);
-          d[0] = w.x;
-          d[1] = w.y;
-        } else {
-          const u4 w = *reinterpret_cast<const u4*>(p);
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* first = a.v + rb[h] * X::kBytes;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = w[e];
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = first + (g * (4 * X::kBytes) + r * (X::kBytes / 16)) + i * X::kBytes;
+      if constexpr (X::kBytes == 32)
+        v[4 * h + i] = *reinterpret_cast<const uint16_t*>(p);
+      else
+        load_words<X::kValueWords>(p, v + (4 * h + i) * X::kValueWords);
     }
   }
-};
+}
+// The scales of tokens 4 g + i of both halves.
+__device__ __forceinline__ void load_scales(const float* s, const int64_t* rb, uint32_t g, f4* d) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    d[h] = *reinterpret_cast<const f4*>(s + rb[h] + 4 * g);
+}
 
 // K's codes 8 j to 8 j + 7 of a lane, unsigned, as fp16 subnormal numbers u 2^-24
 // (the bits of a small whole number are that times 2^-24): in the order
@@ -211,12 +201,14 @@ __device__ constexpr int key_factor(int e) {
 // of the lane's own.  (An offset of the values cannot wait like the keys': it
 // would be 8 times the sum of the weights, which the result is a small part of.)
 template <int D, int BITS>
-__device__ __forceinline__ void value_operands(const StepValues<D, BITS>& s, int q, const Masks& m, Operand* o) {
+__device__ __forceinline__ void value_operands(const uint32_t* v, int q, const Masks& m, Operand* o) {
+  constexpr int VW = Row<D, BITS>::kValueWords;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
+    const int word = BITS == 4 ? q / 2 : q;
+    uint32_t w0 = v[2 * p * VW + word], w1 = v[(2 * p + 1) * VW + word];
     if constexpr (BITS == 4) {
-      const uint32_t t =
-          __builtin_amdgcn_perm(s.v[2 * p + 1][q / 2], s.v[2 * p][q / 2], q % 2 ? 0x07060302u : 0x05040100u);
+      const uint32_t t = __builtin_amdgcn_perm(w1, w0, q % 2 ? 0x07060302u : 0x05040100u);
       const uint32_t u = t >> 8;
       o[0].w[p] = (t & m.even) ^ m.value_even;
       o[1].w[p] = (t & m.odd) ^ m.value_odd;
@@ -228,7 +220,8 @@ __device__ __forceinline__ void value_operands(const StepValues<D, BITS>& s, int
       o[2].p[p] -= off;
       o[3].p[p] = __builtin_elementwise_fma(o[3].p[p], sixteenth, off16);
     } else {
-      const uint32_t w0 = s.v[2 * p][q] ^ 0x80808080u, w1 = s.v[2 * p + 1][q] ^ 0x80808080u;
+      w0 ^= 0x80808080u;
+      w1 ^= 0x80808080u;
       o[0].p[p] = two_bytes<0x0c040c00>(w1, w0);
       o[1].p[p] = two_bytes<0x0c050c01>(w1, w0);
       o[2].p[p] = two_bytes<0x0c060c02>(w1, w0);
@@ -237,164 +230,356 @@ __device__ __forceinline__ void value_operands(const StepValues<D, BITS>& s, int
   }
 }
 
+// Two values as fp16, to nearest, and what that leaves of them.
+__device__ __forceinline__ h2 two_halves(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f2{a, b}), h2);
+}
+__device__ __forceinline__ h2 remainders(h2 hi, float a, float b) {
+  return two_halves(fmaf(static_cast<float>(hi[0]), -1.f, a), fmaf(static_cast<float>(hi[1]), -1.f, b));
+}
+
 // log2 of a scale, down to the integer, between 2^-60 and 2^127.
 __device__ __forceinline__ float exponent(float v) {
   const int e = __builtin_amdgcn_frexp_expf(v);
   return v > 8.6736174e-19f ? static_cast<float>(e) : -60.f;
 }
 
-template <int D, int BITS, bool PAIR, int R, bool ROWS>
-__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
-    attention_kernel(AttentionArgs a, AttentionCut cut, int front, int slot0, int slots) {
+constexpr float kUnset = -1e30f;  // reference of a row that has seen nothing
+
+// What a row of lane (r, g) has gathered: lanes of one r share ref, and hold
+// their own tokens' part of l and their channels of O.
+template <int NV>
+struct RowState {
+  f4 o[NV];
+  float ref, l;
+  __device__ __forceinline__ void clear() {
+    ref = kUnset;
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) o[j] = f4{0.f, 0.f, 0.f, 0.f};
+  }
+};
+
+// The weights of a step from its products sc, the keys' scales times the row's
+// factor, kc, and the values' scales: hi and lo.  With `partly` positions from limit on, and those of absent pages, are not seen.
+template <int NV>
+__device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const f4* vs_, bool partly, int limit,
+                                           int tok, bool bad0, bool bad1, RowState<NV>& s, Operand* w) {
+  float x[8], kc[8], vs[8], wt[8], sum, top;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = sc[i / 4][i % 4];
+    kc[i] = kc_[i];
+    vs[i] = vs_[i / 4][i % 4];
+  }
+  if (partly) {
+    asm volatile("");  // a branch, not forty selects in every step
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (tok + 16 * (i / 4) + i % 4 >= limit || (i < 4 ? bad0 : bad1)) {  // whatever the scales there are
+        x[i] = -INFINITY;
+        kc[i] = 1.f;
+        vs[i] = 0.f;
+      }
+    }
+  }
+  auto weigh = [&]() {
+    sum = 0.f;
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[i], -s.ref));
+      wt[i] = p * vs[i];
+      sum += p;
+      top = fmaxf(top, wt[i]);
+    }
+  };
+  weigh();
+  if (__any(top > 16384.f || sum > 1.15292150e18f)) {
+    float u = kUnset;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[i], exponent(vs[i])));
+    u = fmaxf(u, __shfl_xor(u, 16));
+    u = fmaxf(u, __shfl_xor(u, 32));
+    const float moved = fmaxf(s.ref, u - 8.f);
+    const float f = __builtin_amdgcn_exp2f(s.ref - moved);
+    s.ref = moved;
+    s.l *= f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) s.o[j] *= f;
+    weigh();
+  }
+  s.l += sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[0].p[i] = two_halves(wt[2 * i], wt[2 * i + 1]);
+    w[1].p[i] = remainders(w[0].p[i], wt[2 * i], wt[2 * i + 1]);
+  }
+}
+
+struct Sight {
+  int length, n;
+  bool all;
+  __device__ __forceinline__ Sight(const AttentionArgs& a, const Span& span, int front)
+      : length(static_cast<int>(span.length)), n(span.n), all(front || !a.causal) {}
+  // Positions below this are what a query sees.
+  __device__ __forceinline__ int limit(int query) const {
+    const int l = length - n + query + 1;
+    return all ? length : l < 0 ? 0 : l;
+  }
+};
+
+// The pages of up to 32 steps, lane 2 i + half holding that of step first + i
+// stride: no wait for the table stands between a step and its loads.  -1: no
+// such page.
+struct Pages {
+  const int32_t* table;
+  int end;  // tokens that it has pages for
+  __device__ __forceinline__ Pages(const AttentionArgs& a, int s, int front)
+      : table(front ? a.prefix_table : a.tables + s * a.width),
+        end(static_cast<int>((front ? a.prefix_width : a.width) << a.page_log2)) {}
+  __device__ __forceinline__ int32_t raw(const AttentionArgs& a, int first, int stride, int lane) const {
+    int tok = (first + (lane >> 1) * stride) * kStep + 16 * (lane & 1);
+    tok = tok < end && tok >= 0 ? tok : end - 16;
+    return end > 0 ? table[tok >> a.page_log2] : -1;
+  }
+  static __device__ __forceinline__ int32_t checked(const AttentionArgs& a, int32_t p) {
+    return p >= 0 && p < a.pages ? p : -1;
+  }
+};
+// The cache rows of the halves of a step in pages p0 and p1.
+__device__ __forceinline__ void rows_of(const AttentionArgs& a, int h, int step, int32_t p0, int32_t p1, int64_t* rb) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int off = (step * kStep + 16 * half) & ((1 << a.page_log2) - 1);
+    const int32_t p = half ? p1 : p0;
+    rb[half] = ((static_cast<int64_t>(p < 0 ? 0 : p) * a.heads + h) << a.page_log2) + off;
+  }
+}
+
+// A lane's channels [g D / 4, +D / 4) of a row of queries.
+template <int D, typename Q>
+__device__ __forceinline__ void load_query(const AttentionArgs& a, const Span& span, int h, int row, int g,
+                                           Raw8<Q>* x) {
+  row = row < span.rows ? row : 0;
+  const int query = a.group.quotient(row);
+  const int64_t at = static_cast<int64_t>(span.first + query) * a.ldq +
+                     static_cast<int64_t>(h * a.group.d + row - query * a.group.d) * D + g * (D / 4);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) x[j].load(static_cast<const Q*>(a.q) + at + 8 * j);
+}
+// The power of two that brings the row's largest below 2^14.
+template <int D, typename Q>
+__device__ __forceinline__ int query_shift(const Raw8<Q>* x) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j].get(e)));
+  m = fmaxf(m, __shfl_xor(m, 16));
+  m = fmaxf(m, __shfl_xor(m, 32));
+  return m > 0.f && m < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;
+}
+// Eight channels as operands in the codes' order.
+template <int BITS, typename Q>
+__device__ __forceinline__ void query_operands(const Raw8<Q>& x, int up, Operand* hi, Operand* lo) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float v0 = ldexpf(x.get(key_channel<BITS>(e)), up - key_factor<BITS>(e));
+    const float v1 = ldexpf(x.get(key_channel<BITS>(e + 1)), up - key_factor<BITS>(e + 1));
+    hi->p[e / 2] = two_halves(v0, v1);
+    lo->p[e / 2] = remainders(hi->p[e / 2], v0, v1);
+  }
+}
+// The codes' offset as an operand: a product with it is what it adds.
+template <int BITS>
+__device__ __forceinline__ h8 offset_operand() {
+  Operand o;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) o.w[p] = BITS == 8 || p % 2 ? 0x00800080u : 0x00080008u;
+  return o.h;
+}
+
+// Partial results: rows of D float32 (O), of the own tokens' slots and then of the
+// prefix's, after them (ref, l) of each, after these, per sequence and for the
+// prefix, its first slot and their number.
+struct Partial {
+  int64_t own_rows, rows;
+  __device__ __forceinline__ Partial(const AttentionArgs& a, const AttentionPlan& p)
+      : own_rows(p.own_slots * (p.own.rowsplit ? a.tokens : a.max_q) * a.q_heads),
+        rows(own_rows + p.front_slots * a.tokens * a.q_heads) {}
+  // The row of a slot: own tokens of few rows are kept by their place in the
+  // sequence, others by their token.
+  __device__ __forceinline__ int64_t row(const AttentionArgs& a, const AttentionPlan& p, bool front, int64_t slot,
+                                         int64_t token, int query, int head) const {
+    const bool by_place = !front && !p.own.rowsplit;
+    return (front ? own_rows : 0) + ((slot * (by_place ? a.max_q : a.tokens) + (by_place ? query : token)) * a.q_heads + head);
+  }
+  __device__ __forceinline__ float* o(const AttentionArgs& a, int64_t row) const { return a.partial + row * a.D; }
+  __device__ __forceinline__ float* stat(const AttentionArgs& a, int64_t row) const {
+    return a.partial + rows * a.D + row * 2;
+  }
+  __device__ __forceinline__ int32_t* slots(const AttentionArgs& a, int s) const {
+    return reinterpret_cast<int32_t*>(a.partial + rows * (a.D + 2)) + 2 * s;
+  }
+};
+
+// Few rows: the waves of a workgroup share its 16 R rows and take every fourth
+// step each.
+template <int D, bool PAIR, int R>
+struct TokensLds {
+  typedef u4 Queries[R][D / 32][PAIR ? 2 : 1][64];
+  // Where two workgroups would not fit a compute unit's 160 KB, the queries lie
+  // where the waves' shares come to lie.
+  static constexpr bool kShare = R * D == 256 && PAIR;
+  f4 o[kAttnWaves][R * (D / 16)][64];
+  float stat[kAttnWaves][R][16][2];
+  u4 apart[kShare ? 1 : sizeof(Queries) / 16];
+  __device__ __forceinline__ Queries& queries() {
+    return *reinterpret_cast<Queries*>(kShare ? static_cast<void*>(o) : static_cast<void*>(apart));
+  }
+};
+// Inclusive sums along the lanes.
+__device__ __forceinline__ int sum_to_lane(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row 0 to 1, 2 to 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2, 3
+  return v;
+}
+
+// A workgroup's run of pieces, and the sequence in which it begins.
+struct Run {
+  int first, end;   // pieces of all sequences
+  int s, start;     // the sequence, and its first piece
+  int each;         // pieces to a workgroup
+  __device__ __forceinline__ Run(const AttentionArgs& a, const AttentionCut& cut, int front, int w, int lane) {
+    const int seqs = front ? 1 : a.seqs;
+    const int64_t cap = (front ? a.prefix_width : a.width) << a.page_log2;
+    const int32_t* lengths = front ? a.prefix_length : a.lengths;
+    auto pieces = [&](int i) { return i < seqs ? pieces_of(clamp_length(lengths[i], cap), cut) : 0; };
+    const int mine = pieces(lane);
+    int all = mine;
+    for (int i = 64 + lane; i < seqs; i += 64) all += pieces(i);
+    all = __builtin_amdgcn_readlane(sum_to_lane(all), 63);
+    each = cut.groups.quotient(all + cut.groups.d - 1);
+    first = w * each;
+    end = first + each < all ? first + each : all;
+    s = start = 0;
+    for (int base = 0; base < seqs && first < end; base += 64) {
+      const int n = base == 0 ? mine : pieces(base + lane);
+      const int to = start + sum_to_lane(n);
+      const uint64_t here = __ballot(to > first);
+      if (here) {
+        const int i = __builtin_ctzll(here);
+        s = base + i;
+        start = __builtin_amdgcn_readlane(to - n, i);
+        break;
+      }
+      start = __builtin_amdgcn_readlane(to, 63);
+    }
+  }
+};
+
+// A section of a run: pieces [from, to) of sequence s.  whole: 1 if these are all
+// and there is no prefix, -1 if that is still to be found out.
+template <int D, int BITS, bool PAIR, int R>
+__device__ __forceinline__ void tokens_section(const AttentionArgs& a, const AttentionPlan& plan, int front, int h,
+                                               int s, int from, int to, int whole, int slot,
+                                               TokensLds<D, PAIR, R>& lds) {
   constexpr int NK = D / 32;   // instructions along a head's channels
   constexpr int NV = D / 16;   // channels of O a lane's row block holds
   constexpr int HALVES = PAIR ? 2 : 1;
-  constexpr float kUnset = -1e30f;  // of a row that has seen nothing
+  const AttentionCut& cut = front ? plan.front : plan.own;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  uint32_t id = blockIdx.x;
-  const int h = id % a.heads;
-  id /= a.heads;
-  const int part = id % cut.parts;
-  id /= cut.parts;
-  const int rg = static_cast<int>(cut.row_groups) - 1 - static_cast<int>(id % static_cast<uint32_t>(cut.row_groups));
-  const int s = static_cast<int>(id / static_cast<uint32_t>(cut.row_groups));
-
+  const int begin = (from << (cut.piece_log2 - 5)) + wave;
+  // Pages and queries are on their way together.
+  const Pages table(a, s, front);
+  int32_t pages = table.raw(a, begin, kAttnWaves, lane);
   const Span span = front ? front_span(a) : own_span(a, s);
-  constexpr int kRows = 16 * R;
-  const int group_rows = ROWS ? kRows * kAttnWaves : kRows;
-  if (static_cast<int64_t>(rg) * group_rows >= span.rows) return;
-  const int eff = parts_of(span.length, cut.parts, cut.least);
-  if (part >= eff) return;
-  const int row0 = rg * group_rows + (ROWS ? wave * kRows : 0);
+  constexpr int row0 = 0;
+  if (span.rows <= 0) return;
+  using Q = std::conditional_t<PAIR, float, _Float16>;
+  Raw8<Q> x[R][NK];
+#pragma unroll
+  for (int t = 0; t < R; ++t) load_query<D>(a, span, h, row0 + 16 * t + r, g, x[t]);
 
-  // What the queries see: positions below the limit.
-  const int length = static_cast<int>(span.length);
-  auto limit_of = [&](int query) -> int {
-    if (front || !a.causal) return length;
-    const int l = length - span.n + query + 1;
-    return l < 0 ? 0 : l;
-  };
-  auto query_of = [&](int row) { return static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.group)); };
+  if (whole < 0) {
+    const int n = pieces_of(span.length, cut);
+    if (from >= n) return;
+    whole = n == 1 && !front && !a.prefix_table;
+    if (plan.join && from == 0 && h == 0 && threadIdx.x == 0) {
+      int32_t* m = Partial(a, plan).slots(a, front ? a.seqs : 0);
+      m[0] = 0;
+      m[1] = n;
+    }
+  }
+  const Sight sight(a, span, front);
+  const int all_see = 16 * R <= span.rows ? sight.limit(0) : 0;  // what every row sees
+  const int steps = (sight.limit(a.group.quotient(span.rows - 1)) + kStep - 1) / kStep;
+  const int stop = to << (cut.piece_log2 - 5);
+  const int end = stop < steps ? stop : steps;
   int limit[R];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int row = row0 + 16 * t + r;
-    limit[t] = row < span.rows ? limit_of(query_of(row)) : 0;
+    limit[t] = row < span.rows ? sight.limit(a.group.quotient(row)) : 0;
   }
-  const int last = (row0 + kRows < span.rows ? row0 + kRows : span.rows) - 1;  // of this wave
-  const int group_last = static_cast<int>(least64(static_cast<int64_t>(rg + 1) * group_rows, span.rows)) - 1;
-  const int wave_end = last >= row0 ? limit_of(last / a.group) : 0;
-  const int all_see = row0 + kRows <= span.rows ? limit_of(row0 / a.group) : 0;  // positions every row sees
-  const int share = static_cast<int>((static_cast<uint32_t>(limit_of(group_last / a.group) + kStep - 1) / kStep + eff - 1) /
-                                     static_cast<uint32_t>(eff));  // steps to a part
-  const int wave_steps = (wave_end + kStep - 1) / kStep;
-  const int begin = part * share + (ROWS ? 0 : wave);
-  const int end = (part + 1) * share < wave_steps ? (part + 1) * share : wave_steps;
-  constexpr int kStride = ROWS ? 1 : kAttnWaves;
 
-  // Pages come 64 at a time, lane 2 i + half holding that of the half of the
-  // wave's step i (of 32): a step reads its two from the lanes, and no wait
-  // for the table stands between a step and its loads.  -1: no such page.
-  const int tile_end = static_cast<int>(span.width << a.page_log2);
-  auto pages_from = [&](int step) -> int32_t {
-    int tok = (step + (lane >> 1) * kStride) * kStep + 16 * (lane & 1);
-    tok = tok < tile_end && tok >= 0 ? tok : tile_end - 16;
-    const int32_t p = span.table[tok >> a.page_log2];
-    return p >= 0 && p < a.pages ? p : -1;
-  };
-  int64_t rb[2];  // cache rows of a step's halves
-  auto rows_of = [&](int step, int32_t p0, int32_t p1) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int off = (step * kStep + 16 * half) & ((1 << a.page_log2) - 1);
-      const int32_t p = half ? p1 : p0;
-      rb[half] = ((static_cast<int64_t>(p < 0 ? 0 : p) * a.heads + h) << a.page_log2) + off;
-    }
-  };
-  StepKeys<D, BITS> keys;
-  StepValues<D, BITS> values;
-  int32_t pages = 0;
+  constexpr int KW = Row<D, BITS>::kKeyWords;
+  uint32_t keys[2 * KW], values[Row<D, BITS>::kWords];
+  f4 ks[2], vs[2];
+  int64_t rb[2];
   int32_t p0 = 0, p1 = 0;  // of the step whose keys are loaded
+  pages = Pages::checked(a, pages);
   if (begin < end) {
-    pages = pages_from(begin);
     p0 = __builtin_amdgcn_readlane(pages, 0);
     p1 = __builtin_amdgcn_readlane(pages, 1);
-    rows_of(begin, p0, p1);
-    keys.load(a, rb, r, g);
-    values.load(a, rb, r, g);
+    rows_of(a, h, begin, p0, p1, rb);
+    load_keys<D, BITS>(a, rb, r, g, keys);
+    load_scales(a.ks, rb, g, ks);
+    load_values<D, BITS>(a, rb, r, g, values);
+    load_scales(a.vs, rb, g, vs);
   }
 
-  // The queries in the codes' order, under a power of two of the row, go to LDS
-  // as operands, and what makes scores (over log 2) of the products to c.  Waves
-  // that share their rows share the work.
-  constexpr int kOwners = ROWS ? kAttnWaves : 1;
-  __shared__ u4 queries[kOwners][R][NK][HALVES][64];
-  auto& mine = queries[ROWS ? wave : 0];
+  // The queries go to LDS as operands, a wave's share of the channels each; c
+  // makes scores (over log 2) of the products.
   float c[R];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    const bool have = row0 + 16 * t + r < span.rows;
-    const int row = have ? row0 + 16 * t + r : 0;
-    const int64_t at = static_cast<int64_t>(span.first + query_of(row)) * a.ldq +
-                       static_cast<int64_t>(h * a.group + row - query_of(row) * a.group) * D + g * (D / 4);
-    using Q = std::conditional_t<PAIR, float, _Float16>;
-    Raw8<Q> x[NK];
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      x[j].load(static_cast<const Q*>(a.q) + at + 8 * j);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j].get(e)));
-    }
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    const int up = m > 0.f && m < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;  // the row's largest below 2^14
+    const int up = query_shift<D>(x[t]);
     c[t] = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
-      if (!ROWS && j % kAttnWaves != wave) continue;
+      if (j % kAttnWaves != wave) continue;
       Operand hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float v0 = ldexpf(x[j].get(key_channel<BITS>(e)), up - key_factor<BITS>(e));
-        const float v1 = ldexpf(x[j].get(key_channel<BITS>(e + 1)), up - key_factor<BITS>(e + 1));
-        hi.p[e / 2] = h2{static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
-        lo.p[e / 2] = h2{static_cast<_Float16>(fmaf(static_cast<float>(hi.p[e / 2][0]), -1.f, v0)),
-                         static_cast<_Float16>(fmaf(static_cast<float>(hi.p[e / 2][1]), -1.f, v1))};
-      }
-      mine[t][j][0][lane] = u4{hi.w[0], hi.w[1], hi.w[2], hi.w[3]};
-      if constexpr (PAIR) mine[t][j][1][lane] = u4{lo.w[0], lo.w[1], lo.w[2], lo.w[3]};
+      query_operands<BITS>(x[t][j], up, &hi, &lo);
+      lds.queries()[t][j][0][lane] = u4{hi.w[0], hi.w[1], hi.w[2], hi.w[3]};
+      if constexpr (PAIR) lds.queries()[t][j][1][lane] = u4{lo.w[0], lo.w[1], lo.w[2], lo.w[3]};
     }
   }
-  if constexpr (!ROWS) __syncthreads();
-  auto query_operand = [&](int t, int j, int p) { return __builtin_bit_cast(h8, mine[t][j][p][lane]); };
+  __syncthreads();
+  auto query_operand = [&](int t, int j, int p) { return __builtin_bit_cast(h8, lds.queries()[t][j][p][lane]); };
   // The products start from what the codes' offset adds to them, taken off.
   f4 start[R];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     f4 sum = {0.f, 0.f, 0.f, 0.f};
-    Operand offset;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) offset.w[p] = BITS == 8 || p % 2 ? 0x00800080u : 0x00080008u;
 #pragma unroll
     for (int j = 0; j < NK; ++j)
 #pragma unroll
       for (int p = HALVES - 1; p >= 0; --p)
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset.h, query_operand(t, j, p), sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), query_operand(t, j, p), sum, 0, 0, 0);
     start[t] = -sum;
   }
 
-  f4 o[R][NV];
-  float ref[R], l[R];
+  RowState<NV> state[R];
 #pragma unroll
-  for (int t = 0; t < R; ++t) {
-    ref[t] = kUnset;
-    l[t] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) o[t][j] = f4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int t = 0; t < R; ++t) state[t].clear();
   const Masks masks;
 
   int turn = 0;  // steps into the 32 whose pages are at hand
@@ -403,9 +588,8 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
   // loads would make every wait one for all of them.)
   auto take = [&](int step, auto last_step) {
     constexpr bool LAST = decltype(last_step)::value;
-    const int tok0 = step * kStep;
     const bool bad0 = p0 < 0, bad1 = p1 < 0;
-    const bool partly = bad0 || bad1 || tok0 + kStep > all_see;  // some row does not see some token
+    const bool partly = bad0 || bad1 || (step + 1) * kStep > all_see;  // some row does not see some token
 
     asm volatile("" ::: "memory");  // the queries are read again, not kept in registers
     f4 sc[R][2];
@@ -413,7 +597,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
     for (int j = 0; j < NK; ++j) {
       h8 k[2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS>(keys.k[half], j, masks);
+      for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS>(keys + half * KW, j, masks);
 #pragma unroll
       for (int t = 0; t < R; ++t)
 #pragma unroll
@@ -429,74 +613,23 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
 #pragma unroll
     for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) kc[t][i] = keys.s[i / 4][i % 4] * c[t];
+      for (int i = 0; i < 8; ++i) kc[t][i] = ks[i / 4][i % 4] * c[t];
     if constexpr (!LAST) {
       if (++turn == 32) {
-        pages = pages_from(step + kStride);
+        pages = Pages::checked(a, table.raw(a, step + kAttnWaves, kAttnWaves, lane));
         turn = 0;
       }
       p0 = __builtin_amdgcn_readlane(pages, 2 * turn);
       p1 = __builtin_amdgcn_readlane(pages, 2 * turn + 1);
-      rows_of(step + kStride, p0, p1);
-      keys.load(a, rb, r, g);
+      rows_of(a, h, step + kAttnWaves, p0, p1, rb);
+      load_keys<D, BITS>(a, rb, r, g, keys);
+      load_scales(a.ks, rb, g, ks);
     }
 
-    Operand w[R][2];  // hi, lo
+    Operand w[R][2];
 #pragma unroll
-    for (int t = 0; t < R; ++t) {
-      float x[8], vs[8], wt[8], sum, top;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = sc[t][i / 4][i % 4];
-        vs[i] = values.s[i / 4][i % 4];
-      }
-      if (partly) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = tok0 + 16 * (i / 4) + 4 * g + i % 4;
-          if (tok >= limit[t] || (i < 4 ? bad0 : bad1)) {  // whatever the scales there are
-            x[i] = -INFINITY;
-            kc[t][i] = 1.f;
-            vs[i] = 0.f;
-          }
-        }
-      }
-      auto weigh = [&]() {
-        sum = 0.f;
-        top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[t][i], -ref[t]));
-          wt[i] = p * vs[i];
-          sum += p;
-          top = fmaxf(top, wt[i]);
-        }
-      };
-      weigh();
-      if (__any(top > 16384.f || sum > 1.15292150e18f)) {
-        float u = kUnset;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[t][i], exponent(vs[i])));
-        u = fmaxf(u, __shfl_xor(u, 16));
-        u = fmaxf(u, __shfl_xor(u, 32));
-        const float moved = fmaxf(ref[t], u - 8.f);
-        const float f = __builtin_amdgcn_exp2f(ref[t] - moved);
-        ref[t] = moved;
-        l[t] *= f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) o[t][j] *= f;
-        weigh();
-      }
-      l[t] += sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const auto hi = __builtin_amdgcn_cvt_pkrtz(wt[2 * i], wt[2 * i + 1]);
-        const auto lo = __builtin_amdgcn_cvt_pkrtz(fmaf(static_cast<float>(hi[0]), -1.f, wt[2 * i]),
-                                                   fmaf(static_cast<float>(hi[1]), -1.f, wt[2 * i + 1]));
-        w[t][0].w[i] = __builtin_bit_cast(uint32_t, hi);
-        w[t][1].w[i] = __builtin_bit_cast(uint32_t, lo);
-      }
-    }
+    for (int t = 0; t < R; ++t)
+      weigh_step<NV>(sc[t], kc[t], vs, partly, limit[t], step * kStep + 4 * g, bad0, bad1, state[t], w[t]);
 
 #pragma unroll
     for (int j = 0; j < NV / 4; ++j) {
@@ -508,147 +641,406 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int t = 0; t < R; ++t)
-            o[t][4 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][p].h, o[t][4 * j + e], 0, 0, 0);
+            state[t].o[4 * j + e] =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][p].h, state[t].o[4 * j + e], 0, 0, 0);
     }
-    if constexpr (!LAST) values.load(a, rb, r, g);
+    if constexpr (!LAST) {
+      load_values<D, BITS>(a, rb, r, g, values);
+      load_scales(a.vs, rb, g, vs);
+    }
   };
   if (begin < end) {
     int step = begin;
-    for (; step + kStride < end; step += kStride) take(step, std::false_type{});
+    for (; step + kAttnWaves < end; step += kAttnWaves) take(step, std::false_type{});
     take(step, std::true_type{});
   }
 
+  // The waves' shares are brought to one reference and added up, in the order of
+  // the waves, each wave taking a quarter of the channels.
+  if constexpr (TokensLds<D, PAIR, R>::kShare) __syncthreads();  // the queries are used up
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    l[t] += __shfl_xor(l[t], 16);
-    l[t] += __shfl_xor(l[t], 32);
-  }
-
-  // The waves' shares of the same rows: brought to one reference, added up in
-  // wave 0, in the order (0 + 2) + (1 + 3).
-  if constexpr (!ROWS) {
-    __shared__ float stat[kAttnWaves][R][16][2];
-    __shared__ f4 lds[2][R * NV][64];
+    float l = state[t].l;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
     if (g == 0) {
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        stat[wave][t][r][0] = ref[t];
-        stat[wave][t][r][1] = l[t];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      float top = kUnset;
-#pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, stat[k][t][r][0]);
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k) {
-        sum += __builtin_amdgcn_exp2f(stat[k][t][r][0] - top) * stat[k][t][r][1];
-      }
-      const float f = __builtin_amdgcn_exp2f(ref[t] - top);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) o[t][j] *= f;
-      ref[t] = top;
-      l[t] = sum;
+      lds.stat[wave][t][r][0] = state[t].ref;
+      lds.stat[wave][t][r][1] = l;
     }
 #pragma unroll
-    for (int far = 2; far >= 1; far >>= 1) {
-      if (wave >= far && wave < 2 * far) {
-#pragma unroll
-        for (int t = 0; t < R; ++t)
-#pragma unroll
-          for (int j = 0; j < NV; ++j) lds[wave - far][t * NV + j][lane] = o[t][j];
-      }
-      __syncthreads();
-      if (wave < far) {
-#pragma unroll
-        for (int t = 0; t < R; ++t)
-#pragma unroll
-          for (int j = 0; j < NV; ++j) o[t][j] += lds[wave][t * NV + j][lane];
-      }
-      __syncthreads();
-    }
-    if (wave != 0) return;
+    for (int j = 0; j < NV; ++j) lds.o[wave][t * NV + j][lane] = state[t].o[j];
   }
-
-  // Lane (r, g) holds channels [g D / 4, +D / 4) of its row: NV i + j is o[j][i].
-  const bool whole = eff == 1 && !front && !a.prefix_table;
+  __syncthreads();
+  const Partial partial(a, plan);
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     const int row = row0 + 16 * t + r;
+    float top = kUnset, f[kAttnWaves], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, lds.stat[k][t][r][0]);
+#pragma unroll
+    for (int k = 0; k < kAttnWaves; ++k) {
+      f[k] = __builtin_amdgcn_exp2f(lds.stat[k][t][r][0] - top);
+      l += f[k] * lds.stat[k][t][r][1];
+    }
+    // Channels of this wave: its quarter of each lane's NV (i, 0 .. NV - 1).
+    constexpr int Q4 = NV / 4;
+    f4 sum[Q4];
+#pragma unroll
+    for (int j = 0; j < Q4; ++j) {
+      sum[j] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kAttnWaves; ++k) sum[j] += f[k] * lds.o[k][t * NV + wave * Q4 + j][lane];
+    }
     if (row >= span.rows) continue;
-    const int64_t token = span.first + query_of(row);
-    const int head = h * a.group + row - query_of(row) * a.group;
+    const int query = a.group.quotient(row);
+    const int64_t token = span.first + query;
+    const int head = h * a.group.d + row - query * a.group.d;
+    const int c = g * (D / 4) + wave * Q4;  // + NV i + j
     if (whole) {
-      const float f = l[t] == 0.f ? 0.f : 1.f / l[t];
-      const int64_t at = token * a.ldo + static_cast<int64_t>(head) * D + g * (D / 4);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t to = token * a.ldo + static_cast<int64_t>(head) * D + c;
 #pragma unroll
-      for (int e = 0; e < D / 4; e += 8) {
-        float v[8];
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = o[t][(e + k) % NV][(e + k) / NV] * f;
-        if (a.out_f16)
-          store_whole8(static_cast<_Float16*>(a.out) + at + e, v);
-        else
-          store_whole8(static_cast<float*>(a.out) + at + e, v);
-      }
+        for (int j = 0; j < Q4; ++j) {
+          if (a.out_f16)
+            static_cast<_Float16*>(a.out)[to + NV * i + j] = static_cast<_Float16>(sum[j][i] * inv);
+          else
+            static_cast<float*>(a.out)[to + NV * i + j] = sum[j][i] * inv;
+        }
     } else {
-      const int64_t at = (static_cast<int64_t>(slot0 + part) * a.tokens + token) * a.q_heads + head;
-      float* po = a.partial + at * D + g * (D / 4);
+      const int64_t at = partial.row(a, plan, front, slot, token, query, head);
+      float* po = partial.o(a, at) + c;
 #pragma unroll
-      for (int e = 0; e < D / 4; e += 4)
-        *reinterpret_cast<f4*>(po + e) = f4{o[t][e % NV][e / NV], o[t][(e + 1) % NV][(e + 1) / NV],
-                                            o[t][(e + 2) % NV][(e + 2) / NV], o[t][(e + 3) % NV][(e + 3) / NV]};
-      if (g == 0) {
-        float* st = a.partial + static_cast<int64_t>(slots) * a.tokens * a.q_heads * D + at * 2;
-        st[0] = ref[t];
-        st[1] = l[t];
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < Q4; ++j) po[NV * i + j] = sum[j][i];
+      if (g == 0 && wave == 0) {
+        float* st = partial.stat(a, at);
+        st[0] = top;
+        st[1] = l;
       }
     }
   }
+}
+template <int D, int BITS, bool PAIR, int R>
+__device__ __forceinline__ void tokens_body(const AttentionArgs& a, const AttentionPlan& plan, int front,
+                                            uint32_t block, TokensLds<D, PAIR, R>& lds) {
+  const AttentionCut& cut = front ? plan.front : plan.own;
+  const int lane = threadIdx.x & 63;
+  const int w = a.by_heads.quotient(block), h = block - w * a.heads;
+  const bool single = (front || a.seqs == 1) && cut.one_piece;  // its table need not wait for its length
+  int s = 0, start = 0, from = w, end = w + 1, each = 1;
+  if (!single) {
+    const Run run(a, cut, front, w, lane);
+    s = run.s;
+    start = run.start;
+    from = run.first;
+    end = run.end;
+    each = run.each;
+  }
+  const int first = from;
+  for (; from < end; ++s) {
+    int to = end, whole = -1, n = 0;
+    if (!single) {
+      const int64_t cap = (front ? a.prefix_width : a.width) << a.page_log2;
+      n = pieces_of(clamp_length((front ? a.prefix_length : a.lengths)[s], cap), cut);
+      to = end < start + n ? end : start + n;
+      const bool all = from == start && to == start + n;
+      whole = all && !front && !a.prefix_table;
+      // Slots of a sequence follow one another: its runs, counted from its number.
+      if (plan.join && from == start && h == 0 && threadIdx.x == 0) {
+        int32_t* m = Partial(a, plan).slots(a, front ? a.seqs : s);
+        m[0] = front ? 0 : w + s;
+        m[1] = all ? 1 : static_cast<int>(static_cast<uint32_t>(start + n - 1) / static_cast<uint32_t>(each)) - w + 1;
+      }
+      if (from > first) __syncthreads();  // the section before has left LDS
+    }
+    tokens_section<D, BITS, PAIR, R>(a, plan, front, h, s, from - start, to - start, whole, front ? w : w + s, lds);
+    from = to;
+    start += n;
+  }
+}
+template <int D, int BITS, bool PAIR, int R>
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
+    attention_tokens_kernel(AttentionArgs a, AttentionPlan plan, int front) {
+  __shared__ TokensLds<D, PAIR, R> lds;
+  tokens_body<D, BITS, PAIR, R>(a, plan, front, blockIdx.x, lds);
+}
+
+// Many rows: a wave's 16 rows are its own, and the waves share the widening.
+// Two steps at a time go through LDS as operands, each wave bringing the keys
+// or the values of one of them, and all waves multiply both.
+template <int D>
+struct RowsLds {
+  static constexpr int kBlock = 2;
+  u4 k[kBlock][2][D / 32][64];
+  u4 v[kBlock][D / 16][64];
+  f4 ks[kBlock][8], vs[kBlock][8];
+};
+constexpr int kGroupRows = 16 * kAttnWaves;
+
+// Parts of a range of L tokens.
+__device__ __forceinline__ int parts_of(int64_t L, const AttentionCut& c) {
+  const uint32_t p = static_cast<uint32_t>(L) >> c.piece_log2;
+  return static_cast<int>(p < 1 ? 1 : p < c.parts.d ? p : c.parts.d);
 }
 
 template <int D, int BITS, bool PAIR>
-void launch_cut(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, hipStream_t st) {
-  const int64_t seqs = front ? 1 : a.seqs;
-  const dim3 grid(static_cast<unsigned>(seqs * c.row_groups * c.parts * a.heads)), block(kAttnWaves * 64);
-  if (c.rowsplit) {
-    if constexpr (D < 256) {
-      if (c.tiles == 2) {
-        hipLaunchKernelGGL((attention_kernel<D, BITS, PAIR, 2, true>), grid, block, 0, st, a, c, front, slot0, slots);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((attention_kernel<D, BITS, PAIR, 1, true>), grid, block, 0, st, a, c, front, slot0, slots);
-  } else {
-    if constexpr (D < 256) {
-      if (c.tiles == 2) {
-        hipLaunchKernelGGL((attention_kernel<D, BITS, PAIR, 2, false>), grid, block, 0, st, a, c, front, slot0, slots);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((attention_kernel<D, BITS, PAIR, 1, false>), grid, block, 0, st, a, c, front, slot0, slots);
+__device__ __forceinline__ void rows_body(const AttentionArgs& a, const AttentionPlan& plan, int front,
+                                          uint32_t place, RowsLds<D>& lds) {
+  constexpr int NK = D / 32, NV = D / 16;
+  constexpr int BLOCK = RowsLds<D>::kBlock;
+  constexpr int HALVES = PAIR ? 2 : 1;
+  const AttentionCut& cut = front ? plan.front : plan.own;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Workgroup (part, s, rg, h), h fastest, so that those of one length lie
+  // together; late row groups, which see most, first.
+  uint32_t id = a.by_heads.quotient(place);
+  const int h = place - id * a.heads;
+  uint32_t rest = cut.groups.quotient(id);
+  const int rg = cut.groups.d - 1 - (id - rest * cut.groups.d);
+  const uint32_t seqs = front ? 1 : a.seqs;
+  const int part = rest / seqs, s = rest - part * seqs;
+  const Pages table(a, s, front);
+  const Span span = front ? front_span(a) : own_span(a, s);
+  if (rg * kGroupRows >= span.rows) return;
+  const int parts = parts_of(span.length, cut);
+  if (part >= parts) return;
+  if (plan.join && part == 0 && rg == 0 && h == 0 && threadIdx.x == 0) {
+    int32_t* m = Partial(a, plan).slots(a, front ? a.seqs : s);
+    m[0] = 0;
+    m[1] = parts;
   }
+  const int row = rg * kGroupRows + wave * 16 + r;  // of this lane
+
+  const Sight sight(a, span, front);
+  const int first = row - r;  // of this wave
+  const int last = (first + 16 < span.rows ? first + 16 : span.rows) - 1;
+  const int group_last = ((rg + 1) * kGroupRows < span.rows ? (rg + 1) * kGroupRows : span.rows) - 1;
+  const int wave_steps = last >= first ? (sight.limit(a.group.quotient(last)) + kStep - 1) / kStep : 0;
+  const int all_see = first + 16 <= span.rows ? sight.limit(a.group.quotient(first)) : 0;
+  const int limit = row < span.rows ? sight.limit(a.group.quotient(row)) : 0;
+  const int steps = (sight.limit(a.group.quotient(group_last)) + kStep - 1) / kStep;
+  const int share = parts == 1 ? steps : static_cast<int>(static_cast<uint32_t>(steps + parts - 1) / static_cast<uint32_t>(parts));
+  const int begin = part * share;
+  const int end = begin + share < steps ? begin + share : steps;
+
+  int32_t pages = table.raw(a, begin, 1, lane), ahead = 0;  // of the 32 steps at hand and of the next
+  using Q = std::conditional_t<PAIR, float, _Float16>;
+  Raw8<Q> x[NK];
+  load_query<D>(a, span, h, row, g, x);
+
+  const bool brings_keys = wave < 2;
+  const int mine = wave & 1;  // the step of a block that this wave brings
+  uint32_t codes[Row<D, BITS>::kWords];
+  float scale = 0.f;  // of token lane, of the first 32 lanes
+  auto bring = [&](int step, int32_t from, int turn) {
+    if (step >= end) return;
+    int64_t rb[2];
+    rows_of(a, h, step, __builtin_amdgcn_readlane(from, 2 * turn), __builtin_amdgcn_readlane(from, 2 * turn + 1), rb);
+    const int64_t token = (lane & 16 ? rb[1] : rb[0]) + r;
+    if (brings_keys) {
+      load_keys<D, BITS>(a, rb, r, g, codes);
+      scale = a.ks[token];
+    } else {
+      load_values<D, BITS>(a, rb, r, g, codes);
+      scale = a.vs[token];
+    }
+  };
+  pages = Pages::checked(a, pages);
+  bring(begin + mine, pages, mine);
+
+  Operand q[NK][HALVES];
+  const int up = query_shift<D>(x);
+  const float c = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
+  f4 start = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NK; ++j) {
+    Operand lo;
+    query_operands<BITS>(x[j], up, &q[j][0], &lo);
+    if constexpr (PAIR) q[j][1] = lo;
+#pragma unroll
+    for (int p = HALVES - 1; p >= 0; --p)
+      start = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), q[j][p].h, start, 0, 0, 0);
+  }
+  start = -start;
+  RowState<NV> state;
+  state.clear();
+  const Masks masks;
+
+  for (int block = begin; block < end; block += BLOCK) {
+    const int turn = (block - begin) & 31;
+    if (turn == 0 && block > begin) pages = ahead;
+    __syncthreads();  // the block before is used up
+    if (block + mine < end) {
+      if (brings_keys) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+            lds.k[mine][half][j][lane] =
+                __builtin_bit_cast(u4, key_operand<BITS>(codes + half * Row<D, BITS>::kKeyWords, j, masks));
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV / 4; ++j) {
+          Operand v[4];
+          value_operands<D, BITS>(codes, j, masks, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) lds.v[mine][4 * j + e][lane] = __builtin_bit_cast(u4, v[e].h);
+        }
+      }
+      if (lane < 32) reinterpret_cast<float*>(brings_keys ? lds.ks[mine] : lds.vs[mine])[lane] = scale;
+    }
+    if (((block + BLOCK - begin) & 31) == 0 && block + BLOCK < end) {
+      ahead = Pages::checked(a, table.raw(a, block + BLOCK, 1, lane));
+      bring(block + BLOCK + mine, ahead, mine);
+    } else {
+      bring(block + BLOCK + mine, pages, (turn + BLOCK + mine) & 31);
+    }
+    __syncthreads();
+
+    for (int b = 0; b < BLOCK; ++b) {
+      const int step = block + b;
+      if (step >= end || step >= wave_steps) break;
+      const bool bad0 = __builtin_amdgcn_readlane(pages, 2 * (turn + b)) < 0;
+      const bool bad1 = __builtin_amdgcn_readlane(pages, 2 * (turn + b) + 1) < 0;
+      const bool partly = bad0 || bad1 || (step + 1) * kStep > all_see;
+      f4 sc[2];
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const h8 k = __builtin_bit_cast(h8, lds.k[b][half][j][lane]);
+#pragma unroll
+          for (int p = HALVES - 1; p >= 0; --p)
+            sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[j][p].h, j == 0 && p == HALVES - 1 ? start : sc[half],
+                                                              0, 0, 0);
+        }
+      }
+      const f4 ks[2] = {lds.ks[b][g], lds.ks[b][4 + g]}, vs[2] = {lds.vs[b][g], lds.vs[b][4 + g]};
+      float kc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) kc[i] = ks[i / 4][i % 4] * c;
+      Operand w[2];
+      weigh_step<NV>(sc, kc, vs, partly, limit, step * kStep + 4 * g, bad0, bad1, state, w);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const h8 v = __builtin_bit_cast(h8, lds.v[b][j][lane]);
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+          state.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[p].h, state.o[j], 0, 0, 0);
+      }
+    }
+  }
+
+  state.l += __shfl_xor(state.l, 16);
+  state.l += __shfl_xor(state.l, 32);
+  if (row >= span.rows) return;
+  const int query = a.group.quotient(row);
+  const int64_t token = span.first + query;
+  const int head = h * a.group.d + row - query * a.group.d;
+  // Lane (r, g) holds channels [g D / 4, +D / 4): NV i + j is o[j][i].
+  if (parts == 1 && !front && !a.prefix_table) {
+    const float f = state.l == 0.f ? 0.f : 1.f / state.l;
+    const int64_t at = token * a.ldo + static_cast<int64_t>(head) * D + g * (D / 4);
+#pragma unroll
+    for (int e = 0; e < D / 4; e += 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = state.o[(e + k) % NV][(e + k) / NV] * f;
+      if (a.out_f16)
+        store_whole8(static_cast<_Float16*>(a.out) + at + e, v);
+      else
+        store_whole8(static_cast<float*>(a.out) + at + e, v);
+    }
+  } else {
+    const Partial partial(a, plan);
+    const int64_t at = partial.row(a, plan, front, part, token, query, head);
+    float* po = partial.o(a, at) + g * (D / 4);
+#pragma unroll
+    for (int e = 0; e < D / 4; e += 4)
+      *reinterpret_cast<f4*>(po + e) = f4{state.o[e % NV][e / NV], state.o[(e + 1) % NV][(e + 1) / NV],
+                                          state.o[(e + 2) % NV][(e + 2) / NV], state.o[(e + 3) % NV][(e + 3) / NV]};
+    if (g == 0) {
+      float* f = partial.stat(a, at);
+      f[0] = state.ref;
+      f[1] = state.l;
+    }
+  }
+}
+template <int D, int BITS, bool PAIR>
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
+    attention_rows_kernel(AttentionArgs a, AttentionPlan plan, int front) {
+  __shared__ RowsLds<D> lds;
+  rows_body<D, BITS, PAIR>(a, plan, front, blockIdx.x, lds);
+}
+
+// A prefix with many rows and own tokens with few, as in decoding: both in one
+// launch, the prefix's workgroups first.
+template <int D, int BITS, bool PAIR>
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
+    attention_both_kernel(AttentionArgs a, AttentionPlan plan, uint32_t front_blocks) {
+  __shared__ union Lds {
+    RowsLds<D> rows;
+    TokensLds<D, PAIR, 1> tokens;
+    __device__ Lds() {}
+  } lds;
+  if (blockIdx.x < front_blocks)
+    rows_body<D, BITS, PAIR>(a, plan, 1, blockIdx.x, lds.rows);
+  else
+    tokens_body<D, BITS, PAIR, 1>(a, plan, 0, blockIdx.x - front_blocks, lds.tokens);
+}
+
+// Workgroups of a cut.
+inline int64_t cut_blocks(const AttentionArgs& a, const AttentionCut& c, int64_t seqs) {
+  return a.heads * (c.rowsplit ? seqs * c.groups.d * c.parts.d : static_cast<int64_t>(c.groups.d));
+}
+
+template <int D, int BITS, bool PAIR>
+void launch_cut(const AttentionArgs& a, const AttentionPlan& plan, int front, hipStream_t st) {
+  const AttentionCut& c = front ? plan.front : plan.own;
+  const dim3 block(kAttnWaves * 64), grid(static_cast<unsigned>(cut_blocks(a, c, front ? 1 : a.seqs)));
+  if (c.rowsplit) {
+    hipLaunchKernelGGL((attention_rows_kernel<D, BITS, PAIR>), grid, block, 0, st, a, plan, front);
+    return;
+  }
+  if constexpr (D < 256) {
+    if (c.tiles == 2) {
+      hipLaunchKernelGGL((attention_tokens_kernel<D, BITS, PAIR, 2>), grid, block, 0, st, a, plan, front);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((attention_tokens_kernel<D, BITS, PAIR, 1>), grid, block, 0, st, a, plan, front);
+}
+
+template <int D, int BITS, bool PAIR>
+void launch_parts(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t st) {
+  if (a.prefix_table && plan.front.rowsplit && !plan.own.rowsplit && plan.own.tiles == 1) {
+    const int64_t front = cut_blocks(a, plan.front, 1);
+    const dim3 grid(static_cast<unsigned>(front + cut_blocks(a, plan.own, a.seqs)));
+    hipLaunchKernelGGL((attention_both_kernel<D, BITS, PAIR>), grid, dim3(kAttnWaves * 64), 0, st, a, plan,
+                       static_cast<uint32_t>(front));
+    return;
+  }
+  if (a.prefix_table) launch_cut<D, BITS, PAIR>(a, plan, 1, st);
+  launch_cut<D, BITS, PAIR>(a, plan, 0, st);
 }
 
 template <int D>
-void launch_head_dim(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                     hipStream_t st) {
+void launch_head_dim(const AttentionArgs& a, const AttentionPlan& plan, bool pair, hipStream_t st) {
   if (a.bits == 4)
-    pair ? launch_cut<D, 4, true>(a, c, front, slot0, slots, st) : launch_cut<D, 4, false>(a, c, front, slot0, slots, st);
+    pair ? launch_parts<D, 4, true>(a, plan, st) : launch_parts<D, 4, false>(a, plan, st);
   else
-    pair ? launch_cut<D, 8, true>(a, c, front, slot0, slots, st) : launch_cut<D, 8, false>(a, c, front, slot0, slots, st);
+    pair ? launch_parts<D, 8, true>(a, plan, st) : launch_parts<D, 8, false>(a, plan, st);
 }
 
 }  // namespace
 
-void launch_attention_64(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                         hipStream_t st);
-void launch_attention_128(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                          hipStream_t st);
-void launch_attention_256(const AttentionArgs& a, const AttentionCut& c, int front, int slot0, int slots, bool pair,
-                          hipStream_t st);
+void launch_attention_64(const AttentionArgs& a, const AttentionPlan& plan, bool pair, hipStream_t st);
+void launch_attention_128(const AttentionArgs& a, const AttentionPlan& plan, bool pair, hipStream_t st);
+void launch_attention_256(const AttentionArgs& a, const AttentionPlan& plan, bool pair, hipStream_t st);
 
 }  // namespace w4a4

@@ -72,7 +72,8 @@ int attention_sizes(const w4a4_cache* c, int64_t tokens, int64_t q_heads, int64_
   a->pages = static_cast<int>(c->pages); a->heads = static_cast<int>(c->heads);
   a->page_log2 = log2_of(c->page_size); a->D = static_cast<int>(c->head_dim); a->bits = c->bits;
   a->tokens = static_cast<int>(tokens); a->q_heads = static_cast<int>(q_heads);
-  a->group = static_cast<int>(q_heads / c->heads);
+  a->group = w4a4::Divisor(static_cast<uint32_t>(q_heads / c->heads));
+  a->by_heads = w4a4::Divisor(static_cast<uint32_t>(c->heads));
   a->seqs = static_cast<int>(seqs); a->width = width;
   // A sequence has no more queries than there are.
   a->max_q = static_cast<int>(max_q < tokens ? max_q : tokens > 0 ? tokens : 1);

@@ -46,6 +46,20 @@ hipError_t launch_cache_write(const CacheArgs& a, bool f16, hipStream_t st);
 hipError_t launch_cache_read(const CacheArgs& a, bool f16, hipStream_t st);
 
 // ---- attention over the cache (attention.hip) -------------------------------------
+// Division of numbers below 2^31 by one that the host knows: q = (hi(n m) + n) >> s
+// with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+struct Divisor {
+  uint32_t d = 1, m = 1, s = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t v) : d(v) {
+    while ((uint64_t{1} << s) < d) ++s;
+    m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << s) - d) / d + 1);
+  }
+  __host__ __device__ uint32_t quotient(uint32_t n) const {
+    return (static_cast<uint32_t>(static_cast<uint64_t>(n) * m >> 32) + n) >> s;
+  }
+};
+
 struct AttentionArgs {
   const uint8_t* k;
   const uint8_t* v;
@@ -54,7 +68,9 @@ struct AttentionArgs {
   int pages, heads, page_log2, D, bits;
   const void* q;
   int64_t ldq;
-  int tokens, q_heads, group;  // group: query heads to a cache head
+  int tokens, q_heads;
+  Divisor group;  // query heads to a cache head
+  Divisor by_heads;  // heads
   const int32_t* tables;
   int seqs;
   int64_t width;
@@ -71,17 +87,25 @@ struct AttentionArgs {
   float* partial;  // workspace, or null
 };
 
-// How a call is cut.  `own`: the sequences' own tokens, in up to own_parts
-// parts of at least own_least tokens each; `front`: the prefix, the same.
-// A workgroup takes 16 * tiles rows (its waves sharing the tokens) or, with
-// rowsplit, four times as many (a wave's rows its own).
+// How the tokens of the sequences (own), or of the prefix (front), are cut.
+// Few rows (rowsplit 0): a workgroup takes 16 * tiles rows of a cache head, its
+// waves sharing the tokens.  Tokens come in pieces of 2^piece_log2, and each of
+// `groups` workgroups of a head takes an equal run of the pieces of all
+// sequences (`groups` ones of the prefix).
+// Many rows: it takes 64, a wave's 16 its own; `groups` is the row groups of a
+// sequence (or of all queries), and their tokens are cut into up to `parts`
+// equal parts of 2^piece_log2 or more.
 struct AttentionCut {
-  int tiles, rowsplit, parts, least;
-  int64_t row_groups;  // workgroups' rows per sequence (own) or in all (front)
+  int tiles, rowsplit, piece_log2;
+  int one_piece;  // few rows: a workgroup of a head for every piece there can be
+  Divisor groups;
+  Divisor parts;
 };
 struct AttentionPlan {
   AttentionCut own, front;
-  int64_t slots;  // partial results of a row, 0: results are stored at once
+  int join;                  // partial results are joined by another launch
+  int64_t own_slots;         // [own_slots][rows of a slot]: few rows: the runs' sections, many: the parts
+  int64_t front_slots;
 };
 bool attention_plan(const AttentionArgs& a, AttentionPlan* plan);
 size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& plan);
