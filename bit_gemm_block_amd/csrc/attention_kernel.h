@@ -96,17 +96,6 @@ __device__ __forceinline__ h2 two_bytes(uint32_t w1, uint32_t w0) {
   return v.h - h2{1152.f16, 1152.f16};
 }
 
-// Constants that stay in registers: with two literals the mask and the sign's
-// flip below would be two instructions.
-struct Masks {
-  uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
-  uint32_t key_even = 0x00080008u, key_odd = 0x00800080u;
-  uint32_t value_even = 0x64086408u, value_odd = 0x64806480u;
-  __device__ __forceinline__ Masks() {
-    asm("" : "+s"(even), "+s"(odd), "+v"(key_even), "+v"(key_odd), "+v"(value_even), "+v"(value_odd));
-  }
-};
-
 // A step's codes as a lane holds them: of the keys, its share of token r of both
 // halves; of the values, its channels of tokens 4 g + i of both.
 template <int D, int BITS>
@@ -209,16 +198,7 @@ __device__ __forceinline__ void value_operands(const uint32_t* v, int q, const M
     uint32_t w0 = v[2 * p * VW + word], w1 = v[(2 * p + 1) * VW + word];
     if constexpr (BITS == 4) {
       const uint32_t t = __builtin_amdgcn_perm(w1, w0, q % 2 ? 0x07060302u : 0x05040100u);
-      const uint32_t u = t >> 8;
-      o[0].w[p] = (t & m.even) ^ m.value_even;
-      o[1].w[p] = (t & m.odd) ^ m.value_odd;
-      o[2].w[p] = (u & m.even) ^ m.value_even;
-      o[3].w[p] = (u & m.odd) ^ m.value_odd;
-      const h2 off = {1032.f16, 1032.f16}, sixteenth = {0.0625f16, 0.0625f16}, off16 = {-72.f16, -72.f16};
-      o[0].p[p] -= off;
-      o[1].p[p] = __builtin_elementwise_fma(o[1].p[p], sixteenth, off16);
-      o[2].p[p] -= off;
-      o[3].p[p] = __builtin_elementwise_fma(o[3].p[p], sixteenth, off16);
+      nibbles_to_f16(t, m, &o[0].p[p], &o[1].p[p], &o[2].p[p], &o[3].p[p]);
     } else {
       w0 ^= 0x80808080u;
       w1 ^= 0x80808080u;

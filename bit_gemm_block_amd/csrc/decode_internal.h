@@ -7,6 +7,20 @@
 
 namespace w4a4 {
 
+// Division of numbers below 2^31 by one that the host knows: q = (hi(n m) + n) >> s
+// with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+struct Divisor {
+  uint32_t d = 1, m = 1, s = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t v) : d(v) {
+    while ((uint64_t{1} << s) < d) ++s;
+    m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << s) - d) / d + 1);
+  }
+  __host__ __device__ uint32_t quotient(uint32_t n) const {
+    return (static_cast<uint32_t>(static_cast<uint64_t>(n) * m >> 32) + n) >> s;
+  }
+};
+
 // ---- a projection with 4-bit weights and unquantized activations (w4a16.hip) ----
 struct W4a16Args {
   const void* x;  // [M, K], row distance ldx
@@ -16,17 +30,18 @@ struct W4a16Args {
   const void* sw;  // [N, K / group]
   int sw_f16;
   int64_t M, N;
-  int K, group;  // group K: one scale per channel
+  int K, groups;         // groups of K a channel, each with its scale
+  Divisor group_halves;  // 64s of K to a group
   void* y;       // [M, N], row distance ldy
   int y_f16;
   int64_t ldy;
   float* partial;  // workspace: [parts][M][N], or null
 };
 
-// How a call is cut: 16 nb output channels and 16 mt rows to a workgroup, whose
-// waves share the channels' K; parts of K over workgroups.
+// How a call is cut: 16 nb output channels to a workgroup (up to 16 rows) or a
+// wave, 16 mt rows, K in parts that another launch adds up.
 struct W4a16Plan {
-  int nb, mt, waves, parts;
+  int nb, mt, parts;
 };
 W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K);
 hipError_t launch_w4a16(const W4a16Args& a, bool x_f16, hipStream_t st);
@@ -46,20 +61,6 @@ hipError_t launch_cache_write(const CacheArgs& a, bool f16, hipStream_t st);
 hipError_t launch_cache_read(const CacheArgs& a, bool f16, hipStream_t st);
 
 // ---- attention over the cache (attention.hip) -------------------------------------
-// Division of numbers below 2^31 by one that the host knows: q = (hi(n m) + n) >> s
-// with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
-struct Divisor {
-  uint32_t d = 1, m = 1, s = 0;
-  Divisor() = default;
-  explicit Divisor(uint32_t v) : d(v) {
-    while ((uint64_t{1} << s) < d) ++s;
-    m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << s) - d) / d + 1);
-  }
-  __host__ __device__ uint32_t quotient(uint32_t n) const {
-    return (static_cast<uint32_t>(static_cast<uint64_t>(n) * m >> 32) + n) >> s;
-  }
-};
-
 struct AttentionArgs {
   const uint8_t* k;
   const uint8_t* v;

@@ -26,31 +26,33 @@ union Operand {
   b8 b;
 };
 
-// Two nibbles at bits 0 and 16 (UP: 4 and 20) of unsigned codes, minus 8.
-template <bool UP>
-__device__ __forceinline__ h2 nibbles(uint32_t w) {
-  union {
-    uint32_t u;
-    h2 h;
-  } v;
-  if constexpr (UP) {
-    v.u = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 u
-    return __builtin_elementwise_fma(v.h, h2{0.0625f16, 0.0625f16}, h2{-72.f16, -72.f16});
-  } else {
-    v.u = (w & 0x000f000fu) | 0x64006400u;
-    return v.h - h2{1032.f16, 1032.f16};
+// Constants that stay in registers: with two literals the mask and what follows
+// it would be two instructions.
+struct Masks {
+  uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
+  uint32_t key_even = 0x00080008u, key_odd = 0x00800080u;
+  uint32_t value_even = 0x64086408u, value_odd = 0x64806480u;
+  __device__ __forceinline__ Masks() {
+    asm("" : "+s"(even), "+s"(odd), "+v"(key_even), "+v"(key_odd), "+v"(value_even), "+v"(value_odd));
   }
+};
+
+// Nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word of codes as fp16: flipping
+// the sign bit in the same instruction makes u = q + 8 of the code (a nibble
+// higher up counts 16 times).
+__device__ __forceinline__ void nibbles_to_f16(uint32_t w, const Masks& m, h2* even0, h2* odd0, h2* even1, h2* odd1) {
+  const uint32_t s = w >> 8;
+  const h2 off = {1032.f16, 1032.f16}, sixteenth = {0.0625f16, 0.0625f16}, off16 = {-72.f16, -72.f16};
+  *even0 = __builtin_bit_cast(h2, (w & m.even) ^ m.value_even) - off;
+  *odd0 = __builtin_elementwise_fma(__builtin_bit_cast(h2, (w & m.odd) ^ m.value_odd), sixteenth, off16);
+  *even1 = __builtin_bit_cast(h2, (s & m.even) ^ m.value_even) - off;
+  *odd1 = __builtin_elementwise_fma(__builtin_bit_cast(h2, (s & m.odd) ^ m.value_odd), sixteenth, off16);
 }
 
 // The eight codes of a word as fp16, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ Operand int4_to_f16(uint32_t w) {
-  w ^= 0x88888888u;
-  const uint32_t s = w >> 8;
+__device__ __forceinline__ Operand int4_to_f16(uint32_t w, const Masks& m) {
   Operand o;
-  o.p[0] = nibbles<false>(w);
-  o.p[1] = nibbles<true>(w);
-  o.p[2] = nibbles<false>(s);
-  o.p[3] = nibbles<true>(s);
+  nibbles_to_f16(w, m, &o.p[0], &o.p[1], &o.p[2], &o.p[3]);
   return o;
 }
 // Eight fp16 values to that order.

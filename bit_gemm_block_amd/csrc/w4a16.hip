@@ -3,14 +3,11 @@
 //
 //   y[m, n] = sum_j s[n, j] sum_{k in group j} x[m, k] q[n, k]
 //
-// A wave takes 16 NB output channels and 16 MT rows (rows past M repeat the
-// last one and are not stored) over some of K's tiles of 128: lane 16 g + r
-// loads the 16 bytes that hold codes [32 g, +32) of channel r, which in tiled
-// weights makes one run of 1 KB, and widens each word to an operand of the
-// 16 x 16 x 32 matrix instruction.  The order of K inside an instruction is
-// free, so x is brought to the codes' order: 32 of its elements to a lane.
-// The waves of a workgroup share the channels' tiles, next to each other, and
-// add up through LDS in a fixed order.
+// Weights come in tiles of 16 channels and 128 of K: lane 16 g + r loads the 16
+// bytes that hold codes [32 g, +32) of channel r, which in tiled weights makes
+// one run of 1 KB, and widens each word to an operand of the 16 x 16 x 32
+// matrix instruction.  The order of K inside an instruction is free, so x is
+// brought to the codes' order.
 //
 // fp16 x meets fp16 codes.  float32 x enters as three bfloat16 parts.  Products
 // are exact in both, sums float32.  A tile whose halves have different scales
@@ -23,159 +20,331 @@
 namespace w4a4 {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 8;      // of a workgroup, few rows
+constexpr int kManyWaves = 4;  // many rows
 
 enum Groups { WHOLE = 0, TILES = 1, HALVES = 2 };  // scales: one per channel, per tiles, per half tiles
 
+// Where a lane's codes of 16 channels lie.
+struct Channels {
+  const uint8_t* p;
+  int64_t n;      // the lane's channel (the last one past N)
+  int64_t scale;  // its first scale
+  __device__ __forceinline__ void set(const W4a16Args& a, int64_t block, int lane) {
+    const int64_t last = (a.N - 1) / 16;
+    block = block < last ? block : last;  // a block past the last one repeats it
+    n = block * 16 + (lane & 15);
+    n = n < a.N ? n : a.N - 1;
+    p = a.tiled ? a.wq + block * (8 * static_cast<int64_t>(a.K)) + lane * 16 : a.wq + n * (a.K / 2) + (lane >> 4) * 16;
+    scale = n * a.groups;
+  }
+};
+
+// Scales of 16 channels, four half tiles or tiles to a load: lane (r, i) holds that
+// of the i-th from `first` on (in halves or tiles of K, not past `end`), and
+// element i of channel r is that lane's.
+template <int GROUPS>
+__device__ __forceinline__ uint32_t load_scales(const W4a16Args& a, int64_t channel, int first, int end, int i) {
+  int at = first + i;
+  at = at < end ? at : end - 1;
+  const int64_t s = channel + a.group_halves.quotient(GROUPS == HALVES ? at : 2 * at);
+  return a.sw_f16 ? static_cast<const uint16_t*>(a.sw)[s] : static_cast<const uint32_t*>(a.sw)[s];
+}
+__device__ __forceinline__ float scale_of(const W4a16Args& a, uint32_t s) {
+  return a.sw_f16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(s))) : float_of(s);
+}
+__device__ __forceinline__ float spread_scale(float s, int i, int r) { return __shfl(s, 16 * i + r); }
+
+// x's operands for the word j of a tile's codes.
+// `past` lanes hold what lies behind K: zeros.
+// (Here, where the values are used: a change right behind the load would wait for
+// it, and with it for every other load on its way.)
+template <bool XF16>
+__device__ __forceinline__ void widen_x(u4* v, bool last, bool past, Operand* o) {
+  if (last) {
+#pragma unroll
+    for (int i = 0; i < (XF16 ? 1 : 2); ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = past ? 0u : v[i][e];
+  }
+  if constexpr (XF16)
+    o[0] = order_04152637(v[0]);
+  else
+    split_bf16(reinterpret_cast<const float*>(v), o);
+}
+template <bool XF16>
+__device__ __forceinline__ Operand widen_codes(uint32_t w, const Masks& m) {
+  return XF16 ? int4_to_f16(w, m) : int4_to_bf16_over16(w);
+}
+template <bool XF16>
+__device__ __forceinline__ f4 multiply(const Operand& x, const Operand& q, f4 d) {
+  if constexpr (XF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x.h, q.h, d, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.b, q.b, d, 0, 0, 0);
+}
+// The operand with the other half of the tile's K zero: lanes of g / 2 == h stay.
+__device__ __forceinline__ Operand half_of(const Operand& x, bool keep) {
+  Operand o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o.w[e] = keep ? x.w[e] : 0u;
+  return o;
+}
+
+__device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part, int64_t row, int64_t col, float y) {
+  if (parts > 1)
+    a.partial[(part * a.M + row) * a.N + col] = y;
+  else if (a.y_f16)
+    static_cast<_Float16*>(a.y)[row * a.ldy + col] = static_cast<_Float16>(y);
+  else
+    static_cast<float*>(a.y)[row * a.ldy + col] = y;
+}
+
+// Up to 16 rows: a workgroup takes 16 NB channels, its waves runs of their tiles,
+// and adds the waves' sums up through LDS, in their order.  Each wave brings x
+// from the caches itself (rows past M repeat the last one and are not stored).
+template <bool XF16, int NB, int GROUPS>
+__global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
+  constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
+  constexpr int XV = XF16 ? 1 : 2;                   // 16 bytes of x to eight elements
+  constexpr int U = NB == 1 && XF16 ? 4 : 2;         // tiles of each block of channels on their way together
+  constexpr int SL = GROUPS == WHOLE ? 1 : U * HALF / 4 < 1 ? 1 : U * HALF / 4;  // loads of their scales
+  __shared__ f4 lds[kWaves][NB][64];
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * NB;
+  const int share = (ntiles + kWaves - 1) / kWaves;
+  const int t0 = wave * share, t1 = t0 + share < ntiles ? t0 + share : ntiles;
+  const int64_t wstep = a.tiled ? 1024 : 64;
+  const bool half_tile = (a.K & 127) != 0;  // the last tile's upper half is past K (row-major only)
+  const int64_t m = r < a.M ? r : a.M - 1;
+  const char* x = static_cast<const char*>(a.x) + (m * a.ldx + 32 * g) * (XF16 ? 2 : 4);
+  f4 acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = f4{0.f, 0.f, 0.f, 0.f};
+  Channels ch[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) ch[b].set(a, block0 + b, lane);
+  const Masks masks;
+
+  for (int t = t0; t < t1; t += U) {
+    u4 c[U][NB], xr[U][4][XV];
+    uint32_t sr[NB][SL];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int tt = t + u < t1 ? t + u : t1 - 1;
+      const bool past = half_tile && tt == ntiles - 1 && g >= 2;  // this lane's codes are past K
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        c[u][b] = *reinterpret_cast<const u4*>(ch[b].p + tt * wstep - (past ? 32 : 0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < XV; ++e) {
+          const char* p = x + tt * (256 * XV) + j * (16 * XV) - (past ? 128 * XV : 0);
+          xr[u][j][e] = reinterpret_cast<const u4*>(p)[e];
+          }
+    }
+    if constexpr (GROUPS != WHOLE) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int l = 0; l < SL; ++l) sr[b][l] = load_scales<GROUPS>(a, ch[b].scale, t * HALF + 4 * l, t1 * HALF, g);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t + u >= t1) break;
+      f4 sum[NB][HALF];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < HALF; ++h) sum[b][h] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // eight codes of every lane at a time
+        Operand xo[PARTS];
+        widen_x<XF16>(xr[u][j], half_tile && t + u == ntiles - 1, g >= 2, xo);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const Operand q = widen_codes<XF16>(c[u][b][j], masks);
+#pragma unroll
+          for (int h = 0; h < HALF; ++h)
+#pragma unroll
+            for (int i = PARTS - 1; i >= 0; --i) {  // the small parts first
+              f4& d = GROUPS == WHOLE ? acc[b] : sum[b][h];
+              d = multiply<XF16>(HALF == 1 ? xo[i] : half_of(xo[i], (g >= 2) == (h == 1)), q, d);
+            }
+        }
+      }
+      if constexpr (GROUPS != WHOLE) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int h = 0; h < HALF; ++h) {
+            const int i = u * HALF + h;
+            const float s = spread_scale(scale_of(a, sr[b][i / 4]), i % 4, r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[b][e] = fmaf(s, sum[b][h][e], acc[b][e]);
+          }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int b = 0; b < NB; ++b) lds[wave][b][lane] = acc[b];
+  __syncthreads();
+  for (int b = wave; b < NB; b += kWaves) {
+    f4 v = lds[0][b][lane];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) v += lds[k][b][lane];
+    const int64_t col = (block0 + b) * 16 + r;
+    if (col >= a.N) continue;
+    float f = XF16 ? 1.f : 16.f;
+    if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, col, a.sw_f16);
+    asm volatile("" : "+v"(f));  // waits for it here, once, and not in each branch of a store
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * g + e < a.M) store_y(a, 1, 0, 4 * g + e, col, v[e] * f);
+  }
+}
+
+// More rows: a wave takes 16 NB channels, a workgroup those of its waves, 16 MT
+// rows and a part of K.  x goes through LDS as operands, a tile ahead, each
+// thread bringing its share; the waves' codes come from memory to registers a
+// tile ahead too.
 template <bool XF16, int NB, int MT, int GROUPS>
-__global__ void __launch_bounds__(kWaves * 64) w4a16_kernel(W4a16Args a, int parts, int ntiles) {
-  constexpr int PARTS = XF16 ? 1 : 3;
-  __shared__ f4 lds[kWaves][NB * MT][64];
+__global__ void __launch_bounds__(kManyWaves * 64, 2) w4a16_many_kernel(W4a16Args a, int parts, int ntiles) {
+  constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
+  constexpr int BUFFERS = XF16 ? 2 : 1;
+  // A thread brings the operands (i, j) of MT * 4, lane its own, of its wave.
+  constexpr int OWN = MT * 4 / kManyWaves;
+  __shared__ u4 lds[BUFFERS][PARTS][MT * 4][64];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = blockIdx.x % parts;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x / parts) * (16 * NB);
+  const int64_t block0 = (static_cast<int64_t>(blockIdx.x / parts) * kManyWaves + wave) * NB;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT);
   const int t0 = static_cast<int>(static_cast<int64_t>(ntiles) * part / parts);
   const int t1 = static_cast<int>(static_cast<int64_t>(ntiles) * (part + 1) / parts);
-  const int ngroups = a.K / a.group;
-  const bool half_tile = (a.K & 127) != 0;  // the last tile's upper half is past K (row-major only)
-
-  const uint8_t* w[NB];
-  int64_t n[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    n[b] = n0 + 16 * b + r;
-    n[b] = n[b] < a.N ? n[b] : a.N - 1;
-    // Tiled: a block past the last one repeats it.
-    const int64_t blk = n0 / 16 + b < (a.N + 15) / 16 ? n0 / 16 + b : (a.N - 1) / 16;
-    w[b] = a.tiled ? a.wq + blk * (8 * static_cast<int64_t>(a.K)) + lane * 16
-                   : a.wq + n[b] * (a.K / 2) + g * 16;
-  }
   const int64_t wstep = a.tiled ? 1024 : 64;
-  const char* x[MT];
+  const bool half_tile = (a.K & 127) != 0;
+  Channels ch[NB];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    int64_t m = m0 + 16 * i + r;
+  for (int b = 0; b < NB; ++b) ch[b].set(a, block0 + b, lane);
+  const char* x[OWN];
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) {
+    const int o = wave * OWN + i;  // operand o: row block o / 4, word o % 4
+    int64_t m = m0 + 16 * (o / 4) + r;
     m = m < a.M ? m : a.M - 1;
-    x[i] = static_cast<const char*>(a.x) + (m * a.ldx + 32 * g) * (XF16 ? 2 : 4);
+    x[i] = static_cast<const char*>(a.x) + (m * a.ldx + 32 * g + 8 * (o % 4)) * (XF16 ? 2 : 4);
   }
-
+  const Masks masks;
   f4 acc[NB][MT];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[b][i] = f4{0.f, 0.f, 0.f, 0.f};
 
-  for (int t = t0 + wave; t < t1; t += kWaves) {
-    const bool past = half_tile && t == ntiles - 1 && g >= 2;  // this lane's codes are past K
-    u4 c[NB];
+  u4 c[NB];
+  uint32_t s[NB];
+  u4 raw[OWN][XF16 ? 1 : 2];
+  auto bring = [&](int t) {
+    const bool past = half_tile && t == ntiles - 1 && g >= 2;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+#pragma unroll
+      for (int e = 0; e < (XF16 ? 1 : 2); ++e) {
+        raw[i][e] = reinterpret_cast<const u4*>(x[i] + t * (XF16 ? 256 : 512) - (past ? (XF16 ? 128 : 256) : 0))[e];
+      }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint8_t* p = w[b] + t * wstep - (past ? 32 : 0);
-      c[b] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(p));
+      c[b] = *reinterpret_cast<const u4*>(ch[b].p + t * wstep - (past ? 32 : 0));
+      if constexpr (GROUPS != WHOLE) s[b] = load_scales<GROUPS>(a, ch[b].scale, t * HALF, ntiles * HALF, g);
     }
-    float s[NB][GROUPS == HALVES ? 2 : 1];
-    if constexpr (GROUPS != WHOLE) {
+  };
+  auto put = [&](int t, int buffer) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        s[b][0] = load_scale(a.sw, n[b] * ngroups + t * 128 / a.group, a.sw_f16);
-        if constexpr (GROUPS == HALVES) {
-          const int up = t * 128 + 64 < a.K ? (t * 128 + 64) / a.group : ngroups - 1;
-          s[b][1] = load_scale(a.sw, n[b] * ngroups + up, a.sw_f16);
-        }
-      }
+    for (int i = 0; i < OWN; ++i) {
+      Operand o[PARTS];
+      widen_x<XF16>(raw[i], half_tile && t == ntiles - 1, g >= 2, o);
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        lds[buffer][p][wave * OWN + i][lane] = u4{o[p].w[0], o[p].w[1], o[p].w[2], o[p].w[3]};
     }
-    f4 sum[NB][MT][GROUPS == HALVES ? 2 : 1];
-    if constexpr (GROUPS != WHOLE) {
+  };
+  if (t0 < t1) bring(t0);
+  for (int t = t0; t < t1; ++t) {
+    const int buffer = BUFFERS == 2 ? (t - t0) & 1 : 0;
+    if (BUFFERS == 1 && t > t0) __syncthreads();  // the tile before is used up
+    put(t, buffer);
+    u4 now[NB];
+    uint32_t sn[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int h = 0; h < (GROUPS == HALVES ? 2 : 1); ++h) sum[b][i][h] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < NB; ++b) {
+      now[b] = c[b];
+      if constexpr (GROUPS != WHOLE) sn[b] = s[b];
     }
+    bring(t + 1 < t1 ? t + 1 : t);
+    __syncthreads();
+    f4 sum[NB][MT][HALF];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // eight codes of every lane at a time
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < HALF; ++h) sum[b][i][h] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       Operand q[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) q[b] = XF16 ? int4_to_f16(c[b][j]) : int4_to_bf16_over16(c[b][j]);
+      for (int b = 0; b < NB; ++b) q[b] = widen_codes<XF16>(now[b][j], masks);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        Operand xo[PARTS];
-        if constexpr (XF16) {
-          u4 v = *reinterpret_cast<const u4*>(x[i] + t * 256 + 16 * j - (past ? 128 : 0));
-          if (past) v = u4{0, 0, 0, 0};
-          xo[0] = order_04152637(v);
-        } else {
-          union {
-            f4 v[2];
-            float f[8];
-          } u;
-          const f4* p = reinterpret_cast<const f4*>(x[i] + t * 512 + 32 * j - (past ? 256 : 0));
-          u.v[0] = p[0];
-          u.v[1] = p[1];
-          if (past) u.v[0] = u.v[1] = f4{0.f, 0.f, 0.f, 0.f};
-          split_bf16(u.f, xo);
-        }
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int h = 0; h < (GROUPS == HALVES ? 2 : 1); ++h) {
+        for (int p = PARTS - 1; p >= 0; --p) {
+          Operand xo;
+          const u4 v = lds[buffer][p][4 * i + j][lane];
 #pragma unroll
-          for (int p = PARTS - 1; p >= 0; --p) {  // the small parts first
-            Operand xh = xo[p];
-            if constexpr (GROUPS == HALVES) {
+          for (int e = 0; e < 4; ++e) xo.w[e] = v[e];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) xh.w[e] = (g >= 2) == (h == 1) ? xh.w[e] : 0u;
-            }
+          for (int h = 0; h < HALF; ++h) {
+            const Operand xh = HALF == 1 ? xo : half_of(xo, (g >= 2) == (h == 1));
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               f4& d = GROUPS == WHOLE ? acc[b][i] : sum[b][i][h];
-              if constexpr (XF16)
-                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh.h, q[b].h, d, 0, 0, 0);
-              else
-                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xh.b, q[b].b, d, 0, 0, 0);
+              d = multiply<XF16>(xh, q[b], d);
             }
           }
         }
-      }
     }
     if constexpr (GROUPS != WHOLE) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int h = 0; h < HALF; ++h) {
+          const float f = spread_scale(scale_of(a, sn[b]), h, r);
 #pragma unroll
-          for (int h = 0; h < (GROUPS == HALVES ? 2 : 1); ++h)
+          for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[b][i][e] = fmaf(s[b][h], sum[b][i][h][e], acc[b][i][e]);
+            for (int e = 0; e < 4; ++e) acc[b][i][e] = fmaf(f, sum[b][i][h][e], acc[b][i][e]);
+        }
     }
   }
 
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) lds[wave][b * MT + i][lane] = acc[b][i];
-  __syncthreads();
-  for (int o = wave; o < NB * MT; o += kWaves) {
-    f4 v = lds[0][o][lane];
-#pragma unroll
-    for (int k = 1; k < kWaves; ++k) v += lds[k][o][lane];
-    const int64_t col = n0 + 16 * (o / MT) + r;
-    const int64_t row = m0 + 16 * (o % MT) + 4 * g;
+  for (int b = 0; b < NB; ++b) {
+    const int64_t col = (block0 + b) * 16 + r;
     if (col >= a.N) continue;
     float f = XF16 ? 1.f : 16.f;
     if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, col, a.sw_f16);
+    asm volatile("" : "+v"(f));  // waits for it here, once, and not in each branch of a store
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (row + e >= a.M) break;
-      const float y = v[e] * f;
-      if (parts > 1)
-        a.partial[(part * a.M + row + e) * a.N + col] = y;
-      else if (a.y_f16)
-        static_cast<_Float16*>(a.y)[(row + e) * a.ldy + col] = static_cast<_Float16>(y);
-      else
-        static_cast<float*>(a.y)[(row + e) * a.ldy + col] = y;
-    }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t row = m0 + 16 * i + 4 * g + e;
+        if (row < a.M) store_y(a, parts, part, row, col, acc[b][i][e] * f);
+      }
   }
 }
 
@@ -185,39 +354,76 @@ __global__ void __launch_bounds__(256) w4a16_join_kernel(W4a16Args a, int parts)
   const int64_t row = blockIdx.y;
   if (col >= a.N) return;
   float v = 0.f;
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) v += a.partial[(p * a.M + row) * a.N + col];
-  if (a.y_f16)
-    static_cast<_Float16*>(a.y)[row * a.ldy + col] = static_cast<_Float16>(v);
-  else
-    static_cast<float*>(a.y)[row * a.ldy + col] = v;
+  store_y(a, 1, 0, row, col, v);
+}
+
+template <bool XF16, int NB, int MT, int GROUPS>
+void launch_kernel(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
+  const int ntiles = (a.K + 127) / 128;
+  const int64_t blocks = (a.N + 15) / 16;
+  if constexpr (MT == 1) {
+    hipLaunchKernelGGL((w4a16_few_kernel<XF16, NB, GROUPS>), dim3(static_cast<unsigned>((blocks + NB - 1) / NB)),
+                       dim3(kWaves * 64), 0, st, a, ntiles);
+  } else {
+    constexpr int kBlocks = NB * kManyWaves;
+    const dim3 grid(static_cast<unsigned>((blocks + kBlocks - 1) / kBlocks * p.parts),
+                    static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((w4a16_many_kernel<XF16, NB, MT, GROUPS>), grid, dim3(kManyWaves * 64), 0, st, a, p.parts, ntiles);
+  }
 }
 
 template <bool XF16, int NB, int MT>
 void launch_groups(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
-  const int ntiles = (a.K + 127) / 128;
-  const dim3 grid(static_cast<unsigned>((a.N + 16 * NB - 1) / (16 * NB) * p.parts),
-                  static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
-  const dim3 block(kWaves * 64);
-  if (a.group == a.K)
-    hipLaunchKernelGGL((w4a16_kernel<XF16, NB, MT, WHOLE>), grid, block, 0, st, a, p.parts, ntiles);
-  else if (a.group % 128 == 0)
-    hipLaunchKernelGGL((w4a16_kernel<XF16, NB, MT, TILES>), grid, block, 0, st, a, p.parts, ntiles);
+  if (a.groups == 1)
+    launch_kernel<XF16, NB, MT, WHOLE>(a, p, st);
+  else if (a.group_halves.d % 2 == 0)
+    launch_kernel<XF16, NB, MT, TILES>(a, p, st);
   else
-    hipLaunchKernelGGL((w4a16_kernel<XF16, NB, MT, HALVES>), grid, block, 0, st, a, p.parts, ntiles);
+    launch_kernel<XF16, NB, MT, HALVES>(a, p, st);
 }
 
 template <bool XF16>
 void launch_x(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
-  if (p.mt == 1)
-    launch_groups<XF16, 1, 1>(a, p, st);
-  else
-    launch_groups<XF16, 1, 4>(a, p, st);
+  if (p.mt == 1) {
+    if (p.nb == 1)
+      launch_groups<XF16, 1, 1>(a, p, st);
+    else if (p.nb == 2)
+      launch_groups<XF16, 2, 1>(a, p, st);
+    else
+      launch_groups<XF16, 4, 1>(a, p, st);
+  } else if (p.mt == 2) {
+    launch_groups<XF16, 2, 2>(a, p, st);
+  } else {
+    launch_groups<XF16, 2, 4>(a, p, st);
+  }
 }
 
 }  // namespace
 
+// Up to 16 rows: a workgroup with more channels reads x less often, one with fewer
+// leaves more workgroups to fill the chip.  Measured, 16 / 32 / 64 channels: at
+// 1792 blocks of 16 channels (8 x 4096 -> 28672) 25.6 / 19.4 / 18.2 us; at 384
+// (1 x 4096 -> 6144) 6.4 / 6.5 / 8.3 and at 313 (5 float32 x 1088 -> 5007) 6.8 /
+// 6.2 / 8.0 us.
+// More rows: parts of K until 512 workgroups share the work, each at least four
+// tiles.  At 64 x 14336 -> 4096 it takes 24.2 us with 256 workgroups, 22.6 with
+// 512, 27.9 with 1024 (the parts' sums are written and read again).
 W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
-  W4a16Plan p{1, M <= 16 ? 1 : 4, kWaves, 1};
+  const int64_t blocks = (N + 15) / 16, tiles = (K + 127) / 128;
+  W4a16Plan p{1, 1, 1};
+  if (M <= 16) {
+    p.nb = blocks >= 1024 ? 4 : blocks >= 256 ? 2 : 1;
+    return p;
+  }
+  p.nb = 2;
+  p.mt = M <= 32 ? 2 : 4;
+  const int64_t groups = (blocks + 2 * kManyWaves - 1) / (2 * kManyWaves) * ((M + 16 * p.mt - 1) / (16 * p.mt));
+  int64_t parts = (512 + groups - 1) / groups;
+  const int64_t most = tiles / 4;
+  parts = parts < most ? parts : most;
+  p.parts = static_cast<int>(parts < 1 ? 1 : parts);
   return p;
 }
 
