@@ -825,6 +825,7 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
     if (brings_keys) {
       load_keys<D, BITS>(a, rb, r, g, codes);
       scale = a.ks[token];
+      asm volatile("");  // keeps the two branches' stores apart: merged, they would put codes in memory
     } else {
       load_values<D, BITS>(a, rb, r, g, codes);
       scale = a.vs[token];
