@@ -35,9 +35,15 @@ AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capac
   }
   const int64_t groups = (rows + kGroupRows - 1) / kGroupRows;
   c.groups = Divisor(static_cast<uint32_t>(groups));
+  // Rows' workgroups cost their queries' operands and a partial result each, so
+  // parts are long (1024 tokens; 3 prompts of 1021 queries: 98 us, with 512 113,
+  // with 2048 101), unless without parts of 256 the chip would be half empty.
+  // One workgroup on each unit is enough then: a second round of them, or own
+  // tokens that wait behind, cost more (64 sequences on a prefix of 8192: 38 us
+  // with 256 workgroups, 45 with 512, 50 with 1024).
   const int64_t units = seqs * heads * groups;
   c.piece_log2 = units < resident ? 8 : 10;
-  int64_t parts = units < resident ? (512 + units - 1) / units : 8;
+  int64_t parts = units < resident ? (256 + units - 1) / units : 8;
   const int64_t most = capacity >> c.piece_log2;
   parts = parts < most ? parts : most;
   c.parts = Divisor(static_cast<uint32_t>(parts < 1 ? 1 : parts));

@@ -122,29 +122,35 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* d) {
     }
   }
 }
+// Of one half, whose first token is cache row rb.
+template <int D, int BITS>
+__device__ __forceinline__ void load_half_keys(const AttentionArgs& a, int64_t rb, uint32_t r, uint32_t g, uint32_t* k) {
+  using X = Row<D, BITS>;
+  load_words<X::kKeyWords>(a.k + rb * X::kBytes + (r * X::kBytes + g * (X::kBytes / 4)), k);
+}
+template <int D, int BITS>
+__device__ __forceinline__ void load_half_values(const AttentionArgs& a, int64_t rb, uint32_t r, uint32_t g, uint32_t* v) {
+  using X = Row<D, BITS>;
+  const uint8_t* first = a.v + rb * X::kBytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* p = first + (g * (4 * X::kBytes) + r * (X::kBytes / 16)) + i * X::kBytes;
+    if constexpr (X::kBytes == 32)
+      v[i] = *reinterpret_cast<const uint16_t*>(p);
+    else
+      load_words<X::kValueWords>(p, v + i * X::kValueWords);
+  }
+}
 // rb: the cache rows of the halves' first tokens.
 template <int D, int BITS>
 __device__ __forceinline__ void load_keys(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* k) {
-  using X = Row<D, BITS>;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    load_words<X::kKeyWords>(a.k + rb[h] * X::kBytes + (r * X::kBytes + g * (X::kBytes / 4)), k + h * X::kKeyWords);
+  for (int h = 0; h < 2; ++h) load_half_keys<D, BITS>(a, rb[h], r, g, k + h * Row<D, BITS>::kKeyWords);
 }
 template <int D, int BITS>
 __device__ __forceinline__ void load_values(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* v) {
-  using X = Row<D, BITS>;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint8_t* first = a.v + rb[h] * X::kBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = first + (g * (4 * X::kBytes) + r * (X::kBytes / 16)) + i * X::kBytes;
-      if constexpr (X::kBytes == 32)
-        v[4 * h + i] = *reinterpret_cast<const uint16_t*>(p);
-      else
-        load_words<X::kValueWords>(p, v + (4 * h + i) * X::kValueWords);
-    }
-  }
+  for (int h = 0; h < 2; ++h) load_half_values<D, BITS>(a, rb[h], r, g, v + h * 4 * Row<D, BITS>::kValueWords);
 }
 // The scales of tokens 4 g + i of both halves.
 __device__ __forceinline__ void load_scales(const float* s, const int64_t* rb, uint32_t g, f4* d) {
@@ -186,14 +192,14 @@ __device__ constexpr int key_factor(int e) {
   return BITS == 4 && (e & 2) ? 4 : 0;
 }
 
-// Four channels of the eight tokens of a lane, as fp16: channels 4 q to 4 q + 3
-// of the lane's own.  (An offset of the values cannot wait like the keys': it
+// Four channels of a lane's tokens in pairs (four of a step, two of a half), as
+// fp16: channels 4 q to 4 q + 3 of the lane's own.  (An offset of the values cannot wait like the keys': it
 // would be 8 times the sum of the weights, which the result is a small part of.)
-template <int D, int BITS>
+template <int D, int BITS, int PAIRS = 4>
 __device__ __forceinline__ void value_operands(const uint32_t* v, int q, const Masks& m, Operand* o) {
   constexpr int VW = Row<D, BITS>::kValueWords;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
+  for (int p = 0; p < PAIRS; ++p) {
     const int word = BITS == 4 ? q / 2 : q;
     uint32_t w0 = v[2 * p * VW + word], w1 = v[(2 * p + 1) * VW + word];
     if constexpr (BITS == 4) {
@@ -328,14 +334,15 @@ struct Pages {
     return p >= 0 && p < a.pages ? p : -1;
   }
 };
+// The cache row of a half step's first token, in page p.
+__device__ __forceinline__ int64_t half_row(const AttentionArgs& a, int h, int step, int half, int32_t p) {
+  const int off = (step * kStep + 16 * half) & ((1 << a.page_log2) - 1);
+  return ((static_cast<int64_t>(p < 0 ? 0 : p) * a.heads + h) << a.page_log2) + off;
+}
 // The cache rows of the halves of a step in pages p0 and p1.
 __device__ __forceinline__ void rows_of(const AttentionArgs& a, int h, int step, int32_t p0, int32_t p1, int64_t* rb) {
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int off = (step * kStep + 16 * half) & ((1 << a.page_log2) - 1);
-    const int32_t p = half ? p1 : p0;
-    rb[half] = ((static_cast<int64_t>(p < 0 ? 0 : p) * a.heads + h) << a.page_log2) + off;
-  }
+  rb[0] = half_row(a, h, step, 0, p0);
+  rb[1] = half_row(a, h, step, 1, p1);
 }
 
 // A lane's channels [g D / 4, +D / 4) of a row of queries.
@@ -750,8 +757,9 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
 }
 
 // Many rows: a wave's 16 rows are its own, and the waves share the widening.
-// Two steps at a time go through LDS as operands, each wave bringing the keys
-// or the values of one of them, and all waves multiply both.
+// Two steps at a time (a block) go through LDS as operands, each wave bringing
+// the keys and values of half a step, and all waves multiply all.  The codes of
+// two more blocks are on their way meanwhile.
 template <int D>
 struct RowsLds {
   static constexpr int kBlock = 2;
@@ -813,26 +821,30 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
   Raw8<Q> x[NK];
   load_query<D>(a, span, h, row, g, x);
 
-  const bool brings_keys = wave < 2;
-  const int mine = wave & 1;  // the step of a block that this wave brings
-  uint32_t codes[Row<D, BITS>::kWords];
-  float scale = 0.f;  // of token lane, of the first 32 lanes
-  auto bring = [&](int step, int32_t from, int turn) {
-    if (step >= end) return;
-    int64_t rb[2];
-    rows_of(a, h, step, __builtin_amdgcn_readlane(from, 2 * turn), __builtin_amdgcn_readlane(from, 2 * turn + 1), rb);
-    const int64_t token = (lane & 16 ? rb[1] : rb[0]) + r;
-    if (brings_keys) {
-      load_keys<D, BITS>(a, rb, r, g, codes);
-      scale = a.ks[token];
-      asm volatile("");  // keeps the two branches' stores apart: merged, they would put codes in memory
-    } else {
-      load_values<D, BITS>(a, rb, r, g, codes);
-      scale = a.vs[token];
-    }
+  // This wave brings half `half` of step `mine` of each block; DEPTH blocks at a
+  // time are on their way (one where two would not fit the registers).  Without
+  // conditions: a wait for one set's loads must not become one for all.
+  constexpr int DEPTH = BITS == 8 && (PAIR || D == 256) ? 1 : 2;
+  const int mine = wave & 1, half = wave >> 1;
+  constexpr int KW = Row<D, BITS>::kKeyWords, VW = 4 * Row<D, BITS>::kValueWords;
+  uint32_t keys[DEPTH][KW], values[DEPTH][VW];
+  float scale[DEPTH];  // of token lane % 16: lanes 0 to 15 the keys', 16 to 31 the values'
+  const float* const scales = lane & 16 ? a.vs : a.ks;
+  auto bring = [&](int set, int step, int32_t from, int turn) {
+    const int64_t rb = half_row(a, h, step, half, __builtin_amdgcn_readlane(from, 2 * turn + half));
+    load_half_keys<D, BITS>(a, rb, r, g, keys[set]);
+    load_half_values<D, BITS>(a, rb, r, g, values[set]);
+    scale[set] = scales[rb + r];
   };
+  const int last_step = end - 1;
   pages = Pages::checked(a, pages);
-  bring(begin + mine, pages, mine);
+  if (begin < end) {
+#pragma unroll
+    for (int set = 0; set < DEPTH; ++set) {
+      const int step = begin + set * BLOCK + mine < last_step ? begin + set * BLOCK + mine : last_step;
+      bring(set, step, pages, step - begin);
+    }
+  }
 
   Operand q[NK][HALVES];
   const int up = query_shift<D>(x);
@@ -852,37 +864,29 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
   state.clear();
   const Masks masks;
 
-  for (int block = begin; block < end; block += BLOCK) {
+  auto take = [&](int block, int set) {
     const int turn = (block - begin) & 31;
     if (turn == 0 && block > begin) pages = ahead;
     __syncthreads();  // the block before is used up
-    if (block + mine < end) {
-      if (brings_keys) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+    for (int j = 0; j < NK; ++j)
+      lds.k[mine][half][j][lane] = __builtin_bit_cast(u4, key_operand<BITS>(keys[set], j, masks));
 #pragma unroll
-          for (int j = 0; j < NK; ++j)
-            lds.k[mine][half][j][lane] =
-                __builtin_bit_cast(u4, key_operand<BITS>(codes + half * Row<D, BITS>::kKeyWords, j, masks));
-      } else {
+    for (int j = 0; j < NV / 4; ++j) {
+      Operand v[4];
+      value_operands<D, BITS, 2>(values[set], j, masks, v);
 #pragma unroll
-        for (int j = 0; j < NV / 4; ++j) {
-          Operand v[4];
-          value_operands<D, BITS>(codes, j, masks, v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) lds.v[mine][4 * j + e][lane] = __builtin_bit_cast(u4, v[e].h);
-        }
-      }
-      if (lane < 32) reinterpret_cast<float*>(brings_keys ? lds.ks[mine] : lds.vs[mine])[lane] = scale;
+      for (int e = 0; e < 4; ++e)
+        reinterpret_cast<uint2*>(&lds.v[mine][4 * j + e][lane])[half] = uint2{v[e].w[0], v[e].w[1]};
     }
-    if (((block + BLOCK - begin) & 31) == 0 && block + BLOCK < end) {
-      ahead = Pages::checked(a, table.raw(a, block + BLOCK, 1, lane));
-      bring(block + BLOCK + mine, ahead, mine);
-    } else {
-      bring(block + BLOCK + mine, pages, (turn + BLOCK + mine) & 31);
-    }
+    if (lane < 32) reinterpret_cast<float*>(lane & 16 ? lds.vs[mine] : lds.ks[mine])[16 * half + r] = scale[set];
+    const int next = block + DEPTH * BLOCK - begin;  // to be brought, from begin
+    if ((next & 31) == 0 && next + begin < end) ahead = Pages::checked(a, table.raw(a, next + begin, 1, lane));
+    const int step = next + begin + mine < last_step ? next + begin + mine : last_step;
+    bring(set, step, (step - begin) >> 5 == (block - begin) >> 5 ? pages : ahead, (step - begin) & 31);
     __syncthreads();
 
+#pragma unroll
     for (int b = 0; b < BLOCK; ++b) {
       const int step = block + b;
       if (step >= end || step >= wave_steps) break;
@@ -908,13 +912,22 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
       Operand w[2];
       weigh_step<NV>(sc, kc, vs, partly, limit, step * kStep + 4 * g, bad0, bad1, state, w);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const h8 v = __builtin_bit_cast(h8, lds.v[b][j][lane]);
+      for (int j0 = 0; j0 < NV; j0 += 4) {
+        h8 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(h8, lds.v[b][j0 + j][lane]);
 #pragma unroll
         for (int p = 1; p >= 0; --p)
-          state.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[p].h, state.o[j], 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            state.o[j0 + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[j], w[p].h, state.o[j0 + j], 0, 0, 0);
       }
     }
+  };
+  for (int block = begin; block < end; block += DEPTH * BLOCK) {
+    take(block, 0);
+    if (DEPTH == 1 || block + BLOCK >= end) continue;
+    take(block + BLOCK, DEPTH - 1);
   }
 
   state.l += __shfl_xor(state.l, 16);
@@ -952,8 +965,11 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
     }
   }
 }
+// Workgroups to a compute unit; the widest variant would keep registers in memory
+// with two.
+constexpr int rows_resident(int D, int bits, bool pair) { return D < 256 ? 3 : pair && bits == 8 ? 1 : 2; }
 template <int D, int BITS, bool PAIR>
-__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
+__global__ void __launch_bounds__(kAttnWaves * 64, rows_resident(D, BITS, PAIR))
     attention_rows_kernel(AttentionArgs a, AttentionPlan plan, int front) {
   __shared__ RowsLds<D> lds;
   rows_body<D, BITS, PAIR>(a, plan, front, blockIdx.x, lds);
@@ -962,7 +978,7 @@ __global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
 // A prefix with many rows and own tokens with few, as in decoding: both in one
 // launch, the prefix's workgroups first.
 template <int D, int BITS, bool PAIR>
-__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
+__global__ void __launch_bounds__(kAttnWaves * 64, rows_resident(D, BITS, PAIR))
     attention_both_kernel(AttentionArgs a, AttentionPlan plan, uint32_t front_blocks) {
   __shared__ union Lds {
     RowsLds<D> rows;

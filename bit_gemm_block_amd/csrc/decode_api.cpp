@@ -118,6 +118,7 @@ int w4a16_qlinear_forward(const void* x, int x_dtype, int64_t ldx, const uint8_t
   a.groups = static_cast<int>(w_group ? K / w_group : 1);
   a.group_halves = w4a4::Divisor(static_cast<uint32_t>((w_group ? w_group : K) / 64));
   a.y = y; a.y_f16 = y_dtype == W4A4_F16; a.ldy = ldy;
+  a.y_wide = aligned(y, 16) && ldy % 4 == 0;
   a.partial = need > 0 ? static_cast<float*>(workspace) : nullptr;
   return status(w4a4::launch_w4a16(a, x_dtype == W4A4_F16, static_cast<hipStream_t>(stream)));
 }

@@ -34,6 +34,7 @@ struct W4a16Args {
   Divisor group_halves;  // 64s of K to a group
   void* y;       // [M, N], row distance ldy
   int y_f16;
+  int y_wide;    // rows of y allow stores of four elements
   int64_t ldy;
   float* partial;  // workspace: [parts][M][N], or null
 };

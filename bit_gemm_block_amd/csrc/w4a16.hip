@@ -9,10 +9,17 @@
 // matrix instruction.  The order of K inside an instruction is free, so x is
 // brought to the codes' order.
 //
-// fp16 x meets fp16 codes.  float32 x enters as three bfloat16 parts.  Products
-// are exact in both, sums float32.  A tile whose halves have different scales
-// (groups of an odd multiple of 64) is multiplied once per half, with the
-// other half of x zero.
+// fp16 x meets fp16 codes.  float32 x enters as three bfloat16 parts, which hold
+// all its 24 bits.  Products are exact in both, sums float32; only the result is
+// rounded to fewer bits, where fp16 is asked for.  A tile whose halves have
+// different scales (groups of an odd multiple of 64) is multiplied once per half,
+// with the other half of x zero.
+//
+// What bounds it: the codes' bytes, at 5.2 TB/s of a large copy.  8 x 4096 ->
+// 28672 (61 MB) takes 17.5 us, 3.4 TB/s, against 11.7; one token 4096 -> 6144 (13
+// MB, 2.5 us) 6.2, which is the launch and one way to memory and back; 64 x 14336
+// -> 4096 (31.7 MB, 6.1 us) 20.1: 16 in the product, whose tiles of x, 16 KB
+// beside 8 KB of codes, each wait for a barrier, and 4 in the parts' sum.
 #include "decode_internal.h"
 #include "gemm_common.h"
 #include "int4_operands.h"
@@ -21,7 +28,8 @@ namespace w4a4 {
 namespace {
 
 constexpr int kWaves = 8;      // of a workgroup, few rows
-constexpr int kManyWaves = 4;  // many rows
+constexpr int kManyWaves = 4;  // many rows: that share a tile of x
+constexpr int kManySides = 2;  // and how many such tiles at a time
 
 enum Groups { WHOLE = 0, TILES = 1, HALVES = 2 };  // scales: one per channel, per tiles, per half tiles
 
@@ -103,6 +111,9 @@ __device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part,
 // Up to 16 rows: a workgroup takes 16 NB channels, its waves runs of their tiles,
 // and adds the waves' sums up through LDS, in their order.  Each wave brings x
 // from the caches itself (rows past M repeat the last one and are not stored).
+// All loads of U tiles are issued before the first is used; a ring of single
+// tiles instead takes 23 us for 17.5 at 8 x 4096 -> 28672, and loads that bypass
+// the caches 23.
 template <bool XF16, int NB, int GROUPS>
 __global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
@@ -208,23 +219,29 @@ __global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, 
 }
 
 // More rows: a wave takes 16 NB channels, a workgroup those of its waves, 16 MT
-// rows and a part of K.  x goes through LDS as operands, a tile ahead, each
-// thread bringing its share; the waves' codes come from memory to registers a
-// tile ahead too.
+// rows and a part of K.  Its two sides of four waves take every second tile each
+// and add up through LDS (parts over workgroups instead would be written and read
+// again).  x goes through LDS as operands, a tile ahead, each thread bringing its
+// share; the waves' codes come from memory to registers a tile ahead too.
 template <bool XF16, int NB, int MT, int GROUPS>
-__global__ void __launch_bounds__(kManyWaves * 64, 2) w4a16_many_kernel(W4a16Args a, int parts, int ntiles) {
+__global__ void __launch_bounds__(kManySides * kManyWaves * 64, 2) w4a16_many_kernel(W4a16Args a, Divisor parts, int share, int longer, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
   constexpr int BUFFERS = XF16 ? 2 : 1;
   // A thread brings the operands (i, j) of MT * 4, lane its own, of its wave.
   constexpr int OWN = MT * 4 / kManyWaves;
-  __shared__ u4 lds[BUFFERS][PARTS][MT * 4][64];
+  constexpr int SIDE = BUFFERS * PARTS * MT * 4 * 64;                // of LDS, in u4
+  constexpr int COLS = 16 * NB * kManyWaves;                         // of the workgroup
+  static_assert(kManySides * 16 * MT * COLS <= kManySides * SIDE * 4, "the sides' sums fit LDS");
+  __shared__ u4 shared[kManySides * SIDE];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = blockIdx.x % parts;
-  const int64_t block0 = (static_cast<int64_t>(blockIdx.x / parts) * kManyWaves + wave) * NB;
+  const int side = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kManyWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kManyWaves;
+  u4(*lds)[PARTS][MT * 4][64] = reinterpret_cast<u4(*)[PARTS][MT * 4][64]>(shared + side * SIDE);
+  const int group = parts.quotient(blockIdx.x), part = blockIdx.x - group * parts.d;
+  const int64_t block0 = (static_cast<int64_t>(group) * kManyWaves + wave) * NB;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT);
-  const int t0 = static_cast<int>(static_cast<int64_t>(ntiles) * part / parts);
-  const int t1 = static_cast<int>(static_cast<int64_t>(ntiles) * (part + 1) / parts);
+  const int t0 = part * share + (part < longer ? part : longer);  // the first parts have a tile more
+  const int t1 = t0 + share + (part < longer ? 1 : 0);
   const int64_t wstep = a.tiled ? 1024 : 64;
   const bool half_tile = (a.K & 127) != 0;
   Channels ch[NB];
@@ -272,10 +289,12 @@ __global__ void __launch_bounds__(kManyWaves * 64, 2) w4a16_many_kernel(W4a16Arg
         lds[buffer][p][wave * OWN + i][lane] = u4{o[p].w[0], o[p].w[1], o[p].w[2], o[p].w[3]};
     }
   };
-  if (t0 < t1) bring(t0);
-  for (int t = t0; t < t1; ++t) {
-    const int buffer = BUFFERS == 2 ? (t - t0) & 1 : 0;
-    if (BUFFERS == 1 && t > t0) __syncthreads();  // the tile before is used up
+  // A side past the last tile goes through the motions with it, for the barriers.
+  bring(t0 + side < t1 ? t0 + side : t0);
+  for (int at = t0; at < t1; at += kManySides) {
+    const int t = at + side < t1 ? at + side : t0;
+    const int buffer = BUFFERS == 2 ? (at - t0) / kManySides & 1 : 0;
+    if (BUFFERS == 1 && at > t0) __syncthreads();  // the tile before is used up
     put(t, buffer);
     u4 now[NB];
     uint32_t sn[NB];
@@ -284,8 +303,9 @@ __global__ void __launch_bounds__(kManyWaves * 64, 2) w4a16_many_kernel(W4a16Arg
       now[b] = c[b];
       if constexpr (GROUPS != WHOLE) sn[b] = s[b];
     }
-    bring(t + 1 < t1 ? t + 1 : t);
+    bring(t + kManySides < t1 ? t + kManySides : t0);
     __syncthreads();
+    if (at + side >= t1) continue;
     f4 sum[NB][MT][HALF];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -331,32 +351,60 @@ __global__ void __launch_bounds__(kManyWaves * 64, 2) w4a16_many_kernel(W4a16Arg
     }
   }
 
+  // The sides' sums as rows of COLS columns, their groups of 16 exchanged by row so
+  // that a wave's writes meet different banks; then whole rows go out.
+  float* const sums = reinterpret_cast<float*>(shared);
+  __syncthreads();
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const int64_t col = (block0 + b) * 16 + r;
-    if (col >= a.N) continue;
     float f = XF16 ? 1.f : 16.f;
-    if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, col, a.sw_f16);
-    asm volatile("" : "+v"(f));  // waits for it here, once, and not in each branch of a store
+    if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, ch[b].n, a.sw_f16);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t row = m0 + 16 * i + 4 * g + e;
-        if (row < a.M) store_y(a, parts, part, row, col, acc[b][i][e] * f);
+        const int row = 16 * i + 4 * g + e, col = (wave * NB + b) * 16 + r;
+        sums[(side * 16 * MT + row) * COLS + (col ^ (16 * g))] = acc[b][i][e] * f;
       }
+  }
+  __syncthreads();
+  const int64_t col0 = static_cast<int64_t>(group) * COLS;
+  const bool wide = a.N % 4 == 0 && (parts.d > 1 || a.y_wide);
+#pragma unroll
+  for (int k = 0; k < 16 * MT * COLS / 4; k += kManySides * kManyWaves * 64) {
+    const int at = k + threadIdx.x, row = at / (COLS / 4), c = at % (COLS / 4) * 4;
+    const int from = row * COLS + (c ^ (16 * (row / 4 % 4)));
+    f4 v = *reinterpret_cast<const f4*>(sums + from);
+#pragma unroll
+    for (int s = 1; s < kManySides; ++s) v += *reinterpret_cast<const f4*>(sums + s * (16 * MT * COLS) + from);
+    const int64_t m = m0 + row, n = col0 + c;
+    if (m >= a.M || n >= a.N) continue;
+    if (wide && (parts.d > 1 || !a.y_f16)) {
+      float* to = parts.d > 1 ? a.partial + (part * a.M + m) * a.N + n : static_cast<float*>(a.y) + m * a.ldy + n;
+      *reinterpret_cast<f4*>(to) = v;
+    } else if (wide) {
+      typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<h4*>(static_cast<_Float16*>(a.y) + m * a.ldy + n) = __builtin_convertvector(v, h4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) store_y(a, parts.d, part, m, n + e, v[e]);
+    }
   }
 }
 
-// The sum over the parts of K, in their order.
+// The sum over the parts of K, in their order; V columns to a thread.
+template <int V>
 __global__ void __launch_bounds__(256) w4a16_join_kernel(W4a16Args a, int parts) {
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  typedef float fv __attribute__((ext_vector_type(V)));
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
   const int64_t row = blockIdx.y;
   if (col >= a.N) return;
-  float v = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) v += a.partial[(p * a.M + row) * a.N + col];
-  store_y(a, 1, 0, row, col, v);
+  fv v = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const fv*>(a.partial + (p * a.M + row) * a.N + col);
+#pragma unroll
+  for (int e = 0; e < V; ++e) store_y(a, 1, 0, row, col + e, v[e]);
 }
 
 template <bool XF16, int NB, int MT, int GROUPS>
@@ -370,7 +418,8 @@ void launch_kernel(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
     constexpr int kBlocks = NB * kManyWaves;
     const dim3 grid(static_cast<unsigned>((blocks + kBlocks - 1) / kBlocks * p.parts),
                     static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL((w4a16_many_kernel<XF16, NB, MT, GROUPS>), grid, dim3(kManyWaves * 64), 0, st, a, p.parts, ntiles);
+    hipLaunchKernelGGL((w4a16_many_kernel<XF16, NB, MT, GROUPS>), grid, dim3(kManySides * kManyWaves * 64), 0, st, a,
+                       Divisor(static_cast<uint32_t>(p.parts)), ntiles / p.parts, ntiles % p.parts, ntiles);
   }
 }
 
@@ -407,9 +456,10 @@ void launch_x(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
 // 1792 blocks of 16 channels (8 x 4096 -> 28672) 25.6 / 19.4 / 18.2 us; at 384
 // (1 x 4096 -> 6144) 6.4 / 6.5 / 8.3 and at 313 (5 float32 x 1088 -> 5007) 6.8 /
 // 6.2 / 8.0 us.
-// More rows: parts of K until 512 workgroups share the work, each at least four
-// tiles.  At 64 x 14336 -> 4096 it takes 24.2 us with 256 workgroups, 22.6 with
-// 512, 27.9 with 1024 (the parts' sums are written and read again).
+// More rows: parts of K until 256 workgroups share the work, one on each compute
+// unit, each at least eight tiles.  64 x 14336 -> 4096 takes 20.1 us with 256
+// workgroups, 23.5 with 512 and 28.7 with 128 (of more parts the sums are written
+// and read again).
 W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = (N + 15) / 16, tiles = (K + 127) / 128;
   W4a16Plan p{1, 1, 1};
@@ -420,8 +470,8 @@ W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   p.nb = 2;
   p.mt = M <= 32 ? 2 : 4;
   const int64_t groups = (blocks + 2 * kManyWaves - 1) / (2 * kManyWaves) * ((M + 16 * p.mt - 1) / (16 * p.mt));
-  int64_t parts = (512 + groups - 1) / groups;
-  const int64_t most = tiles / 4;
+  int64_t parts = (256 + groups - 1) / groups;
+  const int64_t most = tiles / 8;
   parts = parts < most ? parts : most;
   p.parts = static_cast<int>(parts < 1 ? 1 : parts);
   return p;
@@ -430,9 +480,14 @@ W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_w4a16(const W4a16Args& a, bool x_f16, hipStream_t st) {
   const W4a16Plan p = w4a16_plan(a.M, a.N, a.K);
   x_f16 ? launch_x<true>(a, p, st) : launch_x<false>(a, p, st);
-  if (p.parts > 1)
-    hipLaunchKernelGGL(w4a16_join_kernel, dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>(a.M)),
-                       dim3(256), 0, st, a, p.parts);
+  if (p.parts > 1) {
+    if (a.N % 4 == 0)
+      hipLaunchKernelGGL(w4a16_join_kernel<4>, dim3(static_cast<unsigned>((a.N + 1023) / 1024), static_cast<unsigned>(a.M)),
+                         dim3(256), 0, st, a, p.parts);
+    else
+      hipLaunchKernelGGL(w4a16_join_kernel<1>, dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>(a.M)),
+                         dim3(256), 0, st, a, p.parts);
+  }
   return hipGetLastError();
 }
 
