@@ -19,10 +19,15 @@ constexpr int64_t kGrid = 1 << 24;   // workgroups of 256 threads: below 2^32 th
 
 AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D) {
   AttentionCut c{};
-  c.rowsplit = rows > 32 || (D == 256 && rows > 16);
-  c.tiles = !c.rowsplit && rows > 16 ? 2 : 1;
+  // One tile of rows: waves share it and take tokens each (16 rows of 64 sequences
+  // of up to 1024 tokens: 28.7 us, by rows 32.3; of 16 up to 2048: 19.5, 31.0).
+  // More: waves share the tokens and take rows each (32 rows: 38.1 us, with two
+  // tiles to every wave and tokens shared out 50.4; 32.6 and 31.6).
+  c.rowsplit = rows > 16;
   if (seqs < 1) seqs = 1;
-  const int64_t resident = 256 * (D == 256 || c.tiles == 2 ? 2 : 3);  // workgroups that fit the chip
+  const int64_t resident = 256 * (D == 256 ? 2 : 3);  // workgroups that fit the chip
+  // Few rows: pieces of 256 tokens, two steps for each wave of a workgroup (64
+  // sequences of 300 to 16384 tokens: 127 us, with 128 tokens 134, with 512 131).
   if (!c.rowsplit) {
     c.piece_log2 = 8;
     while ((seqs * capacity >> c.piece_log2) >= int64_t{1} << 30) ++c.piece_log2;
@@ -202,6 +207,9 @@ __global__ void __launch_bounds__(256) attention_join_parts_kernel(AttentionArgs
 template <int D>
 void launch_join(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t st) {
   const uint32_t rows = static_cast<uint32_t>(a.seqs) * a.max_q * a.q_heads;  // below 2^24
+  // Few rows have lanes enough only if a row's channels and parts are spread (32
+  // rows of 63 parts: 14.8 us with the attention, one wave to a row 26.2; 128
+  // rows 18.5, 20.8; 512 rows 31.0, 29.1; 2048 rows 77.5, 68.7).
   if (rows < 512 && (plan.own.rowsplit ? plan.own_slots : plan.own.groups.d) + plan.front_slots > 8)
     hipLaunchKernelGGL((attention_join_parts_kernel<D>), dim3(rows * (D / 32)), dim3(256), 0, st, a, plan);
   else

@@ -1,8 +1,8 @@
 // attention_kernel.h — softmax(c q . k) v of 16-row tiles over the quantized
 // cache, one pass over the tokens.
 //
-// A wave takes 16 R rows (a row: a query of one head of the group that shares
-// the cache head) through steps of 32 tokens:
+// A wave takes 16 rows (a row: a query of one head of the group that shares the
+// cache head) through steps of 32 tokens:
 //
 //   S^T = K Q^T   16 tokens x 16 rows an instruction; lane (row r, g) gets
 //                 tokens 4 g + i of both halves of the step;
@@ -12,15 +12,25 @@
 //
 // Codes meet the matrix instruction as exact fp16 numbers, widened in
 // registers as they come from memory: K's words hold eight channels of one
-// token, V's of two tokens are paired by halves first.  A float32 query is a
-// pair hi + lo of fp16 under a power of two of its row, and w is such a pair,
-// so that only the queries' and the probabilities' low 2^-20 are lost.
+// token, V's of two tokens are paired by halves first.  A query is brought under
+// a power of two of its row; a float32 one is a pair hi + lo of fp16 there, and
+// so is w, so that no more than 2^-22 of either is lost.  (A single fp16 w would
+// save an eighth of the many-row kernel's instructions and lose 2^-11 of every
+// weight.)  All other numbers are float32.
 //
 // ref stands in for the running maximum: any reference gives the same
 // quotient, and this one moves only when a weight w leaves 2^14 (fp16 ends at
 // 2^16) or a sum of p leaves 2^60.  It then becomes the maximum of t + log2 s_v
 // (s_v no less than 2^-60), minus 8, over the tokens seen.  The usual step
 // exchanges nothing between lanes and rescales nothing.
+//
+// What bounds it.  Few rows: the cache's bytes.  64 sequences of 300 to 16384
+// tokens, 8 heads of 128 at 4 bits (527 MB, 101 us at a large copy's rate, 88 at
+// the rate at which a kernel can only read them) take 117 us and their join 5.
+// Many rows: instructions.  A step of a wave is 24 to 32 matrix instructions (384
+// to 512 cycles), about 150 others (700) and 20 KB of LDS, and they overlap
+// little: 3 prompts of up to 1021 queries take 80 us beside 15 of the join, 17 of
+// them in matrix instructions.
 #pragma once
 
 #include <type_traits>
@@ -412,16 +422,20 @@ struct Partial {
   }
 };
 
-// Few rows: the waves of a workgroup share its 16 R rows and take every fourth
-// step each.
-template <int D, bool PAIR, int R>
+// Few rows: the waves of a workgroup share its 16 rows and take every fourth
+// step each.  The workgroups that fit the chip at once take equal runs of all
+// sequences' tokens: with parts of one sequence each, as many as the longest
+// needs, 64 sequences of 300 to 16384 tokens took 148 us for 117, since short
+// ones leave and long ones start late.  The queries' operands stay in LDS: in
+// registers they would leave two workgroups a compute unit for three.
+template <int D, bool PAIR>
 struct TokensLds {
-  typedef u4 Queries[R][D / 32][PAIR ? 2 : 1][64];
+  typedef u4 Queries[D / 32][PAIR ? 2 : 1][64];
   // Where two workgroups would not fit a compute unit's 160 KB, the queries lie
   // where the waves' shares come to lie.
-  static constexpr bool kShare = R * D == 256 && PAIR;
-  f4 o[kAttnWaves][R * (D / 16)][64];
-  float stat[kAttnWaves][R][16][2];
+  static constexpr bool kShare = D == 256 && PAIR;
+  f4 o[kAttnWaves][D / 16][64];
+  float stat[kAttnWaves][16][2];
   u4 apart[kShare ? 1 : sizeof(Queries) / 16];
   __device__ __forceinline__ Queries& queries() {
     return *reinterpret_cast<Queries*>(kShare ? static_cast<void*>(o) : static_cast<void*>(apart));
@@ -473,10 +487,10 @@ struct Run {
 
 // A section of a run: pieces [from, to) of sequence s.  whole: 1 if these are all
 // and there is no prefix, -1 if that is still to be found out.
-template <int D, int BITS, bool PAIR, int R>
+template <int D, int BITS, bool PAIR>
 __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const AttentionPlan& plan, int front, int h,
                                                int s, int from, int to, int whole, int slot,
-                                               TokensLds<D, PAIR, R>& lds) {
+                                               TokensLds<D, PAIR>& lds) {
   constexpr int NK = D / 32;   // instructions along a head's channels
   constexpr int NV = D / 16;   // channels of O a lane's row block holds
   constexpr int HALVES = PAIR ? 2 : 1;
@@ -488,12 +502,10 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
   const Pages table(a, s, front);
   int32_t pages = table.raw(a, begin, kAttnWaves, lane);
   const Span span = front ? front_span(a) : own_span(a, s);
-  constexpr int row0 = 0;
   if (span.rows <= 0) return;
   using Q = std::conditional_t<PAIR, float, _Float16>;
-  Raw8<Q> x[R][NK];
-#pragma unroll
-  for (int t = 0; t < R; ++t) load_query<D>(a, span, h, row0 + 16 * t + r, g, x[t]);
+  Raw8<Q> x[NK];
+  load_query<D>(a, span, h, r, g, x);
 
   if (whole < 0) {
     const int n = pieces_of(span.length, cut);
@@ -506,16 +518,11 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
     }
   }
   const Sight sight(a, span, front);
-  const int all_see = 16 * R <= span.rows ? sight.limit(0) : 0;  // what every row sees
+  const int all_see = 16 <= span.rows ? sight.limit(0) : 0;  // what every row sees
   const int steps = (sight.limit(a.group.quotient(span.rows - 1)) + kStep - 1) / kStep;
   const int stop = to << (cut.piece_log2 - 5);
   const int end = stop < steps ? stop : steps;
-  int limit[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int row = row0 + 16 * t + r;
-    limit[t] = row < span.rows ? sight.limit(a.group.quotient(row)) : 0;
-  }
+  const int limit = r < span.rows ? sight.limit(a.group.quotient(r)) : 0;
 
   constexpr int KW = Row<D, BITS>::kKeyWords;
   uint32_t keys[2 * KW], values[Row<D, BITS>::kWords];
@@ -535,38 +542,29 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
 
   // The queries go to LDS as operands, a wave's share of the channels each; c
   // makes scores (over log 2) of the products.
-  float c[R];
+  const int up = query_shift<D>(x);
+  const float c = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
 #pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int up = query_shift<D>(x[t]);
-    c[t] = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      if (j % kAttnWaves != wave) continue;
-      Operand hi, lo;
-      query_operands<BITS>(x[t][j], up, &hi, &lo);
-      lds.queries()[t][j][0][lane] = u4{hi.w[0], hi.w[1], hi.w[2], hi.w[3]};
-      if constexpr (PAIR) lds.queries()[t][j][1][lane] = u4{lo.w[0], lo.w[1], lo.w[2], lo.w[3]};
-    }
+  for (int j = 0; j < NK; ++j) {
+    if (j % kAttnWaves != wave) continue;
+    Operand hi, lo;
+    query_operands<BITS>(x[j], up, &hi, &lo);
+    lds.queries()[j][0][lane] = u4{hi.w[0], hi.w[1], hi.w[2], hi.w[3]};
+    if constexpr (PAIR) lds.queries()[j][1][lane] = u4{lo.w[0], lo.w[1], lo.w[2], lo.w[3]};
   }
   __syncthreads();
-  auto query_operand = [&](int t, int j, int p) { return __builtin_bit_cast(h8, lds.queries()[t][j][p][lane]); };
+  auto query_operand = [&](int j, int p) { return __builtin_bit_cast(h8, lds.queries()[j][p][lane]); };
   // The products start from what the codes' offset adds to them, taken off.
-  f4 start[R];
+  f4 start = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int t = 0; t < R; ++t) {
-    f4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NK; ++j)
 #pragma unroll
-    for (int j = 0; j < NK; ++j)
-#pragma unroll
-      for (int p = HALVES - 1; p >= 0; --p)
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), query_operand(t, j, p), sum, 0, 0, 0);
-    start[t] = -sum;
-  }
+    for (int p = HALVES - 1; p >= 0; --p)
+      start = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), query_operand(j, p), start, 0, 0, 0);
+  start = -start;
 
-  RowState<NV> state[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) state[t].clear();
+  RowState<NV> state;
+  state.clear();
   const Masks masks;
 
   int turn = 0;  // steps into the 32 whose pages are at hand
@@ -579,28 +577,24 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
     const bool partly = bad0 || bad1 || (step + 1) * kStep > all_see;  // some row does not see some token
 
     asm volatile("" ::: "memory");  // the queries are read again, not kept in registers
-    f4 sc[R][2];
+    f4 sc[2];
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
       h8 k[2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS>(keys + half * KW, j, masks);
 #pragma unroll
-      for (int t = 0; t < R; ++t)
+      for (int p = HALVES - 1; p >= 0; --p) {
+        const h8 q = query_operand(j, p);
 #pragma unroll
-        for (int p = HALVES - 1; p >= 0; --p) {
-          const h8 q = query_operand(t, j, p);
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            sc[t][half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                k[half], q, j == 0 && p == HALVES - 1 ? start[t] : sc[t][half], 0, 0, 0);
-        }
+        for (int half = 0; half < 2; ++half)
+          sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[half], q, j == 0 && p == HALVES - 1 ? start : sc[half], 0,
+                                                            0, 0);
+      }
     }
-    float kc[R][8];
+    float kc[8];
 #pragma unroll
-    for (int t = 0; t < R; ++t)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) kc[t][i] = ks[i / 4][i % 4] * c[t];
+    for (int i = 0; i < 8; ++i) kc[i] = ks[i / 4][i % 4] * c;
     if constexpr (!LAST) {
       if (++turn == 32) {
         pages = Pages::checked(a, table.raw(a, step + kAttnWaves, kAttnWaves, lane));
@@ -613,10 +607,8 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
       load_scales(a.ks, rb, g, ks);
     }
 
-    Operand w[R][2];
-#pragma unroll
-    for (int t = 0; t < R; ++t)
-      weigh_step<NV>(sc[t], kc[t], vs, partly, limit[t], step * kStep + 4 * g, bad0, bad1, state[t], w[t]);
+    Operand w[2];
+    weigh_step<NV>(sc, kc, vs, partly, limit, step * kStep + 4 * g, bad0, bad1, state, w);
 
 #pragma unroll
     for (int j = 0; j < NV / 4; ++j) {
@@ -626,10 +618,7 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
       for (int p = 1; p >= 0; --p)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int t = 0; t < R; ++t)
-            state[t].o[4 * j + e] =
-                __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[t][p].h, state[t].o[4 * j + e], 0, 0, 0);
+          state.o[4 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[e].h, w[p].h, state.o[4 * j + e], 0, 0, 0);
     }
     if constexpr (!LAST) {
       load_values<D, BITS>(a, rb, r, g, values);
@@ -644,76 +633,69 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
 
   // The waves' shares are brought to one reference and added up, in the order of
   // the waves, each wave taking a quarter of the channels.
-  if constexpr (TokensLds<D, PAIR, R>::kShare) __syncthreads();  // the queries are used up
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    float l = state[t].l;
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (g == 0) {
-      lds.stat[wave][t][r][0] = state[t].ref;
-      lds.stat[wave][t][r][1] = l;
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) lds.o[wave][t * NV + j][lane] = state[t].o[j];
+  if constexpr (TokensLds<D, PAIR>::kShare) __syncthreads();  // the queries are used up
+  float own = state.l;
+  own += __shfl_xor(own, 16);
+  own += __shfl_xor(own, 32);
+  if (g == 0) {
+    lds.stat[wave][r][0] = state.ref;
+    lds.stat[wave][r][1] = own;
   }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) lds.o[wave][j][lane] = state.o[j];
   __syncthreads();
-  const Partial partial(a, plan);
+  float top = kUnset, f[kAttnWaves], l = 0.f;
 #pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int row = row0 + 16 * t + r;
-    float top = kUnset, f[kAttnWaves], l = 0.f;
+  for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, lds.stat[k][r][0]);
 #pragma unroll
-    for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, lds.stat[k][t][r][0]);
+  for (int k = 0; k < kAttnWaves; ++k) {
+    f[k] = __builtin_amdgcn_exp2f(lds.stat[k][r][0] - top);
+    l += f[k] * lds.stat[k][r][1];
+  }
+  // Channels of this wave: its quarter of each lane's NV (i, 0 .. NV - 1).
+  constexpr int Q4 = NV / 4;
+  f4 sum[Q4];
 #pragma unroll
-    for (int k = 0; k < kAttnWaves; ++k) {
-      f[k] = __builtin_amdgcn_exp2f(lds.stat[k][t][r][0] - top);
-      l += f[k] * lds.stat[k][t][r][1];
-    }
-    // Channels of this wave: its quarter of each lane's NV (i, 0 .. NV - 1).
-    constexpr int Q4 = NV / 4;
-    f4 sum[Q4];
+  for (int j = 0; j < Q4; ++j) {
+    sum[j] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < Q4; ++j) {
-      sum[j] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < kAttnWaves; ++k) sum[j] += f[k] * lds.o[k][wave * Q4 + j][lane];
+  }
+  if (r >= span.rows) return;
+  const int query = a.group.quotient(r);
+  const int64_t token = span.first + query;
+  const int head = h * a.group.d + r - query * a.group.d;
+  const int channel = g * (D / 4) + wave * Q4;  // + NV i + j
+  if (whole) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t to = token * a.ldo + static_cast<int64_t>(head) * D + channel;
 #pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k) sum[j] += f[k] * lds.o[k][t * NV + wave * Q4 + j][lane];
-    }
-    if (row >= span.rows) continue;
-    const int query = a.group.quotient(row);
-    const int64_t token = span.first + query;
-    const int head = h * a.group.d + row - query * a.group.d;
-    const int c = g * (D / 4) + wave * Q4;  // + NV i + j
-    if (whole) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t to = token * a.ldo + static_cast<int64_t>(head) * D + c;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < Q4; ++j) {
-          if (a.out_f16)
-            static_cast<_Float16*>(a.out)[to + NV * i + j] = static_cast<_Float16>(sum[j][i] * inv);
-          else
-            static_cast<float*>(a.out)[to + NV * i + j] = sum[j][i] * inv;
-        }
-    } else {
-      const int64_t at = partial.row(a, plan, front, slot, token, query, head);
-      float* po = partial.o(a, at) + c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < Q4; ++j) po[NV * i + j] = sum[j][i];
-      if (g == 0 && wave == 0) {
-        float* st = partial.stat(a, at);
-        st[0] = top;
-        st[1] = l;
+      for (int j = 0; j < Q4; ++j) {
+        if (a.out_f16)
+          static_cast<_Float16*>(a.out)[to + NV * i + j] = static_cast<_Float16>(sum[j][i] * inv);
+        else
+          static_cast<float*>(a.out)[to + NV * i + j] = sum[j][i] * inv;
       }
+  } else {
+    const Partial partial(a, plan);
+    const int64_t at = partial.row(a, plan, front, slot, token, query, head);
+    float* po = partial.o(a, at) + channel;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < Q4; ++j) po[NV * i + j] = sum[j][i];
+    if (g == 0 && wave == 0) {
+      float* st = partial.stat(a, at);
+      st[0] = top;
+      st[1] = l;
     }
   }
 }
-template <int D, int BITS, bool PAIR, int R>
+template <int D, int BITS, bool PAIR>
 __device__ __forceinline__ void tokens_body(const AttentionArgs& a, const AttentionPlan& plan, int front,
-                                            uint32_t block, TokensLds<D, PAIR, R>& lds) {
+                                            uint32_t block, TokensLds<D, PAIR>& lds) {
   const AttentionCut& cut = front ? plan.front : plan.own;
   const int lane = threadIdx.x & 63;
   const int w = a.by_heads.quotient(block), h = block - w * a.heads;
@@ -744,22 +726,25 @@ __device__ __forceinline__ void tokens_body(const AttentionArgs& a, const Attent
       }
       if (from > first) __syncthreads();  // the section before has left LDS
     }
-    tokens_section<D, BITS, PAIR, R>(a, plan, front, h, s, from - start, to - start, whole, front ? w : w + s, lds);
+    tokens_section<D, BITS, PAIR>(a, plan, front, h, s, from - start, to - start, whole, front ? w : w + s, lds);
     from = to;
     start += n;
   }
 }
-template <int D, int BITS, bool PAIR, int R>
-__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 || R > 1 ? 2 : 3)
+template <int D, int BITS, bool PAIR>
+__global__ void __launch_bounds__(kAttnWaves * 64, D == 256 ? 2 : 3)
     attention_tokens_kernel(AttentionArgs a, AttentionPlan plan, int front) {
-  __shared__ TokensLds<D, PAIR, R> lds;
-  tokens_body<D, BITS, PAIR, R>(a, plan, front, blockIdx.x, lds);
+  __shared__ TokensLds<D, PAIR> lds;
+  tokens_body<D, BITS, PAIR>(a, plan, front, blockIdx.x, lds);
 }
 
 // Many rows: a wave's 16 rows are its own, and the waves share the widening.
 // Two steps at a time (a block) go through LDS as operands, each wave bringing
 // the keys and values of half a step, and all waves multiply all.  The codes of
-// two more blocks are on their way meanwhile.
+// two more blocks are on their way meanwhile.  (Keys to two waves and values to
+// the others, one block ahead: 102 us for 98 at 3 prompts of up to 1021 queries.
+// Two row tiles a wave, which read LDS half as often but leave two waves to a
+// SIMD for three: 188.  Four waves at the price of one block ahead: 111.)
 template <int D>
 struct RowsLds {
   static constexpr int kBlock = 2;
@@ -982,13 +967,13 @@ __global__ void __launch_bounds__(kAttnWaves * 64, rows_resident(D, BITS, PAIR))
     attention_both_kernel(AttentionArgs a, AttentionPlan plan, uint32_t front_blocks) {
   __shared__ union Lds {
     RowsLds<D> rows;
-    TokensLds<D, PAIR, 1> tokens;
+    TokensLds<D, PAIR> tokens;
     __device__ Lds() {}
   } lds;
   if (blockIdx.x < front_blocks)
     rows_body<D, BITS, PAIR>(a, plan, 1, blockIdx.x, lds.rows);
   else
-    tokens_body<D, BITS, PAIR, 1>(a, plan, 0, blockIdx.x - front_blocks, lds.tokens);
+    tokens_body<D, BITS, PAIR>(a, plan, 0, blockIdx.x - front_blocks, lds.tokens);
 }
 
 // Workgroups of a cut.
@@ -1004,18 +989,12 @@ void launch_cut(const AttentionArgs& a, const AttentionPlan& plan, int front, hi
     hipLaunchKernelGGL((attention_rows_kernel<D, BITS, PAIR>), grid, block, 0, st, a, plan, front);
     return;
   }
-  if constexpr (D < 256) {
-    if (c.tiles == 2) {
-      hipLaunchKernelGGL((attention_tokens_kernel<D, BITS, PAIR, 2>), grid, block, 0, st, a, plan, front);
-      return;
-    }
-  }
-  hipLaunchKernelGGL((attention_tokens_kernel<D, BITS, PAIR, 1>), grid, block, 0, st, a, plan, front);
+  hipLaunchKernelGGL((attention_tokens_kernel<D, BITS, PAIR>), grid, block, 0, st, a, plan, front);
 }
 
 template <int D, int BITS, bool PAIR>
 void launch_parts(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t st) {
-  if (a.prefix_table && plan.front.rowsplit && !plan.own.rowsplit && plan.own.tiles == 1) {
+  if (a.prefix_table && plan.front.rowsplit && !plan.own.rowsplit) {
     const int64_t front = cut_blocks(a, plan.front, 1);
     const dim3 grid(static_cast<unsigned>(front + cut_blocks(a, plan.own, a.seqs)));
     hipLaunchKernelGGL((attention_both_kernel<D, BITS, PAIR>), grid, dim3(kAttnWaves * 64), 0, st, a, plan,

@@ -90,7 +90,7 @@ struct AttentionArgs {
 };
 
 // How the tokens of the sequences (own), or of the prefix (front), are cut.
-// Few rows (rowsplit 0): a workgroup takes 16 * tiles rows of a cache head, its
+// Few rows (rowsplit 0): a workgroup takes the rows of a cache head, its
 // waves sharing the tokens.  Tokens come in pieces of 2^piece_log2, and each of
 // `groups` workgroups of a head takes an equal run of the pieces of all
 // sequences (`groups` ones of the prefix).
@@ -98,7 +98,7 @@ struct AttentionArgs {
 // sequence (or of all queries), and their tokens are cut into up to `parts`
 // equal parts of 2^piece_log2 or more.
 struct AttentionCut {
-  int tiles, rowsplit, piece_log2;
+  int rowsplit, piece_log2;
   int one_piece;  // few rows: a workgroup of a head for every piece there can be
   Divisor groups;
   Divisor parts;

@@ -139,10 +139,11 @@ size_t w4a4_cache_attention_workspace_size(const w4a4_cache* cache, int64_t toke
  *           0: none.
  *   Rows of q that belong to no sequence are not read, and those of out are
  *   left as they are.  A query that sees nothing gets zeros.
- *   Scores and sums are float32: codes are exact, a float32 query enters as a
- *   pair of fp16 values under a power of two of its row, and the probability
- *   times the value's scale as such a pair too (off by 2^-22 of itself or
- *   2^-33 of the row's largest).  What masked positions hold has no effect.
+ *   Scores and sums are float32: codes are exact, queries enter under a power
+ *   of two of their row, fp16 ones as they are (what is below 2^-31 of the
+ *   row's largest may be lost) and float32 ones as a pair of fp16 values, and
+ *   the probability times the value's scale as such a pair too (off by 2^-22 of
+ *   itself or 2^-33 of the row's largest).  What masked positions hold has no effect.
  *   A row's result depends on its own sequence and the prefix only (the
  *   call's sizes and the lengths choose the order of its sums) and is the
  *   same from call to call.
