@@ -54,6 +54,7 @@ struct Channels {
 template <int GROUPS>
 __device__ __forceinline__ uint32_t load_scales(const W4a16Args& a, int64_t channel, int first, int end, int i) {
   int at = first + i;
+  if constexpr (GROUPS == HALVES) end = end < a.K / 64 ? end : a.K / 64;  // K may end in the middle of the last tile
   at = at < end ? at : end - 1;
   const int64_t s = channel + a.group_halves.quotient(GROUPS == HALVES ? at : 2 * at);
   return a.sw_f16 ? static_cast<const uint16_t*>(a.sw)[s] : static_cast<const uint32_t*>(a.sw)[s];

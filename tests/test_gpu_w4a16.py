@@ -200,3 +200,17 @@ def test_graph_and_streams():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), k
+
+
+@pytest.mark.parametrize("K,group", [(64, 64), (192, 64), (192, 192), (1088, 64)])
+@pytest.mark.parametrize("x_dt", ["f16", "f32"])
+def test_nothing_behind_the_scales_counts(K, group, x_dt):
+    # K ends in the middle of a tile: that tile's second half has no scale.
+    print("w4a16 scales' end", K, group, x_dt, flush=True)
+    for M in (1, 5, 20, 40):
+        x, wq, s = inputs(M, K, 33, group, x_dt, "f32", K + M)
+        room = torch.full((s.size + 64,), float("nan"), device=DEV)
+        room[:s.size] = dev(s).reshape(-1)
+        ref, size = O.qlinear_w4a16(x, wq, s, group)
+        got = host(D.qlinear_w4a16(dev(x), dev(wq), room[:s.size].view(s.shape), group, w_layout="rowmajor"))
+        assert np.all(np.abs(got - ref) <= bar(size, ref, K, "f32"))
