@@ -19,7 +19,7 @@
 // weight.)  All other numbers are float32.
 //
 // ref stands in for the running maximum: any reference gives the same
-// quotient, and this one moves only when a weight w leaves 2^14 (fp16 ends at
+// quotient, and this one moves only when a weight |w| leaves 2^14 (fp16 ends at
 // 2^16) or a sum of p leaves 2^60.  It then becomes the maximum of t + log2 s_v
 // (s_v no less than 2^-60), minus 8, over the tokens seen.  The usual step
 // exchanges nothing between lanes and rescales nothing.
@@ -235,10 +235,10 @@ __device__ __forceinline__ h2 remainders(h2 hi, float a, float b) {
   return two_halves(fmaf(static_cast<float>(hi[0]), -1.f, a), fmaf(static_cast<float>(hi[1]), -1.f, b));
 }
 
-// log2 of a scale, down to the integer, between 2^-60 and 2^127.
+// log2 of a scale's size, down to the integer, between 2^-60 and 2^127.
 __device__ __forceinline__ float exponent(float v) {
   const int e = __builtin_amdgcn_frexp_expf(v);
-  return v > 8.6736174e-19f ? static_cast<float>(e) : -60.f;
+  return fabsf(v) > 8.6736174e-19f ? static_cast<float>(e) : -60.f;
 }
 
 constexpr float kUnset = -1e30f;  // reference of a row that has seen nothing
@@ -288,7 +288,7 @@ __device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const
       const float p = __builtin_amdgcn_exp2f(fmaf(x[i], kc[i], -s.ref));
       wt[i] = p * vs[i];
       sum += p;
-      top = fmaxf(top, wt[i]);
+      top = fmaxf(top, fabsf(wt[i]));
     }
   };
   weigh();

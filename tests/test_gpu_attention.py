@@ -407,3 +407,54 @@ def test_graph_and_streams(prefix):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), k
+
+
+@pytest.mark.parametrize("dim,bits,dt", [(64, 4, "f32"), (64, 8, "f16"), (128, 8, "f32"), (128, 4, "f16")])
+def test_long_parts_of_many_rows(dim, bits, dt):
+    # So many sequences that one of 9000 tokens is cut into eight parts of 36 steps
+    # of 32 only, more than whose pages are looked up at once; some of them absent.
+    print("attention long parts", dim, bits, dt, flush=True)
+    S, heads, group, page = 96, 8, 20, 64
+    lengths = [9000] + [1] * (S - 1)
+    cache = make_cache(240, heads, page, dim, bits, 21)
+    tables, _ = tables_of(240, lengths, page, np.random.default_rng(3), width=144)
+    tables[0, [5, 18, 70, 71, 140]] = [-1, 240, -7, 1 << 30, -1]
+    check(queries(S, heads * group, dim, dt, 9), cache, tables, lengths)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_long_runs_of_few_rows(dt):
+    # So many heads that one workgroup takes all tokens of a head, its waves 36
+    # steps each.  The reference takes three of the heads.
+    print("attention long runs", dt, flush=True)
+    heads, dim, page, lengths = 768, 64, 64, [4500, 300]
+    g = np.random.default_rng(4)
+    kc, vc = (g.integers(0, 256, (78, heads, page, dim // 2), dtype=np.uint8) for _ in range(2))
+    ks, vs = (g.uniform(0.01, 0.05, (78, heads, page)).astype(np.float32) for _ in range(2))
+    tables, _ = tables_of(78, lengths, page, g)
+    tables[0, [3, 66]] = -1
+    q = queries(2, heads, dim, dt, 5)
+    got = host(D.cache_attention(dev(q), D.KVCache(dev(kc), dev(vc), dev(ks), dev(vs), 4), dev(tables),
+                                 dev(np.array(lengths, np.int32)), out_dtype=torch.float32)).reshape(2, heads, dim)
+    at = [0, 400, 767]
+    few = tuple(np.ascontiguousarray(t[:, at]) for t in (kc, vc, ks, vs))
+    ref, size, reach = O.attention(q.reshape(2, heads, dim)[:, at].reshape(2, -1), few + (4,), tables, lengths)
+    assert np.all(np.abs(got[:, at].reshape(2, -1) - ref) <= bar(ref, size, reach, tables.shape[1] * page, "f32"))
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_scales_of_either_sign(n):
+    # A cache that a caller filled: values are codes times scales, whatever their signs.
+    print("attention signs", n, flush=True)
+    heads, group, dim, page = 2, 4, 64, 16
+    (kc, vc, ks, vs, bits), _ = make_cache(40, heads, page, dim, 8, 14)
+    rng = np.random.default_rng(15)
+    vs *= (rng.choice([-1.0, 1.0], vs.shape) * 2.0 ** rng.integers(-30, 31, vs.shape)).astype(np.float32)
+    ks *= rng.choice([-1.0, 1.0], ks.shape).astype(np.float32)
+    cache = ((kc, vc, ks, vs, bits), D.KVCache(dev(kc), dev(vc), dev(ks), dev(vs), bits))
+    lengths = [300, 40, 17, 200]
+    tables, _ = tables_of(40, lengths, page, rng)
+    check(queries(4 * n, heads * group, dim, "f32", 16), cache, tables, lengths, q_start=np.arange(5) * n, max_q=n)
+    vs[:] = -np.float32(2.0 ** 40)
+    cache = ((kc, vc, ks, vs, bits), D.KVCache(dev(kc), dev(vc), dev(ks), dev(vs), bits))
+    check(queries(4 * n, heads * group, dim, "f32", 17), cache, tables, lengths, q_start=np.arange(5) * n, max_q=n)
