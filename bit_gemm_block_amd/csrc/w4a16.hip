@@ -33,18 +33,26 @@ constexpr int kManySides = 2;  // and how many such tiles at a time
 
 enum Groups { WHOLE = 0, TILES = 1, HALVES = 2 };  // scales: one per channel, per tiles, per half tiles
 
-// Where a lane's codes of 16 channels lie.
+// Where a lane's codes and scales of 16 channels lie: uniform bases and 32-bit
+// offsets, two registers instead of six.
 struct Channels {
-  const uint8_t* p;
-  int64_t n;      // the lane's channel (the last one past N)
-  int64_t scale;  // its first scale
+  const uint8_t* base;
+  int64_t n0, scale;        // the first channel, its first scale
+  uint32_t off, scale_off;  // the lane's
+  int in;                   // its channel is n0 + in (the last one past N)
   __device__ __forceinline__ void set(const W4a16Args& a, int64_t block, int lane) {
     const int64_t last = (a.N - 1) / 16;
     block = block < last ? block : last;  // a block past the last one repeats it
-    n = block * 16 + (lane & 15);
-    n = n < a.N ? n : a.N - 1;
-    p = a.tiled ? a.wq + block * (8 * static_cast<int64_t>(a.K)) + lane * 16 : a.wq + n * (a.K / 2) + (lane >> 4) * 16;
-    scale = n * a.groups;
+    n0 = block * 16;
+    const int left = a.N - n0 < 16 ? static_cast<int>(a.N - n0) : 16;
+    in = (lane & 15) < left ? lane & 15 : left - 1;
+    base = a.wq + (a.tiled ? block * (8 * static_cast<int64_t>(a.K)) : n0 * (a.K / 2));
+    off = a.tiled ? lane * 16 : in * (a.K / 2) + (lane >> 4) * 16;
+    scale = n0 * a.groups;
+    scale_off = in * a.groups;
+  }
+  __device__ __forceinline__ u4 codes(int64_t at, bool past) const {
+    return *reinterpret_cast<const u4*>(base + at + (off - (past ? 32u : 0u)));
   }
 };
 
@@ -52,12 +60,12 @@ struct Channels {
 // of the i-th from `first` on (in halves or tiles of K, not past `end`), and
 // element i of channel r is that lane's.
 template <int GROUPS>
-__device__ __forceinline__ uint32_t load_scales(const W4a16Args& a, int64_t channel, int first, int end, int i) {
+__device__ __forceinline__ uint32_t load_scales(const W4a16Args& a, const Channels& ch, int first, int end, int i) {
   int at = first + i;
   if constexpr (GROUPS == HALVES) end = end < a.K / 64 ? end : a.K / 64;  // K may end in the middle of the last tile
   at = at < end ? at : end - 1;
-  const int64_t s = channel + a.group_halves.quotient(GROUPS == HALVES ? at : 2 * at);
-  return a.sw_f16 ? static_cast<const uint16_t*>(a.sw)[s] : static_cast<const uint32_t*>(a.sw)[s];
+  const uint32_t s = ch.scale_off + a.group_halves.quotient(GROUPS == HALVES ? at : 2 * at);
+  return a.sw_f16 ? (static_cast<const uint16_t*>(a.sw) + ch.scale)[s] : (static_cast<const uint32_t*>(a.sw) + ch.scale)[s];
 }
 __device__ __forceinline__ float scale_of(const W4a16Args& a, uint32_t s) {
   return a.sw_f16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(s))) : float_of(s);
@@ -116,7 +124,7 @@ __device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part,
 // tiles instead takes 23 us for 17.5 at 8 x 4096 -> 28672, and loads that bypass
 // the caches 23.
 template <bool XF16, int NB, int GROUPS>
-__global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
+__global__ void __launch_bounds__(kWaves * 64, XF16 && GROUPS != HALVES ? 4 : 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
   constexpr int XV = XF16 ? 1 : 2;                   // 16 bytes of x to eight elements
   constexpr int U = NB == 1 && XF16 ? 4 : 2;         // tiles of each block of channels on their way together
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, 
       const bool past = half_tile && tt == ntiles - 1 && g >= 2;  // this lane's codes are past K
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        c[u][b] = *reinterpret_cast<const u4*>(ch[b].p + tt * wstep - (past ? 32 : 0));
+        c[u][b] = ch[b].codes(tt * wstep, past);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) w4a16_few_kernel(W4a16Args a, 
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int l = 0; l < SL; ++l) sr[b][l] = load_scales<GROUPS>(a, ch[b].scale, t * HALF + 4 * l, t1 * HALF, g);
+        for (int l = 0; l < SL; ++l) sr[b][l] = load_scales<GROUPS>(a, ch[b], t * HALF + 4 * l, t1 * HALF, g);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -276,8 +284,8 @@ __global__ void __launch_bounds__(kManySides * kManyWaves * 64, 2) w4a16_many_ke
       }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      c[b] = *reinterpret_cast<const u4*>(ch[b].p + t * wstep - (past ? 32 : 0));
-      if constexpr (GROUPS != WHOLE) s[b] = load_scales<GROUPS>(a, ch[b].scale, t * HALF, ntiles * HALF, g);
+      c[b] = ch[b].codes(t * wstep, past);
+      if constexpr (GROUPS != WHOLE) s[b] = load_scales<GROUPS>(a, ch[b], t * HALF, ntiles * HALF, g);
     }
   };
   auto put = [&](int t, int buffer) {
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kManySides * kManyWaves * 64, 2) w4a16_many_ke
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     float f = XF16 ? 1.f : 16.f;
-    if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, ch[b].n, a.sw_f16);
+    if constexpr (GROUPS == WHOLE) f *= load_scale(a.sw, ch[b].n0 + ch[b].in, a.sw_f16);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
