@@ -169,20 +169,20 @@ __device__ __forceinline__ void load_scales(const float* s, const int64_t* rb, u
     d[h] = *reinterpret_cast<const f4*>(s + rb[h] + 4 * g);
 }
 
-// K's codes 8 j to 8 j + 7 of a lane, unsigned, as fp16 subnormal numbers u 2^-24
-// (the bits of a small whole number are that times 2^-24): in the order
-// 0 4 1 5 2 6 3 7, the third, fourth, seventh and eighth times 16 (4 bits), or
-// in their own (8 bits).  Their offset, 8 or 128, is taken out of the product
-// by its starting value.
+// K's codes 8 j to 8 j + 7 of a lane, unsigned, as fp16 subnormal numbers u 2^-20
+// (4 bits, in the order 0 4 1 5 2 6 3 7) or u 2^-24 (8 bits): the bits of a small
+// whole number are that times 2^-24.  Their offset, 8 or 128, is taken out of the
+// product by its starting value.  The instruction aligns products by the exponent
+// that subnormals share, 2^-14, and cuts what falls behind: codes stand high in
+// their ten bits (4-bit codes as u 2^-24 cost five bits of the scores).
 template <int BITS>
 __device__ __forceinline__ h8 key_operand(const uint32_t* k, int j, const Masks& m) {
   Operand o;
   if constexpr (BITS == 4) {
-    const uint32_t s = k[j] >> 8;
-    o.w[0] = (k[j] & m.even) ^ m.key_even;
-    o.w[1] = (k[j] & m.odd) ^ m.key_odd;
-    o.w[2] = (s & m.even) ^ m.key_even;
-    o.w[3] = (s & m.odd) ^ m.key_odd;
+    o.w[0] = ((k[j] << 4) & m.odd) ^ m.key;
+    o.w[1] = (k[j] & m.odd) ^ m.key;
+    o.w[2] = ((k[j] >> 4) & m.odd) ^ m.key;
+    o.w[3] = ((k[j] >> 8) & m.odd) ^ m.key;
   } else {
     const uint32_t a = k[2 * j] ^ 0x80808080u, b = k[2 * j + 1] ^ 0x80808080u;
     o.w[0] = __builtin_amdgcn_perm(a, a, 0x0c010c00);
@@ -192,14 +192,15 @@ __device__ __forceinline__ h8 key_operand(const uint32_t* k, int j, const Masks&
   }
   return o.h;
 }
-// The channel of the element e of such an operand, and log2 of its factor.
+// The channel of the element e of such an operand.
 template <int BITS>
 __device__ constexpr int key_channel(int e) {
   return BITS == 4 ? (e & 1) * 4 + e / 2 : e;
 }
+// What makes scores (over log 2) of products with a query brought up by 2^up.
 template <int BITS>
-__device__ constexpr int key_factor(int e) {
-  return BITS == 4 && (e & 2) ? 4 : 0;
+__device__ __forceinline__ float score_factor(const AttentionArgs& a, int up) {
+  return ldexpf(a.scale * 1.4426950408889634f, (BITS == 4 ? 20 : 24) - up);
 }
 
 // Four channels of a lane's tokens in pairs (four of a step, two of a half), as
@@ -383,8 +384,8 @@ template <int BITS, typename Q>
 __device__ __forceinline__ void query_operands(const Raw8<Q>& x, int up, Operand* hi, Operand* lo) {
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    const float v0 = ldexpf(x.get(key_channel<BITS>(e)), up - key_factor<BITS>(e));
-    const float v1 = ldexpf(x.get(key_channel<BITS>(e + 1)), up - key_factor<BITS>(e + 1));
+    const float v0 = ldexpf(x.get(key_channel<BITS>(e)), up);
+    const float v1 = ldexpf(x.get(key_channel<BITS>(e + 1)), up);
     hi->p[e / 2] = two_halves(v0, v1);
     lo->p[e / 2] = remainders(hi->p[e / 2], v0, v1);
   }
@@ -394,7 +395,7 @@ template <int BITS>
 __device__ __forceinline__ h8 offset_operand() {
   Operand o;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) o.w[p] = BITS == 8 || p % 2 ? 0x00800080u : 0x00080008u;
+  for (int p = 0; p < 4; ++p) o.w[p] = 0x00800080u;  // 128, or 16 times 8
   return o.h;
 }
 
@@ -543,7 +544,7 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
   // The queries go to LDS as operands, a wave's share of the channels each; c
   // makes scores (over log 2) of the products.
   const int up = query_shift<D>(x);
-  const float c = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
+  const float c = score_factor<BITS>(a, up);
 #pragma unroll
   for (int j = 0; j < NK; ++j) {
     if (j % kAttnWaves != wave) continue;
@@ -833,7 +834,7 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
 
   Operand q[NK][HALVES];
   const int up = query_shift<D>(x);
-  const float c = ldexpf(a.scale * 1.4426950408889634f, 24 - up);
+  const float c = score_factor<BITS>(a, up);
   f4 start = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < NK; ++j) {

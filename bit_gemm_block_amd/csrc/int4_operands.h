@@ -30,10 +30,10 @@ union Operand {
 // it would be two instructions.
 struct Masks {
   uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
-  uint32_t key_even = 0x00080008u, key_odd = 0x00800080u;
+  uint32_t key = 0x00800080u;
   uint32_t value_even = 0x64086408u, value_odd = 0x64806480u;
   __device__ __forceinline__ Masks() {
-    asm("" : "+s"(even), "+s"(odd), "+v"(key_even), "+v"(key_odd), "+v"(value_even), "+v"(value_odd));
+    asm("" : "+s"(even), "+s"(odd), "+v"(key), "+v"(value_even), "+v"(value_odd));
   }
 };
 

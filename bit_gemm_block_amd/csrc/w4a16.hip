@@ -16,7 +16,7 @@
 // with the other half of x zero.
 //
 // What bounds it: the codes' bytes, at 5.2 TB/s of a large copy.  8 x 4096 ->
-// 28672 (61 MB) takes 17.5 us, 3.4 TB/s, against 11.7; one token 4096 -> 6144 (13
+// 28672 (61 MB) takes 15.7 us, 3.8 TB/s, against 11.7; one token 4096 -> 6144 (13
 // MB, 2.5 us) 6.2, which is the launch and one way to memory and back; 64 x 14336
 // -> 4096 (31.7 MB, 6.1 us) 20.1: 16 in the product, whose tiles of x, 16 KB
 // beside 8 KB of codes, each wait for a barrier, and 4 in the parts' sum.
@@ -120,9 +120,9 @@ __device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part,
 // Up to 16 rows: a workgroup takes 16 NB channels, its waves runs of their tiles,
 // and adds the waves' sums up through LDS, in their order.  Each wave brings x
 // from the caches itself (rows past M repeat the last one and are not stored).
-// All loads of U tiles are issued before the first is used; a ring of single
-// tiles instead takes 23 us for 17.5 at 8 x 4096 -> 28672, and loads that bypass
-// the caches 23.
+// All loads of U tiles are issued before the first is used; at 8 x 4096 -> 28672 a
+// ring of single tiles instead took 23 us for 17.5, loads that bypass the caches 23,
+// and registers for one workgroup a compute unit only 17.4 for 15.7.
 template <bool XF16, int NB, int GROUPS>
 __global__ void __launch_bounds__(kWaves * 64, XF16 && GROUPS != HALVES ? 4 : 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
@@ -460,11 +460,11 @@ void launch_x(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
 
 }  // namespace
 
-// Up to 16 rows: a workgroup with more channels reads x less often, one with fewer
-// leaves more workgroups to fill the chip.  Measured, 16 / 32 / 64 channels: at
-// 1792 blocks of 16 channels (8 x 4096 -> 28672) 25.6 / 19.4 / 18.2 us; at 384
-// (1 x 4096 -> 6144) 6.4 / 6.5 / 8.3 and at 313 (5 float32 x 1088 -> 5007) 6.8 /
-// 6.2 / 8.0 us.
+// Up to 16 rows: as few channels to a workgroup as leave one for each compute unit;
+// fewer make a second round of them, more leave compute units empty.  Measured
+// with 16 / 32 / 64 channels, 8 x 4096 ->: 4096 6.3 / 7.3 / 9.0 us, 8192 8.9 / 8.3
+// / 9.6, 12288 12.3 / 11.7 / 9.8, 28672 25.4 / 20.2 / 18.5; float32 5 x 1024 ->
+// 5008 6.4 / 5.5 / 6.3.
 // More rows: parts of K until 256 workgroups share the work, one on each compute
 // unit, each at least eight tiles.  64 x 14336 -> 4096 takes 20.1 us with 256
 // workgroups, 23.5 with 512 and 28.7 with 128 (of more parts the sums are written
@@ -473,7 +473,7 @@ W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = (N + 15) / 16, tiles = (K + 127) / 128;
   W4a16Plan p{1, 1, 1};
   if (M <= 16) {
-    p.nb = blocks >= 1024 ? 4 : blocks >= 256 ? 2 : 1;
+    p.nb = blocks <= 256 ? 1 : blocks <= 512 ? 2 : 4;
     return p;
   }
   p.nb = 2;

@@ -458,3 +458,25 @@ def test_scales_of_either_sign(n):
     vs[:] = -np.float32(2.0 ** 40)
     cache = ((kc, vc, ks, vs, bits), D.KVCache(dev(kc), dev(vc), dev(ks), dev(vs), bits))
     check(queries(4 * n, heads * group, dim, "f32", 17), cache, tables, lengths, q_start=np.arange(5) * n, max_q=n)
+
+
+@pytest.mark.parametrize("dim,bits", [(64, 4), (64, 8), (128, 4), (128, 8), (256, 4), (256, 8)])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_precision_over_a_whole_output(dim, bits, dt, n):
+    # Norm over norm.  A score of normal queries and keys is a few units, a sum of
+    # `dim` products the largest of which is about a fifth of the sum of their
+    # sizes; the matrix instructions cut each product at 2^-22 of the largest with
+    # it (24 bits, two of them lost to subnormal codes), of random sign, so that a
+    # score is off by 2^-22 times a few units times the chain of up to 16: below
+    # 2^-18, as is, to first order, an average of values under such weights.
+    print("attention precision", dim, bits, dt, n, flush=True)
+    heads, group, page, lengths = 2, 4, 32, [700, 64, 333]
+    cache = make_cache(36, heads, page, dim, bits, dim + n)
+    tables, _ = tables_of(36, lengths, page, np.random.default_rng(n))
+    q = queries(3 * n, heads * group, dim, dt, n)
+    got = check(q, cache, tables, lengths, q_start=np.arange(4) * n, max_q=n)
+    ref, _, _ = O.attention(q, cache[0], tables, lengths, q_start=np.arange(4) * n, max_q=n)
+    off = float(np.linalg.norm(got - ref) / np.linalg.norm(ref))
+    print("  off by", off, flush=True)
+    assert off <= 2.0 ** -18
