@@ -17,7 +17,8 @@ namespace {
 
 constexpr int64_t kGrid = 1 << 24;   // workgroups of 256 threads: below 2^32 threads
 
-AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D) {
+// `beside`: a prefix whose workgroups run beside those of the own tokens.
+AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D, bool beside) {
   AttentionCut c{};
   // One tile of rows: waves share it and take tokens each (16 rows of 64 sequences
   // of up to 1024 tokens: 28.7 us, by rows 32.3; of 16 up to 2048: 19.5, 31.0).
@@ -42,13 +43,15 @@ AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capac
   c.groups = Divisor(static_cast<uint32_t>(groups));
   // Rows' workgroups cost their queries' operands and a partial result each, so
   // parts are long (1024 tokens; 3 prompts of 1021 queries: 98 us, with 512 113,
-  // with 2048 101), unless without parts of 256 the chip would be half empty.
-  // One workgroup on each unit is enough then: a second round of them, or own
-  // tokens that wait behind, cost more (64 sequences on a prefix of 8192: 38 us
-  // with 256 workgroups, 45 with 512, 50 with 1024).
+  // with 2048 101), unless there are too few of them for the chip (256 tokens).
+  // Then there are parts until the workgroups that fit at once are there (one
+  // prompt of 512 queries behind 8192 tokens: 153 us with 768, 199 with 256; 44
+  // drafts of 7 behind up to 4474: 24 and 41), but for a prefix only one to a
+  // compute unit, since own tokens share the chip (64 sequences on a prefix of
+  // 8192: 38 us with 256, 45 with 512, 50 with 1024).
   const int64_t units = seqs * heads * groups;
-  c.piece_log2 = units < resident ? 8 : 10;
-  int64_t parts = units < resident ? (256 + units - 1) / units : 8;
+  c.piece_log2 = units < 256 ? 8 : 10;
+  int64_t parts = units < resident ? ((beside ? 256 : resident) + units - 1) / units : 8;
   const int64_t most = capacity >> c.piece_log2;
   parts = parts < most ? parts : most;
   c.parts = Divisor(static_cast<uint32_t>(parts < 1 ? 1 : parts));
@@ -223,14 +226,14 @@ bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
   *plan = AttentionPlan{};
   AttentionCut& own = plan->own;
   AttentionCut& front = plan->front;
-  own = cut_tokens(own_rows, a.seqs, a.heads, a.width << a.page_log2, a.D);
+  own = cut_tokens(own_rows, a.seqs, a.heads, a.width << a.page_log2, a.D, false);
   const int64_t cap = a.width << a.page_log2;
   const bool split = own.rowsplit ? own.parts.d > 1 : cap > int64_t{1} << own.piece_log2;
   plan->join = split || a.prefix_width > 0;
   // Few rows: run w of sequence s is slot w + s.
   if (plan->join) plan->own_slots = own.rowsplit ? own.parts.d : static_cast<int64_t>(own.groups.d) + a.seqs;
   if (a.prefix_width > 0) {
-    front = cut_tokens(front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D);
+    front = cut_tokens(front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D, !own.rowsplit);
     plan->front_slots = front.rowsplit ? front.parts.d : front.groups.d;
   }
   return cut_blocks(a, own, a.seqs) + (a.prefix_width > 0 ? cut_blocks(a, front, 1) : 0) < kGrid &&

@@ -466,9 +466,9 @@ void launch_x(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
 // / 9.6, 12288 12.3 / 11.7 / 9.8, 28672 25.4 / 20.2 / 18.5; float32 5 x 1024 ->
 // 5008 6.4 / 5.5 / 6.3.
 // More rows: parts of K until 256 workgroups share the work, one on each compute
-// unit, each at least eight tiles.  64 x 14336 -> 4096 takes 20.1 us with 256
+// unit, each a tile to a side at least.  64 x 14336 -> 4096 takes 20.1 us with 256
 // workgroups, 23.5 with 512 and 28.7 with 128 (of more parts the sums are written
-// and read again).
+// and read again); 58 x 1472 -> 855 12.1 us, with four tiles to a side 19.8.
 W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = (N + 15) / 16, tiles = (K + 127) / 128;
   W4a16Plan p{1, 1, 1};
@@ -479,8 +479,8 @@ W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   p.nb = 2;
   p.mt = M <= 32 ? 2 : 4;
   const int64_t groups = (blocks + 2 * kManyWaves - 1) / (2 * kManyWaves) * ((M + 16 * p.mt - 1) / (16 * p.mt));
-  int64_t parts = (256 + groups - 1) / groups;
-  const int64_t most = tiles / 8;
+  int64_t parts = 256 / groups;
+  const int64_t most = tiles / kManySides;
   parts = parts < most ? parts : most;
   p.parts = static_cast<int>(parts < 1 ? 1 : parts);
   return p;
