@@ -122,12 +122,14 @@ __device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part,
 // from the caches itself (rows past M repeat the last one and are not stored).
 // All loads of U tiles are issued before the first is used; at 8 x 4096 -> 28672 a
 // ring of single tiles instead took 23 us for 17.5, loads that bypass the caches 23,
-// and registers for one workgroup a compute unit only 17.4 for 15.7.
+// and registers for one workgroup a compute unit only 17.4 for 15.7.  (With 16 or 32
+// channels a workgroup has a compute unit to itself, and four tiles at a time take
+// the registers of two: 8 x 4096 -> 8192 8.2 us with two, 7.8 with four.)
 template <bool XF16, int NB, int GROUPS>
-__global__ void __launch_bounds__(kWaves * 64, XF16 && GROUPS != HALVES ? 4 : 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
+__global__ void __launch_bounds__(kWaves * 64, NB == 4 && XF16 && GROUPS != HALVES ? 4 : 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
   constexpr int XV = XF16 ? 1 : 2;                   // 16 bytes of x to eight elements
-  constexpr int U = NB == 1 && XF16 ? 4 : 2;         // tiles of each block of channels on their way together
+  constexpr int U = NB <= 2 && XF16 ? 4 : 2;         // tiles of each block of channels on their way together
   constexpr int SL = GROUPS == WHOLE ? 1 : U * HALF / 4 < 1 ? 1 : U * HALF / 4;  // loads of their scales
   __shared__ f4 lds[kWaves][NB][64];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
