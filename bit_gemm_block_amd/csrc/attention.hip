@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(256) attention_join_rows_kernel(AttentionArgs 
     for (int k = 0; k < here; k += kGroups) {
       const int mine = k + grp < here ? k + grp : here - 1;
       const f4 v = *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + mine)) + 4 * c);
-      o += (k + grp < here ? __shfl(f, mine) : 0.f) * v;
+      const float weight = __shfl(f, mine);  // by all lanes: one that is switched off gives none
+      o += (k + grp < here ? weight : 0.f) * v;
     }
   }
 #pragma unroll
