@@ -293,13 +293,17 @@ __device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const
     }
   };
   weigh();
-  if (__any(top > 16384.f || sum > 1.15292150e18f)) {
+  int far = top > 16384.f || sum > 1.15292150e18f;
+  if (__any(far)) {
+    // Of this row: others, which may be of other sequences, leave it as it is.
+    far |= __shfl_xor(far, 16);
+    far |= __shfl_xor(far, 32);
     float u = kUnset;
 #pragma unroll
     for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[i], exponent(vs[i])));
     u = fmaxf(u, __shfl_xor(u, 16));
     u = fmaxf(u, __shfl_xor(u, 32));
-    const float moved = fmaxf(s.ref, u - 8.f);
+    const float moved = far ? fmaxf(s.ref, u - 8.f) : s.ref;
     const float f = __builtin_amdgcn_exp2f(s.ref - moved);
     s.ref = moved;
     s.l *= f;
