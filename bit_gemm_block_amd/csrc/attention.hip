@@ -125,19 +125,19 @@ __global__ void __launch_bounds__(256) attention_join_rows_kernel(AttentionArgs 
     float m = fmaxf(top, ref);
 #pragma unroll
     for (int w = 32; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor(m, w));
-    const float back = __builtin_amdgcn_exp2f(top - m);
+    const Lower before(m - top), mine(m - ref);
     top = m;
-    const float f = lane < here ? __builtin_amdgcn_exp2f(ref - m) : 0.f;
-    float add = f * l;
+    const float f = lane < here ? mine.factor() : 0.f;
+    float add = mine.sum(l);
 #pragma unroll
     for (int w = 32; w >= 1; w >>= 1) add += __shfl_xor(add, w);
-    sum = sum * back + add;
-    o *= back;
+    sum = before.sum(sum) + add;
+    o *= before.factor();
 #pragma unroll 4
     for (int k = 0; k < here; k += kGroups) {
-      const int mine = k + grp < here ? k + grp : here - 1;
-      const f4 v = *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + mine)) + 4 * c);
-      const float weight = __shfl(f, mine);  // by all lanes: one that is switched off gives none
+      const int at = k + grp < here ? k + grp : here - 1;
+      const f4 v = *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + at)) + 4 * c);
+      const float weight = __shfl(f, at);  // by all lanes: one that is switched off gives none
       o += (k + grp < here ? weight : 0.f) * v;
     }
   }
@@ -179,17 +179,16 @@ __global__ void __launch_bounds__(256) attention_join_parts_kernel(AttentionArgs
     if (lane == 0) red[wave] = m;
     __syncthreads();
     m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float back = __builtin_amdgcn_exp2f(top - m);
+    const Lower before(m - top), mine(m - ref);
     top = m;
-    const float f = static_cast<int>(threadIdx.x) < here ? __builtin_amdgcn_exp2f(ref - m) : 0.f;
-    weight[threadIdx.x] = f;
-    float add = f * l;
+    weight[threadIdx.x] = static_cast<int>(threadIdx.x) < here ? mine.factor() : 0.f;
+    float add = mine.sum(l);
 #pragma unroll
     for (int w = 32; w >= 1; w >>= 1) add += __shfl_xor(add, w);
     if (lane == 0) red[4 + wave] = add;
     __syncthreads();
-    sum = sum * back + ((red[4] + red[5]) + (red[6] + red[7]));
-    o *= back;
+    sum = before.sum(sum) + ((red[4] + red[5]) + (red[6] + red[7]));
+    o *= before.factor();
 #pragma unroll 4
     for (int k = grp; k < here; k += 32)
       o += weight[k] * *reinterpret_cast<const f4*>(partial.o(a, row_of(a, plan, partial, p, base + k)) + c);

@@ -244,6 +244,16 @@ __device__ __forceinline__ float exponent(float v) {
 
 constexpr float kUnset = -1e30f;  // reference of a row that has seen nothing
 
+// What brings a sum under a reference higher by `by`: 2^-by in two steps.  Where
+// values' sizes differ by 2^126 and more that is no number of its own, but a sum
+// of weights under the lower reference may stand as high.
+struct Lower {
+  float half;
+  __device__ __forceinline__ explicit Lower(float by) : half(__builtin_amdgcn_exp2f(-0.5f * by)) {}
+  __device__ __forceinline__ float sum(float l) const { return l * half * half; }
+  __device__ __forceinline__ float factor() const { return half * half; }
+};
+
 // What a row of lane (r, g) has gathered: lanes of one r share ref, and hold
 // their own tokens' part of l and their channels of O.
 template <int NV>
@@ -304,11 +314,11 @@ __device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const
     u = fmaxf(u, __shfl_xor(u, 16));
     u = fmaxf(u, __shfl_xor(u, 32));
     const float moved = far ? fmaxf(s.ref, u - 8.f) : s.ref;
-    const float f = __builtin_amdgcn_exp2f(s.ref - moved);
+    const Lower lower(moved - s.ref);
     s.ref = moved;
-    s.l *= f;
+    s.l = lower.sum(s.l);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) s.o[j] *= f;
+    for (int j = 0; j < NV; ++j) s.o[j] *= lower.factor();
     weigh();
   }
   s.l += sum;
@@ -654,8 +664,9 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
   for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, lds.stat[k][r][0]);
 #pragma unroll
   for (int k = 0; k < kAttnWaves; ++k) {
-    f[k] = __builtin_amdgcn_exp2f(lds.stat[k][r][0] - top);
-    l += f[k] * lds.stat[k][r][1];
+    const Lower lower(top - lds.stat[k][r][0]);
+    f[k] = lower.factor();
+    l += lower.sum(lds.stat[k][r][1]);
   }
   // Channels of this wave: its quarter of each lane's NV (i, 0 .. NV - 1).
   constexpr int Q4 = NV / 4;
