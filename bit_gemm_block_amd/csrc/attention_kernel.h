@@ -303,11 +303,11 @@ __device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const
     }
   };
   weigh();
-  int far = top > 16384.f || sum > 1.15292150e18f;
-  if (__any(far)) {
+  const uint64_t lanes = __ballot(top > 16384.f || sum > 1.15292150e18f);
+  if (lanes) {
     // Of this row: others, which may be of other sequences, leave it as it is.
-    far |= __shfl_xor(far, 16);
-    far |= __shfl_xor(far, 32);
+    const uint32_t pairs = static_cast<uint32_t>(lanes | lanes >> 32);
+    const bool far = ((pairs | pairs >> 16) >> (threadIdx.x & 15) & 1) != 0;
     float u = kUnset;
 #pragma unroll
     for (int i = 0; i < 8; ++i) u = fmaxf(u, fmaf(x[i], kc[i], exponent(vs[i])));
