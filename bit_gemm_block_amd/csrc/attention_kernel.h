@@ -242,7 +242,7 @@ __device__ __forceinline__ float exponent(float v) {
   return fabsf(v) > 8.6736174e-19f ? static_cast<float>(e) : -60.f;
 }
 
-constexpr float kUnset = -1e30f;  // reference of a row that has seen nothing
+constexpr float kUnset = -__FLT_MAX__;  // reference of a row that has seen nothing: below any score
 
 // What brings a sum under a reference higher by `by`: 2^-by in two steps.  Where
 // values' sizes differ by 2^126 and more that is no number of its own, but a sum

@@ -145,8 +145,10 @@ size_t w4a4_cache_attention_workspace_size(const w4a4_cache* cache, int64_t toke
  *   the probability times the value's scale as such a pair too (off by 2^-22 of
  *   itself or 2^-33 of the row's largest); a score's products are cut at 2^-22
  *   of the largest of 32 channels.  What masked positions hold has no effect.
- *   |scale| times a row's largest query is below 2^115, the values' scales are
- *   below 2^100 (in a row where they are not, infinities and NaN may come out).
+ *   Ranges: |scale| times a row's largest query below 2^115, the sum of a score's
+ *   |scale q k| below 2^120 (where a score passes 2^26, with values' scales below
+ *   2^14), values' scales below 2^100.  In a row outside them infinities, NaN and
+ *   zeros may come out.
  *   A row's result depends on its own sequence and the prefix only (the
  *   call's sizes and the lengths choose the order of its sums) and is the
  *   same from call to call.

@@ -1,7 +1,7 @@
 """cache_attention at the ends of float32's range, on the GPU: values of very
-different sizes among tokens of like scores.
+different sizes among tokens of like scores, and scores far below zero.
 
-Bar: scores that are equal are equal as they are computed, so that every
+Bar of both: scores that are equal are equal as they are computed, so that every
 weight is the same, and exact; what is left of the bar in test_gpu_attention.py
 are the weights' pair, 2^-20, and the sums, 8 u (tokens / 32 + 64), of sum p |v|,
 and a weight's cut-off, 2^-33 of the row's largest for each token.
@@ -73,3 +73,24 @@ def test_large_values_among_zeros(bits, n, large):
                 kw.update(prefix_table=rest[:20], prefix_length=601)
             got, ref, tol = run((k, v), ks, vs, bits, tables, lengths, q, **kw)
             assert np.all(np.abs(got - ref) <= tol), (small, where, float(np.max(np.abs(got - ref) / tol)))
+
+
+@pytest.mark.parametrize("size", [90, 100, 112])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_scores_far_below_zero(n, size):
+    # All scores are -2^size: weights alike, as at any other score.
+    print("attention low scores", n, size, flush=True)
+    heads, group, dim, page = 1, 4, 64, 32
+    rng = np.random.default_rng(size)
+    k = np.zeros((70, heads, page, dim), np.int64)
+    k[..., 0] = 1
+    v = rng.integers(-7, 8, k.shape)
+    ks = np.ones((70, heads, page), np.float32)
+    vs = (2.0 ** rng.integers(-4, 5, ks.shape)).astype(np.float32)
+    q = np.zeros((3 * n, group * dim), np.float32)
+    q[:, ::dim] = -(2.0 ** size)
+    lengths = [700, 333, 64]
+    tables, rest = tables_of(70, lengths, page, rng)
+    for kw in ({}, dict(prefix_table=rest[:20], prefix_length=601)):
+        got, ref, tol = run((k, v), ks, vs, 4, tables, lengths, q, q_start=np.arange(4) * n, max_q=n, scale=1.0, **kw)
+        assert np.all(np.abs(got - ref) <= tol), float(np.max(np.abs(got - ref) / tol))
