@@ -69,10 +69,12 @@ __device__ __forceinline__ bool parts_of_row(const AttentionArgs& a, const Atten
                                              uint32_t id, Parts* p) {
   const uint32_t at = id / static_cast<uint32_t>(a.q_heads);
   p->head = id - at * a.q_heads;
-  const int s = at / static_cast<uint32_t>(a.max_q);
-  p->query = at - s * a.max_q;
+  const int s = plan.join_by_place ? at / static_cast<uint32_t>(a.max_q)
+                                   : first_above(a, at, [](int, int q) { return q; });
+  if (s >= a.seqs) return false;
   const Span span = own_span(a, s);
-  if (p->query >= span.n) return false;
+  p->query = at - (plan.join_by_place ? s * a.max_q : span.first);
+  if (p->query < 0 || p->query >= span.n || p->query >= a.max_q) return false;
   p->own_first = partial.slots(a, s)[0];
   p->own = p->n = partial.slots(a, s)[1];
   p->front_first = 0;
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) attention_join_parts_kernel(AttentionArgs
 
 template <int D>
 void launch_join(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t st) {
-  const uint32_t rows = static_cast<uint32_t>(a.seqs) * a.max_q * a.q_heads;  // below 2^24
+  const uint32_t rows = static_cast<uint32_t>(plan.join_queries) * a.q_heads;  // below 2^24
   // Few rows have lanes enough only if a row's channels and parts are spread (32
   // rows of 63 parts: 14.8 us with the attention, one wave to a row 26.2; 128
   // rows 18.5, 20.8; 512 rows 31.0, 29.1; 2048 rows 77.5, 68.7).
@@ -227,6 +229,8 @@ bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
   AttentionCut& own = plan->own;
   AttentionCut& front = plan->front;
   own = cut_tokens(own_rows, a.seqs, a.heads, a.width << a.page_log2, a.D, false);
+  const int64_t through = (front_rows >> 6) + a.seqs;
+  if (own.rowsplit && through < static_cast<int64_t>(a.seqs) * own.groups.d && through < kGrid) own.places = static_cast<int>(through);
   const int64_t cap = a.width << a.page_log2;
   const bool split = own.rowsplit ? own.parts.d > 1 : cap > int64_t{1} << own.piece_log2;
   plan->join = split || a.prefix_width > 0;
@@ -236,8 +240,13 @@ bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
     front = cut_tokens(front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D, !own.rowsplit);
     plan->front_slots = front.rowsplit ? front.parts.d : front.groups.d;
   }
+  // No more queries than rows of q, and than max_q of every sequence.
+  const int64_t places = static_cast<int64_t>(a.seqs) * a.max_q;
+  plan->join_by_place = places <= a.tokens;
+  const int64_t queries = least64(places, a.tokens);
+  plan->join_queries = static_cast<int>(queries);
   return cut_blocks(a, own, a.seqs) + (a.prefix_width > 0 ? cut_blocks(a, front, 1) : 0) < kGrid &&
-         static_cast<int64_t>(a.seqs) * a.max_q * a.q_heads < kGrid;
+         queries * a.q_heads < kGrid;
 }
 
 size_t attention_workspace(const AttentionArgs& a, const AttentionPlan& plan) {

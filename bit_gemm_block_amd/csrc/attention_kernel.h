@@ -95,6 +95,32 @@ __device__ __forceinline__ Span front_span(const AttentionArgs& a) {
   return p;
 }
 
+// The first sequence s for which bound(s + 1, q_start[s + 1]), which ascends, is
+// above `target`; the number of sequences where none is.  64 of them at a time, by
+// all lanes of a wave.
+template <typename F>
+__device__ __forceinline__ int first_above(const AttentionArgs& a, int target, F bound) {
+  const int lane = threadIdx.x & 63;
+  int first = 0, n = a.seqs;
+  for (;;) {
+    const int stride = (n + 63) >> 6;
+    const int reach = (lane + 1) * stride;
+    const int k = first + (reach < n ? reach : n);
+    int q = a.q_start[k];
+    q = q < 0 ? 0 : q < a.tokens ? q : a.tokens;
+    const int below = __builtin_popcountll(__ballot(reach - stride < n && bound(k, q) <= target)) * stride;
+    if (stride <= 1 || below >= n) return first + (below < n ? below : n);
+    first += below;
+    n = n - below < stride ? n - below : stride;
+  }
+}
+// Row groups numbered through: those of sequence s begin at 64ths(q_start[s] group)
+// + s.  64ths of a sum are no fewer than those of its parts, so that its n group
+// rows have the 64ths(n group) + 1 places that they may need.
+__device__ __forceinline__ int place_of(const AttentionArgs& a, int s, int q) {
+  return static_cast<int>(static_cast<uint32_t>(q) * a.group.d >> 6) + s;
+}
+
 // Bytes E and F of w (unsigned codes u = q + 128) as fp16, minus 128.
 template <int SEL>
 __device__ __forceinline__ h2 two_bytes(uint32_t w1, uint32_t w0) {
@@ -789,13 +815,25 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
   // together; late row groups, which see most, first.
   uint32_t id = a.by_heads.quotient(place);
   const int h = place - id * a.heads;
-  uint32_t rest = cut.groups.quotient(id);
-  const int rg = cut.groups.d - 1 - (id - rest * cut.groups.d);
-  const uint32_t seqs = front ? 1 : a.seqs;
-  const int part = rest / seqs, s = rest - part * seqs;
+  int part, s, rg;
+  const bool through = !front && cut.places;
+  if (through) {
+    part = id / static_cast<uint32_t>(cut.places);
+    const int at = id - part * cut.places;
+    s = __builtin_amdgcn_readfirstlane(first_above(a, at, [&](int k, int q) { return place_of(a, k, q); }));
+    if (s >= a.seqs) return;
+    rg = at;  // from its sequence's first on, below
+  } else {
+    const uint32_t rest = cut.groups.quotient(id);
+    rg = cut.groups.d - 1 - (id - rest * cut.groups.d);
+    const uint32_t seqs = front ? 1 : a.seqs;
+    part = rest / seqs;
+    s = rest - part * seqs;
+  }
   const Pages table(a, s, front);
   const Span span = front ? front_span(a) : own_span(a, s);
-  if (rg * kGroupRows >= span.rows) return;
+  if (through) rg = (span.rows + kGroupRows - 1) / kGroupRows - 1 - (rg - place_of(a, s, span.first));
+  if (rg < 0 || rg * kGroupRows >= span.rows) return;
   const int parts = parts_of(span.length, cut);
   if (part >= parts) return;
   if (plan.join && part == 0 && rg == 0 && h == 0 && threadIdx.x == 0) {
@@ -994,7 +1032,8 @@ __global__ void __launch_bounds__(kAttnWaves * 64, rows_resident(D, BITS, PAIR))
 
 // Workgroups of a cut.
 inline int64_t cut_blocks(const AttentionArgs& a, const AttentionCut& c, int64_t seqs) {
-  return a.heads * (c.rowsplit ? seqs * c.groups.d * c.parts.d : static_cast<int64_t>(c.groups.d));
+  if (!c.rowsplit) return a.heads * static_cast<int64_t>(c.groups.d);
+  return a.heads * (c.places ? c.places : seqs * c.groups.d) * c.parts.d;
 }
 
 template <int D, int BITS, bool PAIR>

@@ -66,7 +66,8 @@ int attention_sizes(const w4a4_cache* c, int64_t tokens, int64_t q_heads, int64_
   if (tokens < 0 || q_heads <= 0 || seqs < 0 || width < 0 || max_q <= 0 || prefix_width < 0)
     return W4A4_ERR_INVALID_ARG;
   if (q_heads % c->heads != 0) return W4A4_ERR_INVALID_ARG;
-  if (q_heads > 65536 || tokens > INT32_MAX / q_heads || seqs > INT32_MAX / q_heads || max_q > INT32_MAX / q_heads ||
+  max_q = max_q < tokens ? max_q : tokens > 0 ? tokens : 1;  // a sequence has no more queries than there are
+  if (q_heads > 65536 || tokens > INT32_MAX / q_heads || seqs > INT32_MAX / q_heads ||
       width > kMaxTokens / c->page_size || prefix_width > kMaxTokens / c->page_size)
     return W4A4_ERR_UNSUPPORTED;
   a->pages = static_cast<int>(c->pages); a->heads = static_cast<int>(c->heads);
@@ -75,8 +76,7 @@ int attention_sizes(const w4a4_cache* c, int64_t tokens, int64_t q_heads, int64_
   a->group = w4a4::Divisor(static_cast<uint32_t>(q_heads / c->heads));
   a->by_heads = w4a4::Divisor(static_cast<uint32_t>(c->heads));
   a->seqs = static_cast<int>(seqs); a->width = width;
-  // A sequence has no more queries than there are.
-  a->max_q = static_cast<int>(max_q < tokens ? max_q : tokens > 0 ? tokens : 1);
+  a->max_q = static_cast<int>(max_q);
   a->prefix_width = prefix_width;
   return w4a4::attention_plan(*a, plan) ? W4A4_OK : W4A4_ERR_UNSUPPORTED;
 }

@@ -94,18 +94,23 @@ struct AttentionArgs {
 // waves sharing the tokens.  Tokens come in pieces of 2^piece_log2, and each of
 // `groups` workgroups of a head takes an equal run of the pieces of all
 // sequences (`groups` ones of the prefix).
-// Many rows: it takes 64, a wave's 16 its own; `groups` is the row groups of a
-// sequence (or of all queries), and their tokens are cut into up to `parts`
-// equal parts of 2^piece_log2 or more.
+// Many rows: it takes 64, a wave's 16 its own; `groups` is the row groups that a
+// sequence (or all queries) can have, and their tokens are cut into up to
+// `parts` equal parts of 2^piece_log2 or more.  Where sequences have far fewer
+// queries than the longest, `places` row groups are numbered through over the
+// queries there are (attention_kernel.h), else it is 0.
 struct AttentionCut {
   int rowsplit, piece_log2;
   int one_piece;  // few rows: a workgroup of a head for every piece there can be
   Divisor groups;
   Divisor parts;
+  int places;
 };
 struct AttentionPlan {
   AttentionCut own, front;
   int join;                  // partial results are joined by another launch
+  int join_queries;          // of so many queries: all of q, or
+  int join_by_place;         // max_q of every sequence
   int64_t own_slots;         // [own_slots][rows of a slot]: few rows: the runs' sections, many: the parts
   int64_t front_slots;
 };

@@ -137,6 +137,10 @@ size_t w4a4_cache_attention_workspace_size(const w4a4_cache* cache, int64_t toke
  *           front of all sequences, and its length (taken between 0 and
  *           prefix_width * page_size); every query sees all of it.  NULL and
  *           0: none.
+ *   Sizes: q_heads at most 65536; table_width and prefix_width times page_size at
+ *   most 2^30; tokens, and seqs, times q_heads below 2^31, seqs times heads below
+ *   2^23, and the lesser of tokens and seqs times max_q, times q_heads, below 2^24
+ *   (262144 queries of 64 heads); what is beyond is W4A4_ERR_UNSUPPORTED.
  *   Rows of q that belong to no sequence are not read, and those of out are
  *   left as they are.  A query that sees nothing gets zeros.
  *   Scores and sums are float32: codes are exact, queries enter under a power
