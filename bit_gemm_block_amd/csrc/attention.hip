@@ -17,8 +17,9 @@ namespace {
 
 constexpr int64_t kGrid = 1 << 24;   // workgroups of 256 threads: below 2^32 threads
 
-// `beside`: a prefix whose workgroups run beside those of the own tokens.
-AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capacity, int D, bool beside) {
+// rows: of a sequence, at most; all: of the call.  `beside`: a prefix whose
+// workgroups run beside those of the own tokens.
+AttentionCut cut_tokens(int64_t rows, int64_t all, int64_t seqs, int64_t heads, int64_t capacity, int D, bool beside) {
   AttentionCut c{};
   // One tile of rows: waves share it and take tokens each (16 rows of 64 sequences
   // of up to 1024 tokens: 28.7 us, by rows 32.3; of 16 up to 2048: 19.5, 31.0).
@@ -49,10 +50,17 @@ AttentionCut cut_tokens(int64_t rows, int64_t seqs, int64_t heads, int64_t capac
   // drafts of 7 behind up to 4474: 24 and 41), but for a prefix only one to a
   // compute unit, since own tokens share the chip (64 sequences on a prefix of
   // 8192: 38 us with 256, 45 with 512, 50 with 1024).
-  const int64_t units = seqs * heads * groups;
+  // And there are fewer parts the more row groups there are, down to one, so that
+  // partial results are bounded by the chip and not by the queries: eight rounds of
+  // what fits at once (a prompt of 8192 queries, 8 heads x 4 of 128: 806 us without
+  // any, with 8 parts 1270 and 1.1 GB; of 4096 307, 342; 63 single queries of up to
+  // 16384 tokens beside 2048 492, 440, beside 512 295, 290; with four rounds 96
+  // sequences of group 20, one of 9000 tokens, 87 for 59).
+  const int64_t units = seqs * heads * groups, through = all / kGroupRows + seqs;
+  if (through < seqs * groups && through < kGrid) c.places = static_cast<int>(through);
   c.piece_log2 = units < 256 ? 8 : 10;
   int64_t parts = units < resident ? ((beside ? 256 : resident) + units - 1) / units : 8;
-  const int64_t most = capacity >> c.piece_log2;
+  const int64_t most = least64(capacity >> c.piece_log2, 8 * resident / (c.places ? heads * c.places : units));
   parts = parts < most ? parts : most;
   c.parts = Divisor(static_cast<uint32_t>(parts < 1 ? 1 : parts));
   return c;
@@ -228,16 +236,14 @@ bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
   *plan = AttentionPlan{};
   AttentionCut& own = plan->own;
   AttentionCut& front = plan->front;
-  own = cut_tokens(own_rows, a.seqs, a.heads, a.width << a.page_log2, a.D, false);
-  const int64_t through = (front_rows >> 6) + a.seqs;
-  if (own.rowsplit && through < static_cast<int64_t>(a.seqs) * own.groups.d && through < kGrid) own.places = static_cast<int>(through);
+  own = cut_tokens(own_rows, front_rows, a.seqs, a.heads, a.width << a.page_log2, a.D, false);
   const int64_t cap = a.width << a.page_log2;
   const bool split = own.rowsplit ? own.parts.d > 1 : cap > int64_t{1} << own.piece_log2;
   plan->join = split || a.prefix_width > 0;
   // Few rows: run w of sequence s is slot w + s.
   if (plan->join) plan->own_slots = own.rowsplit ? own.parts.d : static_cast<int64_t>(own.groups.d) + a.seqs;
   if (a.prefix_width > 0) {
-    front = cut_tokens(front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D, !own.rowsplit);
+    front = cut_tokens(front_rows, front_rows, 1, a.heads, a.prefix_width << a.page_log2, a.D, !own.rowsplit);
     plan->front_slots = front.rowsplit ? front.parts.d : front.groups.d;
   }
   // No more queries than rows of q, and than max_q of every sequence.

@@ -49,6 +49,21 @@ def test_sizes_that_are_refused(T, q_heads, S, width, max_q):
     assert size_and_status(T, q_heads, S, width, max_q) == (0, W.ERR_UNSUPPORTED)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("S", [1, 3, 64])
+def test_workspace_is_bounded_by_the_chip(dim, S):
+    # Many rows: partial results of eight rounds of 768 workgroups of 64 rows, at
+    # most, however long the prompts.
+    largest = 8 * 768 * 64 * (dim + 2) * 4 + (S + 1) * 8
+    for q_heads in (8, 32, 56):
+        for n in (17, 100, 1000, 2048, 4096, 5000, 8192, 16384):
+            if n * S * q_heads < 1 << 24:
+                c = ctypes.byref(D.CacheStruct(P, P, P, P, 1 << 20, 8, 64, dim, 4))
+                for T in {n * S, n + S - 1}:     # all as long, or one
+                    need = D.lib().w4a4_cache_attention_workspace_size(c, T, q_heads, S, 512, n, 0)
+                    assert need <= largest, (q_heads, n, T, need)
+
+
 def mixed(counts, lengths, heads, group, dim, bits, dt, width, seed, spare=3, **kw):
     start = np.concatenate(([0], np.cumsum(counts)))
     page = 32
