@@ -60,6 +60,12 @@ bool rows_fit(const w4a4_cache* c, int64_t T) {
   return T <= ((int64_t{1} << 32) - 256) / (c->heads * (c->head_dim / 8));
 }
 
+// Rows of N float32 partial sums that a projection of M rows writes.
+int64_t w4a16_partial_rows(int64_t M, int64_t N, int64_t K) {
+  const int parts = w4a4::w4a16_plan(M, N, K).parts;
+  return parts > 1 ? parts * M : 0;
+}
+
 // Sizes of an attention call that its plan depends on.
 int attention_sizes(const w4a4_cache* c, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t width, int64_t max_q,
                     int64_t prefix_width, w4a4::AttentionArgs* a, w4a4::AttentionPlan* plan) {
@@ -87,8 +93,15 @@ extern "C" {
 
 size_t w4a16_qlinear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  const w4a4::W4a16Plan p = w4a4::w4a16_plan(M, N, K);
-  return p.parts > 1 ? static_cast<size_t>(p.parts) * static_cast<size_t>(M) * static_cast<size_t>(N) * 4 : 0;
+  // The most that M rows or fewer write: 64 rows may be cut into twice the parts of
+  // 65.  With more 64s of rows there are no more parts.
+  int64_t most = 0;
+  for (int64_t m = 64;; m += 64) {
+    const int64_t rows = w4a16_partial_rows(m < M ? m : M, N, K);
+    most = rows > most ? rows : most;
+    if (m >= M || rows == 0) break;
+  }
+  return static_cast<size_t>(most) * static_cast<size_t>(N) * 4;
 }
 
 int w4a16_qlinear_forward(const void* x, int x_dtype, int64_t ldx, const uint8_t* wq, int w_layout,
@@ -103,7 +116,7 @@ int w4a16_qlinear_forward(const void* x, int x_dtype, int64_t ldx, const uint8_t
       (w_group > 0 && K % w_group != 0) || M > kMaxM || N > kMaxN)
     return W4A4_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return W4A4_OK;
-  const size_t need = w4a16_qlinear_workspace_size(M, N, K);
+  const size_t need = static_cast<size_t>(w4a16_partial_rows(M, N, K)) * static_cast<size_t>(N) * 4;
   if (!x || !wq || !w_scale || !y || (need > 0 && !workspace)) return W4A4_ERR_INVALID_ARG;
   if (!aligned(x, 16) || (M > 1 && static_cast<uintptr_t>(ldx) * esize(x_dtype) % 16 != 0) || !aligned(wq, 16) ||
       !aligned(w_scale, 16) || !aligned(y, esize(y_dtype)) || !aligned(workspace, 16))

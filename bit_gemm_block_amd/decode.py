@@ -82,7 +82,7 @@ def qlinear_w4a16_workspace_size(M: int, N: int, K: int) -> int:
 
 
 def qlinear_w4a16_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
-    """A workspace for qlinear_w4a16 calls of these sizes (contents unspecified)."""
+    """A workspace for qlinear_w4a16 calls of up to M rows (contents unspecified)."""
     return torch.empty((max(qlinear_w4a16_workspace_size(M, N, K), 1),), dtype=torch.uint8, device=device)
 
 
@@ -159,7 +159,8 @@ def cache_attention_workspace_size(cache: KVCache, tokens: int, q_heads: int, se
 
 def cache_attention_workspace(cache: KVCache, tokens: int, q_heads: int, seqs: int, table_width: int, max_q: int = 1,
                               prefix_width: int = 0) -> torch.Tensor:
-    """A workspace for cache_attention calls of these sizes (contents unspecified)."""
+    """A workspace for cache_attention calls of these sizes (contents unspecified).
+    Smaller sizes may need a larger one."""
     n = cache_attention_workspace_size(cache, tokens, q_heads, seqs, table_width, max_q, prefix_width)
     return torch.empty((max(n, 1),), dtype=torch.uint8, device=cache.k.device)
 

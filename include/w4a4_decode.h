@@ -28,7 +28,7 @@
 extern "C" {
 #endif
 
-/* Bytes of workspace w4a16_qlinear_forward needs for these sizes (0 if it
+/* Bytes of workspace w4a16_qlinear_forward needs for up to M rows (0 if it
  * needs none or a size is 0 or negative).  Calls that share one workspace
  * must not overlap in time. */
 size_t w4a16_qlinear_workspace_size(int64_t M, int64_t N, int64_t K);
@@ -109,7 +109,8 @@ int w4a4_cache_read(const w4a4_cache* cache, const int32_t* slots, int64_t T, vo
                     void* v, int64_t ldv, int dtype, void* stream);
 
 /* Bytes of workspace w4a4_cache_attention needs for these sizes (0 if it
- * needs none or a size is outside its limits).  Calls that share one
+ * needs none or a size is outside its limits).  Smaller sizes may need more: a
+ * workspace for several sizes has the largest of theirs.  Calls that share one
  * workspace must not overlap in time. */
 size_t w4a4_cache_attention_workspace_size(const w4a4_cache* cache, int64_t tokens, int64_t q_heads,
                                            int64_t seqs, int64_t table_width, int64_t max_q,
