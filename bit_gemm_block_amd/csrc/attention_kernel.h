@@ -14,7 +14,7 @@
 // registers as they come from memory: K's words hold eight channels of one
 // token, V's of two tokens are paired by halves first.  A query is brought under
 // a power of two of its row; a float32 one is a pair hi + lo of fp16 there, and
-// so is w, so that no more than 2^-22 of either is lost.  (A single fp16 w would
+// so is w, so that no more than 2^-23 of either is lost.  (A single fp16 w would
 // save an eighth of the many-row kernel's instructions and lose 2^-11 of every
 // weight.)  All other numbers are float32.
 //
@@ -121,15 +121,11 @@ __device__ __forceinline__ int place_of(const AttentionArgs& a, int s, int q) {
   return static_cast<int>(static_cast<uint32_t>(q) * a.group.d >> 6) + s;
 }
 
-// Bytes E and F of w (unsigned codes u = q + 128) as fp16, minus 128.
-template <int SEL>
-__device__ __forceinline__ h2 two_bytes(uint32_t w1, uint32_t w0) {
-  union {
-    uint32_t u;
-    h2 h;
-  } v;
-  v.u = __builtin_amdgcn_perm(w1, w0, SEL) | 0x64006400u;
-  return v.h - h2{1152.f16, 1152.f16};
+// Bytes 0 and 1, or 2 and 3, of w (unsigned codes u = q + 128) as fp16, minus 128.
+template <bool UPPER>
+__device__ __forceinline__ h2 two_bytes(uint32_t w) {
+  const h2 off = {1152.f16, 1152.f16};
+  return __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, UPPER ? 0x04030402u : 0x04010400u)) - off;
 }
 
 // A step's codes as a lane holds them: of the keys, its share of token r of both
@@ -195,26 +191,30 @@ __device__ __forceinline__ void load_scales(const float* s, const int64_t* rb, u
     d[h] = *reinterpret_cast<const f4*>(s + rb[h] + 4 * g);
 }
 
-// K's codes 8 j to 8 j + 7 of a lane, unsigned, as fp16 subnormal numbers u 2^-20
-// (4 bits, in the order 0 4 1 5 2 6 3 7) or u 2^-24 (8 bits): the bits of a small
-// whole number are that times 2^-24.  Their offset, 8 or 128, is taken out of the
-// product by its starting value.  The instruction aligns products by the exponent
-// that subnormals share, 2^-14, and cuts what falls behind: codes stand high in
-// their ten bits (4-bit codes as u 2^-24 cost five bits of the scores).
-template <int BITS>
+// K's codes 8 j to 8 j + 7 of a lane as fp16 (4 bits in the order 0 4 1 5 2 6 3 7).
+// WHOLE: the whole numbers that they are.
+// Else, of 4 bits, unsigned, as subnormal numbers u 2^-20, two fewer instructions
+// for two codes: the bits of a small whole number are that times 2^-24.  Their
+// offset of 8 is taken out of the product by its starting value.  The instruction
+// aligns products by the exponent that subnormals share, 2^-14, and cuts what falls
+// behind: codes stand high in their ten bits (as u 2^-24 they cost five bits of the
+// scores), and 8 bits have no room to.
+template <int BITS, bool WHOLE>
 __device__ __forceinline__ h8 key_operand(const uint32_t* k, int j, const Masks& m) {
   Operand o;
-  if constexpr (BITS == 4) {
+  if constexpr (BITS == 4 && WHOLE) {
+    o = int4_to_f16(k[j], m);
+  } else if constexpr (BITS == 4) {
     o.w[0] = ((k[j] << 4) & m.odd) ^ m.key;
     o.w[1] = (k[j] & m.odd) ^ m.key;
     o.w[2] = ((k[j] >> 4) & m.odd) ^ m.key;
     o.w[3] = ((k[j] >> 8) & m.odd) ^ m.key;
   } else {
     const uint32_t a = k[2 * j] ^ 0x80808080u, b = k[2 * j + 1] ^ 0x80808080u;
-    o.w[0] = __builtin_amdgcn_perm(a, a, 0x0c010c00);
-    o.w[1] = __builtin_amdgcn_perm(a, a, 0x0c030c02);
-    o.w[2] = __builtin_amdgcn_perm(b, b, 0x0c010c00);
-    o.w[3] = __builtin_amdgcn_perm(b, b, 0x0c030c02);
+    o.p[0] = two_bytes<false>(a);
+    o.p[1] = two_bytes<true>(a);
+    o.p[2] = two_bytes<false>(b);
+    o.p[3] = two_bytes<true>(b);
   }
   return o.h;
 }
@@ -224,31 +224,32 @@ __device__ constexpr int key_channel(int e) {
   return BITS == 4 ? (e & 1) * 4 + e / 2 : e;
 }
 // What makes scores (over log 2) of products with a query brought up by 2^up.
-template <int BITS>
+template <bool WHOLE>
 __device__ __forceinline__ float score_factor(const AttentionArgs& a, int up) {
-  return ldexpf(a.scale * 1.4426950408889634f, (BITS == 4 ? 20 : 24) - up);
+  return ldexpf(a.scale * 1.4426950408889634f, (WHOLE ? 0 : 20) - up);
 }
 
 // Four channels of a lane's tokens in pairs (four of a step, two of a half), as
-// fp16: channels 4 q to 4 q + 3 of the lane's own.  (An offset of the values cannot wait like the keys': it
-// would be 8 times the sum of the weights, which the result is a small part of.)
+// fp16: channels 4 q to 4 q + 3 of the lane's own.  (An offset of the values cannot
+// wait like the keys': it would be 8 times the sum of the weights, which the result
+// is a small part of.)
 template <int D, int BITS, int PAIRS = 4>
 __device__ __forceinline__ void value_operands(const uint32_t* v, int q, const Masks& m, Operand* o) {
   constexpr int VW = Row<D, BITS>::kValueWords;
 #pragma unroll
   for (int p = 0; p < PAIRS; ++p) {
     const int word = BITS == 4 ? q / 2 : q;
-    uint32_t w0 = v[2 * p * VW + word], w1 = v[(2 * p + 1) * VW + word];
+    const uint32_t w0 = v[2 * p * VW + word], w1 = v[(2 * p + 1) * VW + word];
     if constexpr (BITS == 4) {
       const uint32_t t = __builtin_amdgcn_perm(w1, w0, q % 2 ? 0x07060302u : 0x05040100u);
       nibbles_to_f16(t, m, &o[0].p[p], &o[1].p[p], &o[2].p[p], &o[3].p[p]);
     } else {
-      w0 ^= 0x80808080u;
-      w1 ^= 0x80808080u;
-      o[0].p[p] = two_bytes<0x0c040c00>(w1, w0);
-      o[1].p[p] = two_bytes<0x0c050c01>(w1, w0);
-      o[2].p[p] = two_bytes<0x0c060c02>(w1, w0);
-      o[3].p[p] = two_bytes<0x0c070c03>(w1, w0);
+      const uint32_t lo = __builtin_amdgcn_perm(w1, w0, 0x05010400u) ^ 0x80808080u;  // bytes 0, 0, 1, 1
+      const uint32_t hi = __builtin_amdgcn_perm(w1, w0, 0x07030602u) ^ 0x80808080u;  // 2, 2, 3, 3
+      o[0].p[p] = two_bytes<false>(lo);
+      o[1].p[p] = two_bytes<true>(lo);
+      o[2].p[p] = two_bytes<false>(hi);
+      o[3].p[p] = two_bytes<true>(hi);
     }
   }
 }
@@ -295,7 +296,8 @@ struct RowState {
 };
 
 // The weights of a step from its products sc, the keys' scales times the row's
-// factor, kc, and the values' scales: hi and lo.  With `partly` positions from limit on, and those of absent pages, are not seen.
+// factor, kc, and the values' scales: hi and lo.  With `partly` positions from limit
+// on, and those of absent pages, are not seen.
 template <int NV>
 __device__ __forceinline__ void weigh_step(const f4* sc, const float* kc_, const f4* vs_, bool partly, int limit,
                                            int tok, bool bad0, bool bad1, RowState<NV>& s, Operand* w) {
@@ -430,12 +432,11 @@ __device__ __forceinline__ void query_operands(const Raw8<Q>& x, int up, Operand
     lo->p[e / 2] = remainders(hi->p[e / 2], v0, v1);
   }
 }
-// The codes' offset as an operand: a product with it is what it adds.
-template <int BITS>
+// The offset of 4-bit codes as an operand: a product with it is what it adds.
 __device__ __forceinline__ h8 offset_operand() {
   Operand o;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) o.w[p] = 0x00800080u;  // 128, or 16 times 8
+  for (int p = 0; p < 4; ++p) o.w[p] = 0x00800080u;  // 16 times 8
   return o.h;
 }
 
@@ -581,10 +582,18 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
     load_scales(a.vs, rb, g, vs);
   }
 
+  // With codes as whole numbers a score is one sum over both parts of a query.  With
+  // unsigned ones that sum would be rounded at the size of the offset's, three times
+  // the score's: the two parts are summed apart, the first nearly exact and the
+  // second too small for its roundings to count, and then added (64 sequences of 300
+  // to 16384 tokens, 4 bits: outputs off by 1.2e-6 of themselves in one sum, 3.3e-7 in
+  // two, for 0.8 us of 125).
+  constexpr bool WHOLE = BITS == 8;
+  constexpr int SUMS = WHOLE ? 1 : HALVES;
   // The queries go to LDS as operands, a wave's share of the channels each; c
   // makes scores (over log 2) of the products.
   const int up = query_shift<D>(x);
-  const float c = score_factor<BITS>(a, up);
+  const float c = score_factor<WHOLE>(a, up);
 #pragma unroll
   for (int j = 0; j < NK; ++j) {
     if (j % kAttnWaves != wave) continue;
@@ -596,13 +605,16 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
   __syncthreads();
   auto query_operand = [&](int j, int p) { return __builtin_bit_cast(h8, lds.queries()[j][p][lane]); };
   // The products start from what the codes' offset adds to them, taken off.
-  f4 start = {0.f, 0.f, 0.f, 0.f};
+  f4 start[SUMS];
 #pragma unroll
-  for (int j = 0; j < NK; ++j)
+  for (int p = 0; p < SUMS; ++p) {
+    start[p] = f4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (WHOLE) continue;
 #pragma unroll
-    for (int p = HALVES - 1; p >= 0; --p)
-      start = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), query_operand(j, p), start, 0, 0, 0);
-  start = -start;
+    for (int j = 0; j < NK; ++j)
+      start[p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand(), query_operand(j, p), start[p], 0, 0, 0);
+    start[p] = -start[p];
+  }
 
   RowState<NV> state;
   state.clear();
@@ -618,21 +630,26 @@ __device__ __forceinline__ void tokens_section(const AttentionArgs& a, const Att
     const bool partly = bad0 || bad1 || (step + 1) * kStep > all_see;  // some row does not see some token
 
     asm volatile("" ::: "memory");  // the queries are read again, not kept in registers
-    f4 sc[2];
+    f4 part[SUMS][2];
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
       h8 k[2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS>(keys + half * KW, j, masks);
+      for (int half = 0; half < 2; ++half) k[half] = key_operand<BITS, WHOLE>(keys + half * KW, j, masks);
 #pragma unroll
       for (int p = HALVES - 1; p >= 0; --p) {
         const h8 q = query_operand(j, p);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[half], q, j == 0 && p == HALVES - 1 ? start : sc[half], 0,
-                                                            0, 0);
+        for (int half = 0; half < 2; ++half) {
+          const bool first = j == 0 && (SUMS == HALVES || p == HALVES - 1);
+          f4& d = part[p % SUMS][half];
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[half], q, first ? start[p % SUMS] : d, 0, 0, 0);
+        }
       }
     }
+    f4 sc[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) sc[half] = SUMS == 2 ? part[0][half] + part[SUMS - 1][half] : part[0][half];
     float kc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) kc[i] = ks[i / 4][i % 4] * c;
@@ -885,18 +902,17 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
     }
   }
 
+  constexpr bool WHOLE = BITS == 8 || PAIR;  // as above; the widening is shared, and there are no registers for two sums
   Operand q[NK][HALVES];
   const int up = query_shift<D>(x);
-  const float c = score_factor<BITS>(a, up);
+  const float c = score_factor<WHOLE>(a, up);
   f4 start = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < NK; ++j) {
     Operand lo;
     query_operands<BITS>(x[j], up, &q[j][0], &lo);
     if constexpr (PAIR) q[j][1] = lo;
-#pragma unroll
-    for (int p = HALVES - 1; p >= 0; --p)
-      start = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand<BITS>(), q[j][p].h, start, 0, 0, 0);
+    if constexpr (!WHOLE) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(offset_operand(), q[j][0].h, start, 0, 0, 0);
   }
   start = -start;
   RowState<NV> state;
@@ -909,7 +925,7 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
     __syncthreads();  // the block before is used up
 #pragma unroll
     for (int j = 0; j < NK; ++j)
-      lds.k[mine][half][j][lane] = __builtin_bit_cast(u4, key_operand<BITS>(keys[set], j, masks));
+      lds.k[mine][half][j][lane] = __builtin_bit_cast(u4, key_operand<BITS, WHOLE>(keys[set], j, masks));
 #pragma unroll
     for (int j = 0; j < NV / 4; ++j) {
       Operand v[4];

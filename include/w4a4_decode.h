@@ -147,9 +147,11 @@ size_t w4a4_cache_attention_workspace_size(const w4a4_cache* cache, int64_t toke
  *   Scores and sums are float32: codes are exact, queries enter under a power
  *   of two of their row, fp16 ones as they are (what is below 2^-31 of the
  *   row's largest may be lost) and float32 ones as a pair of fp16 values, and
- *   the probability times the value's scale as such a pair too (off by 2^-22 of
- *   itself or 2^-33 of the row's largest); a score's products are cut at 2^-22
- *   of the largest of 32 channels.  What masked positions hold has no effect.
+ *   the probability times the value's scale as such a pair too (off by 2^-23 of
+ *   itself or 2^-33 of the row's largest); products with 4-bit keys may be cut
+ *   at 2^-22 of the largest of 32 channels.  Float32 outputs are about as close
+ *   as those of the formula in float32 operations.  What masked positions hold
+ *   has no effect.
  *   Ranges: |scale| times a row's largest query below 2^115, the sum of a score's
  *   |scale q k| below 2^120 (where a score passes 2^26, with values' scales below
  *   2^14), values' scales below 2^100.  In a row outside them infinities, NaN and
