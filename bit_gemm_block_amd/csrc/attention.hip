@@ -8,8 +8,9 @@
 // taken in the order of the tokens, the prefix last.
 //
 // The lengths are on the device.  For few rows the workgroups add them up and
-// take equal runs; for many the host cuts by the tables' capacity, and a
-// workgroup whose sequence is shorter ends at once.
+// take equal runs; for many the host cuts by the tables' capacity and the rows
+// there can be, and a workgroup whose sequence is shorter, or has fewer rows, ends
+// at once.
 #include "attention_kernel.h"
 
 namespace w4a4 {
@@ -232,7 +233,8 @@ void launch_join(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t 
 }  // namespace
 
 bool attention_plan(const AttentionArgs& a, AttentionPlan* plan) {
-  const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.group.d, front_rows = static_cast<int64_t>(a.tokens) * a.group.d;
+  const int64_t own_rows = static_cast<int64_t>(a.max_q) * a.group.d;
+  const int64_t front_rows = static_cast<int64_t>(a.tokens) * a.group.d;
   *plan = AttentionPlan{};
   AttentionCut& own = plan->own;
   AttentionCut& front = plan->front;

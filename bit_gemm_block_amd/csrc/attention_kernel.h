@@ -161,7 +161,8 @@ __device__ __forceinline__ void load_half_keys(const AttentionArgs& a, int64_t r
   load_words<X::kKeyWords>(a.k + rb * X::kBytes + (r * X::kBytes + g * (X::kBytes / 4)), k);
 }
 template <int D, int BITS>
-__device__ __forceinline__ void load_half_values(const AttentionArgs& a, int64_t rb, uint32_t r, uint32_t g, uint32_t* v) {
+__device__ __forceinline__ void load_half_values(const AttentionArgs& a, int64_t rb, uint32_t r, uint32_t g,
+                                                 uint32_t* v) {
   using X = Row<D, BITS>;
   const uint8_t* first = a.v + rb * X::kBytes;
 #pragma unroll
@@ -175,12 +176,14 @@ __device__ __forceinline__ void load_half_values(const AttentionArgs& a, int64_t
 }
 // rb: the cache rows of the halves' first tokens.
 template <int D, int BITS>
-__device__ __forceinline__ void load_keys(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* k) {
+__device__ __forceinline__ void load_keys(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g,
+                                          uint32_t* k) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) load_half_keys<D, BITS>(a, rb[h], r, g, k + h * Row<D, BITS>::kKeyWords);
 }
 template <int D, int BITS>
-__device__ __forceinline__ void load_values(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g, uint32_t* v) {
+__device__ __forceinline__ void load_values(const AttentionArgs& a, const int64_t* rb, uint32_t r, uint32_t g,
+                                            uint32_t* v) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) load_half_values<D, BITS>(a, rb[h], r, g, v + h * 4 * Row<D, BITS>::kValueWords);
 }
@@ -453,7 +456,8 @@ struct Partial {
   __device__ __forceinline__ int64_t row(const AttentionArgs& a, const AttentionPlan& p, bool front, int64_t slot,
                                          int64_t token, int query, int head) const {
     const bool by_place = !front && !p.own.rowsplit;
-    return (front ? own_rows : 0) + ((slot * (by_place ? a.max_q : a.tokens) + (by_place ? query : token)) * a.q_heads + head);
+    const int64_t at = slot * (by_place ? a.max_q : a.tokens) + (by_place ? query : token);
+    return (front ? own_rows : 0) + at * a.q_heads + head;
   }
   __device__ __forceinline__ float* o(const AttentionArgs& a, int64_t row) const { return a.partial + row * a.D; }
   __device__ __forceinline__ float* stat(const AttentionArgs& a, int64_t row) const {
@@ -829,7 +833,8 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroup (part, s, rg, h), h fastest, so that those of one length lie
-  // together; late row groups, which see most, first.
+  // together; late row groups, which see most, first.  (s, rg) counts the row groups
+  // that the longest sequence has for each, or those there are.
   uint32_t id = a.by_heads.quotient(place);
   const int h = place - id * a.heads;
   int part, s, rg;
@@ -868,7 +873,8 @@ __device__ __forceinline__ void rows_body(const AttentionArgs& a, const Attentio
   const int all_see = first + 16 <= span.rows ? sight.limit(a.group.quotient(first)) : 0;
   const int limit = row < span.rows ? sight.limit(a.group.quotient(row)) : 0;
   const int steps = (sight.limit(a.group.quotient(group_last)) + kStep - 1) / kStep;
-  const int share = parts == 1 ? steps : static_cast<int>(static_cast<uint32_t>(steps + parts - 1) / static_cast<uint32_t>(parts));
+  const int share =
+      parts == 1 ? steps : static_cast<int>(static_cast<uint32_t>(steps + parts - 1) / static_cast<uint32_t>(parts));
   const int begin = part * share;
   const int end = begin + share < steps ? begin + share : steps;
 

@@ -1,8 +1,9 @@
 // block_binding.cpp — the Python binding of include/w4a4_block.h and
-// include/w4a4_decode.h: checks of the tensors, allocation of the outputs that are not given, and the calls on the
-// tensors' current stream.  No arithmetic.  It is compiled against torch
-// because a call's host time is what a small call costs: through ctypes the
-// marshalling of these argument lists took 5 to 8 us beside the launch's 3.
+// include/w4a4_decode.h: checks of the tensors, allocation of the outputs that are
+// not given, and the calls on the tensors' current stream.  No arithmetic.  It is
+// compiled against torch because a call's host time is what a small call costs:
+// through ctypes the marshalling of these argument lists took 5 to 8 us beside the
+// launch's 3.
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -229,7 +230,8 @@ Tensor qlinear_w4a16(const Tensor& x, const Tensor& wq, const Tensor& w_scale, i
   const int64_t M = x.size(0), K = x.size(1);
   const int64_t ldx = rows(x, "x", dev, M, K);
   const int xd = dtype_of(x.scalar_type()), sd = dtype_of(w_scale.scalar_type());
-  if (w_scale.dim() != (w_group > 0 ? 2 : 1)) throw py::value_error("w_scale must be [N] or, with w_group, [N, K / w_group]");
+  if (w_scale.dim() != (w_group > 0 ? 2 : 1))
+    throw py::value_error("w_scale must be [N] or, with w_group, [N, K / w_group]");
   const int64_t N = w_scale.size(0);
   if (w_group > 0 && K % w_group != 0) throw py::value_error("w_group must divide K");
   const void* sw = w_group > 0 ? whole(w_scale, "w_scale", dev, w_scale.scalar_type(), {N, K / w_group})

@@ -16,10 +16,12 @@
 // with the other half of x zero.
 //
 // What bounds it: the codes' bytes, at 5.2 TB/s of a large copy.  8 x 4096 ->
-// 28672 (61 MB) takes 15.7 us, 3.8 TB/s, against 11.7; one token 4096 -> 6144 (13
-// MB, 2.5 us) 6.2, which is the launch and one way to memory and back; 64 x 14336
-// -> 4096 (31.7 MB, 6.1 us) 20.1: 16 in the product, whose tiles of x, 16 KB
-// beside 8 KB of codes, each wait for a barrier, and 4 in the parts' sum.
+// 28672 (61 MB) takes 15.4 us, 4.0 TB/s, against 11.7; one token 4096 -> 6144 (13
+// MB, 2.5 us) 5.7, which is the launch and one way to memory and back; 64 x 14336
+// -> 4096 (31.7 MB, 6.1 us) 18.2: 15 in the product, whose tiles of x, 16 KB
+// beside 8 KB of codes, each wait for a barrier, and 3 in the parts' sum.  float32
+// x, with three matrix instructions for one and its parts to be made, takes 24.8
+// and 37.8 us at the two larger sizes, with one scale a channel.
 #include "decode_internal.h"
 #include "gemm_common.h"
 #include "int4_operands.h"
@@ -65,7 +67,8 @@ __device__ __forceinline__ uint32_t load_scales(const W4a16Args& a, const Channe
   if constexpr (GROUPS == HALVES) end = end < a.K / 64 ? end : a.K / 64;  // K may end in the middle of the last tile
   at = at < end ? at : end - 1;
   const uint32_t s = ch.scale_off + a.group_halves.quotient(GROUPS == HALVES ? at : 2 * at);
-  return a.sw_f16 ? (static_cast<const uint16_t*>(a.sw) + ch.scale)[s] : (static_cast<const uint32_t*>(a.sw) + ch.scale)[s];
+  return a.sw_f16 ? (static_cast<const uint16_t*>(a.sw) + ch.scale)[s]
+                  : (static_cast<const uint32_t*>(a.sw) + ch.scale)[s];
 }
 __device__ __forceinline__ float scale_of(const W4a16Args& a, uint32_t s) {
   return a.sw_f16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(s))) : float_of(s);
@@ -126,7 +129,8 @@ __device__ __forceinline__ void store_y(const W4a16Args& a, int parts, int part,
 // channels a workgroup has a compute unit to itself, and four tiles at a time take
 // the registers of two: 8 x 4096 -> 8192 8.2 us with two, 7.8 with four.)
 template <bool XF16, int NB, int GROUPS>
-__global__ void __launch_bounds__(kWaves * 64, NB == 4 && XF16 && GROUPS != HALVES ? 4 : 2) w4a16_few_kernel(W4a16Args a, int ntiles) {
+__global__ void __launch_bounds__(kWaves * 64, NB == 4 && XF16 && GROUPS != HALVES ? 4 : 2)
+    w4a16_few_kernel(W4a16Args a, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
   constexpr int XV = XF16 ? 1 : 2;                   // 16 bytes of x to eight elements
   constexpr int U = NB <= 2 && XF16 ? 4 : 2;         // tiles of each block of channels on their way together
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kWaves * 64, NB == 4 && XF16 && GROUPS != HALV
         for (int e = 0; e < XV; ++e) {
           const char* p = x + tt * (256 * XV) + j * (16 * XV) - (past ? 128 * XV : 0);
           xr[u][j][e] = reinterpret_cast<const u4*>(p)[e];
-          }
+        }
     }
     if constexpr (GROUPS != WHOLE) {
 #pragma unroll
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(kWaves * 64, NB == 4 && XF16 && GROUPS != HALV
 // again).  x goes through LDS as operands, a tile ahead, each thread bringing its
 // share; the waves' codes come from memory to registers a tile ahead too.
 template <bool XF16, int NB, int MT, int GROUPS>
-__global__ void __launch_bounds__(kManySides * kManyWaves * 64, 2) w4a16_many_kernel(W4a16Args a, Divisor parts, int share, int longer, int ntiles) {
+__global__ void __launch_bounds__(kManySides * kManyWaves * 64, 2)
+    w4a16_many_kernel(W4a16Args a, Divisor parts, int share, int longer, int ntiles) {
   constexpr int PARTS = XF16 ? 1 : 3, HALF = GROUPS == HALVES ? 2 : 1;
   constexpr int BUFFERS = XF16 ? 2 : 1;
   // A thread brings the operands (i, j) of MT * 4, lane its own, of its wave.
@@ -468,8 +473,8 @@ void launch_x(const W4a16Args& a, const W4a16Plan& p, hipStream_t st) {
 // / 9.6, 12288 12.3 / 11.7 / 9.8, 28672 25.4 / 20.2 / 18.5; float32 5 x 1024 ->
 // 5008 6.4 / 5.5 / 6.3.
 // More rows: parts of K until 256 workgroups share the work, one on each compute
-// unit, each a tile to a side at least.  64 x 14336 -> 4096 takes 20.1 us with 256
-// workgroups, 23.5 with 512 and 28.7 with 128 (of more parts the sums are written
+// unit, each a tile to a side at least.  64 x 14336 -> 4096 takes 18.5 us with 256
+// workgroups, 22.0 with 512 and 25.9 with 128 (of more parts the sums are written
 // and read again); 58 x 1472 -> 855 12.1 us, with four tiles to a side 19.8.
 W4a16Plan w4a16_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = (N + 15) / 16, tiles = (K + 127) / 128;
@@ -493,8 +498,9 @@ hipError_t launch_w4a16(const W4a16Args& a, bool x_f16, hipStream_t st) {
   x_f16 ? launch_x<true>(a, p, st) : launch_x<false>(a, p, st);
   if (p.parts > 1) {
     if (a.N % 4 == 0)
-      hipLaunchKernelGGL(w4a16_join_kernel<4>, dim3(static_cast<unsigned>((a.N + 1023) / 1024), static_cast<unsigned>(a.M)),
-                         dim3(256), 0, st, a, p.parts);
+      hipLaunchKernelGGL(w4a16_join_kernel<4>,
+                         dim3(static_cast<unsigned>((a.N + 1023) / 1024), static_cast<unsigned>(a.M)), dim3(256), 0, st,
+                         a, p.parts);
     else
       hipLaunchKernelGGL(w4a16_join_kernel<1>, dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>(a.M)),
                          dim3(256), 0, st, a, p.parts);
