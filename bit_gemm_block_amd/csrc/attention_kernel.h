@@ -26,11 +26,11 @@
 //
 // What bounds it.  Few rows: the cache's bytes.  64 sequences of 300 to 16384
 // tokens, 8 heads of 128 at 4 bits (527 MB, 101 us at a large copy's rate, 88 at
-// the rate at which a kernel can only read them) take 117 to 123 us, their join 5.
+// the rate at which a kernel can only read them) take 119 to 124 us, their join 5.
 // Many rows: instructions.  A step of a wave is 24 to 32 matrix instructions (384
 // to 512 cycles), about 150 others (700) and 20 KB of LDS, and they overlap
-// little: 3 prompts of up to 1021 queries take 80 us beside 15 of the join, 17 of
-// them in matrix instructions.
+// little: 3 prompts of up to 1021 queries take 84 to 93 us beside 16 of the join, 17
+// of them in matrix instructions.
 #pragma once
 
 #include <type_traits>
