@@ -103,6 +103,21 @@ def test_runs_of_every_length(group, dim, bits, dt):
         mixed(counts, lengths, 1, group, dim, bits, dt, 40, group, **kw)
 
 
+# A tile of rows that waves share, its sequences with none to three queries: joined
+# by the rows of q where there are fewer than three of each.
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[0, 3, 0, 1, 0], [3, 1, 0, 0, 2, 1, 1], [1, 0] * 40 + [3], [0] * 70 + [2, 3]])
+@pytest.mark.parametrize("group", [1, 4, 5])
+@pytest.mark.parametrize("width", [4, 130])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_drafts_of_several_lengths(counts, group, width, prefix):
+    print("attention drafts", len(counts), group, width, prefix, flush=True)
+    rng = np.random.default_rng(len(counts))
+    lengths = rng.integers(1, 60, len(counts))
+    lengths[[1, -1]] = 128 if width == 4 else 2900, 100
+    mixed(counts, lengths.tolist(), 2, group, 128, 4, "f32", width, group, spare=1, max_q=3, prefix=prefix)
+
+
 @pytest.mark.gpu
 def test_more_places_than_a_grid():
     # 1024 sequences of which one has 512 queries, of 32 heads: 2^24 places of rows,
